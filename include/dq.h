@@ -315,6 +315,77 @@ dq_status dq_orbit_linear(const dq_orbit* o, const void* x_dev, dq_dtype dt, dq_
  * `stream` first. */
 dq_status dq_orbit_act_export(const dq_orbit_act* a, uint8_t* codes_host, float* scale_host, void* stream);
 
+/* ---- few rows: the layer for a handful of tokens ---------------------------
+ * Conditioning vectors, single decoded tokens and small batches have no
+ * (T, H, W) grid and too few rows for the tiled GEMMs; their time is that of
+ * reading the 4-bit weight.  These entry points take the same dq_weights as
+ * dq_linear (an MX-FP4 weight with its low-rank factors) and apply
+ *     y_n = x_n Q4(R) + (x_n L1) L2
+ * to rows as they are (bf16 or fp32), or to rows in MX-FP8, as dq_rmsnorm8
+ * writes them.  Products are exact, sums (U = x L1 included, which is not
+ * rounded to bf16 here) are fp32 in a fixed order, and one rounding to y's
+ * type ends them: repeated calls agree bit for bit. */
+
+/* A weight that is already coded, in the layout dq_weights_export writes:
+ *   rcodes_host  [Co][Ci/2] FP4 codes;  rscales_host [Co][Ci/32] scale codes
+ *   l1_host [Ci][rank], l2_host [rank][Co] bf16 bits (may be NULL when rank == 0)
+ * for any entry point that takes a 4-bit weight.  R is what the codes stand
+ * for (dq_weights_export then decodes it).  Requirements on Ci, Co and rank
+ * as dq_prepare_weights_lowrank; DQ_ERR_INVALID_ARG for a scale code of 255.
+ * The arrays' sizes cannot be checked here.  Synchronous. */
+dq_status dq_import_weights(const uint8_t* rcodes_host, const uint8_t* rscales_host, int64_t Ci, int64_t Co,
+                            int32_t rank, const uint16_t* l1_host, const uint16_t* l2_host, int32_t device,
+                            dq_weights** out);
+
+/* Workspace for up to max_rows rows (1 <= max_rows <= 4096) of a 4-bit weight
+ * or of any other with the same Ci, Co and rank on its device.  Tuned for up
+ * to 64 rows; more are taken 64 at a time, each group reading the weight
+ * again.  Must not be used by two streams at once (two captured graphs that
+ * share one must not run at once either). */
+typedef struct dq_rows dq_rows;
+dq_status dq_rows_create(const dq_weights* w, int64_t max_rows, dq_rows** out);
+void dq_rows_destroy(dq_rows* a);
+
+/* y = x Q4(R) + (x L1) L2 for N rows (0 <= N <= max_rows; nothing is done for
+ * N == 0).
+ *   x_dev [N][Ci] of dtype dt, rows ldx elements apart (ldx >= Ci), 16-byte
+ *         aligned rows
+ *   y_dev [N][Co] of dtype ydt, rows ldy elements apart (ldy >= Co), every
+ *         element of the N rows written, nothing else; must not overlap x
+ * fp32 x is taken at its full precision.  Asynchronous on `stream`; allocates
+ * nothing and can be captured into a HIP graph. */
+dq_status dq_linear_rows(const dq_weights* w, const void* x_dev, dq_dtype dt, int64_t ldx, int64_t N, dq_rows* a,
+                         void* y_dev, dq_dtype ydt, int64_t ldy, void* stream);
+/* The same for rows in MX-FP8: codes_dev [N][Ci] E4M3, 8-byte aligned;
+ * scales_dev [N][Ci/32] E8M0 (255: the group's values are NaN). */
+dq_status dq_linear_rows8(const dq_weights* w, const uint8_t* codes_dev, const uint8_t* scales_dev, int64_t N, dq_rows* a,
+                          void* y_dev, dq_dtype ydt, int64_t ldy, void* stream);
+
+/* Root-mean-square norm of N rows of C channels with the residual's addition,
+ * written as MX-FP8 (the quantizer of the layers above), as plain values, or
+ * both:
+ *   h = x + r (fp32 sum, rounded to dt; h = x when res_dev is NULL)
+ *   f = fl32(1 / sqrt(sum_c h_c^2 / C + eps)), formed in fp64
+ *   v_c = fl32(fl32(h_c f) gain_c)
+ *   scale code e + 127 of the smallest e >= -127 with max|v| <= 448 2^e over
+ *   each 32 channels, or 64 (group = 64: stored at both 32-channel places);
+ *   codes v 2^-e in E4M3, nearest, ties to even
+ * Infinite and NaN elements of v get the E4M3 NaN code and do not enter the
+ * scale.  Reproducible bit for bit (the one sum is kept in fp64).
+ *   x_dev, res_dev (or NULL), h_dev (or NULL), y_dev (or NULL; v rounded to dt):
+ *         [N][C] of dtype dt, rows ld elements apart (ld >= C), 16-byte
+ *         aligned rows; h_dev and y_dev may be x_dev or res_dev themselves
+ *         (same stride), else they must not overlap them or each other
+ *   gain_dev [C] of dtype gain_dt, 16-byte aligned, or NULL for ones
+ *   codes_dev [N][C] 8-byte aligned and scales_dev [N][C/32], dense, or both NULL
+ * All on `device`.  Requires C a multiple of `group`, C <= 32768, eps in
+ * [1e-60, inf), 0 <= N <= 2^31 - 256 (nothing is done for N == 0), and codes
+ * or y_dev.  Asynchronous on `stream`; allocates nothing and can be captured
+ * into a HIP graph. */
+dq_status dq_rmsnorm8(const void* x_dev, int64_t ldx, const void* res_dev, int64_t ldr, dq_dtype dt, const void* gain_dev,
+                      dq_dtype gain_dt, double eps, int64_t N, int64_t C, int32_t group, void* h_dev, int64_t ldh,
+                      uint8_t* codes_dev, uint8_t* scales_dev, void* y_dev, int64_t ldy, int32_t device, void* stream);
+
 /* For callers that cannot allocate device memory (code under HIP graph
  * capture, tight serving loops, harnesses that forbid hipMalloc): dq_linear
  * for the geometry `geom` with MX-FP8 cores in groups of 32, without a

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <limits>
@@ -207,6 +208,33 @@ dq_status dq_lowrank_factors(const void* w_host, dq_dtype dt, int64_t Ci, int64_
 
 }  // extern "C"
 
+namespace dq {
+// A weight's bf16 factors: kept on the host for exports, and on the device
+// transposed and padded (zeros) as the kernels read them.
+dq_status upload_factors(dq_weights* w, const uint16_t* l1_host, const uint16_t* l2_host) {
+    const int64_t Ci = w->Ci, Co = w->Co;
+    const int rank = w->rank;
+    if (rank == 0) return DQ_OK;
+    hipError_t e;
+    try {
+        w->l1.assign(l1_host, l1_host + Ci * rank);
+        w->l2.assign(l2_host, l2_host + (int64_t)rank * Co);
+        std::vector<uint16_t> l1t((size_t)(w->rp * w->Kp), 0), l2t((size_t)(w->Cop * w->rp), 0);
+        for (int64_t c = 0; c < Ci; ++c)
+            for (int q = 0; q < rank; ++q) l1t[(size_t)(q * w->Kp + c)] = l1_host[c * rank + q];
+        for (int q = 0; q < rank; ++q)
+            for (int64_t j = 0; j < Co; ++j) l2t[(size_t)(j * w->rp + q)] = l2_host[(int64_t)q * Co + j];
+        if ((e = dalloc(&w->l1t, l1t.size(), &w->bytes)) != hipSuccess ||
+            (e = dalloc(&w->l2t, l2t.size(), &w->bytes)) != hipSuccess) return hip_fail(e, "hipMalloc factors");
+        if ((e = hipMemcpy(w->l1t, l1t.data(), l1t.size() * 2, hipMemcpyHostToDevice)) != hipSuccess ||
+            (e = hipMemcpy(w->l2t, l2t.data(), l2t.size() * 2, hipMemcpyHostToDevice)) != hipSuccess) return hip_fail(e, "copy factors");
+    } catch (const std::bad_alloc&) {
+        return fail(DQ_ERR_OUT_OF_MEMORY, "host allocation failed");
+    }
+    return DQ_OK;
+}
+}  // namespace dq
+
 // Weight preparation for a given code format of R (FMT_FP4, or the 6-bit
 // FMT_FP6 / FMT_BF6).
 static dq_status prepare_weights(const void* w_host, dq_dtype dt, int64_t Ci, int64_t Co, int32_t rank,
@@ -251,12 +279,6 @@ static dq_status prepare_weights(const void* w_host, dq_dtype dt, int64_t Ci, in
         (void)hipFree(l1d);
         (void)hipFree(l2d);
     };
-    try {
-        w->l1.assign(l1_host ? l1_host : (const uint16_t*)nullptr, l1_host ? l1_host + Ci * rank : nullptr);
-        w->l2.assign(l2_host ? l2_host : (const uint16_t*)nullptr, l2_host ? l2_host + (int64_t)rank * Co : nullptr);
-    } catch (const std::bad_alloc&) {
-        return fail(DQ_ERR_OUT_OF_MEMORY, "host allocation failed");
-    }
     if ((e = hipMalloc(&wdev, (size_t)(Ci * Co) * esz)) != hipSuccess) { cleanup(); return hip_fail(e, "hipMalloc W"); }
     if ((e = hipMemcpy(wdev, w_host, (size_t)(Ci * Co) * esz, hipMemcpyHostToDevice)) != hipSuccess) { cleanup(); return hip_fail(e, "copy W"); }
     if (rank > 0) {
@@ -272,17 +294,7 @@ static dq_status prepare_weights(const void* w_host, dq_dtype dt, int64_t Ci, in
     e = six ? launch_encode_fp6(w->r, 0, Co, Ci, Ci, w->Kp, w->rq, w->rs, wfmt == 3, nullptr)
             : launch_encode_fp4_rows(w->r, Co, Ci, Ci, w->Kp, w->rq, w->rs, nullptr);
     if (e != hipSuccess) { cleanup(); return hip_fail(e, "encode kernel"); }
-    if (w->rp > 0) {
-        std::vector<uint16_t> l1t((size_t)(w->rp * w->Kp), 0), l2t((size_t)(w->Cop * w->rp), 0);
-        for (int64_t c = 0; c < Ci; ++c)
-            for (int q = 0; q < rank; ++q) l1t[(size_t)(q * w->Kp + c)] = l1_host[c * rank + q];
-        for (int q = 0; q < rank; ++q)
-            for (int64_t j = 0; j < Co; ++j) l2t[(size_t)(j * w->rp + q)] = l2_host[(int64_t)q * Co + j];
-        if ((e = dalloc(&w->l1t, l1t.size(), &w->bytes)) != hipSuccess ||
-            (e = dalloc(&w->l2t, l2t.size(), &w->bytes)) != hipSuccess) { cleanup(); return hip_fail(e, "hipMalloc factors"); }
-        if ((e = hipMemcpy(w->l1t, l1t.data(), l1t.size() * 2, hipMemcpyHostToDevice)) != hipSuccess ||
-            (e = hipMemcpy(w->l2t, l2t.data(), l2t.size() * 2, hipMemcpyHostToDevice)) != hipSuccess) { cleanup(); return hip_fail(e, "copy factors"); }
-    }
+    if ((st = upload_factors(w, l1_host, l2_host)) != DQ_OK) { cleanup(); return st; }
     if ((e = hipDeviceSynchronize()) != hipSuccess) { cleanup(); return hip_fail(e, "weight preparation"); }
     cleanup();
     *out = guard.release();
@@ -346,10 +358,25 @@ dq_status dq_weights_export(const dq_weights* w, uint16_t* l1_host, uint16_t* l2
     if (l1_host && w->rank) std::memcpy(l1_host, w->l1.data(), w->l1.size() * 2);
     if (l2_host && w->rank) std::memcpy(l2_host, w->l2.data(), w->l2.size() * 2);
     hipError_t e;
-    if (r_host && (e = hipMemcpy(r_host, w->r, (size_t)(w->Ci * w->Co) * 4, hipMemcpyDeviceToHost)) != hipSuccess)
+    if (r_host && w->r && (e = hipMemcpy(r_host, w->r, (size_t)(w->Ci * w->Co) * 4, hipMemcpyDeviceToHost)) != hipSuccess)
         return hip_fail(e, "copy R");
     try {
         std::vector<uint8_t> buf;
+        if (r_host && !w->r) {                       // an imported weight: R is what its codes stand for
+            static const float mag[8] = {0.0f, 0.5f, 1.0f, 1.5f, 2.0f, 3.0f, 4.0f, 6.0f};
+            std::vector<uint8_t> sb, codes((size_t)(w->Ci / 2)), scales((size_t)(w->Ci / 32));
+            if ((e = fetch_all(w->rq, (size_t)(w->Cop * w->Kp / 2), buf)) != hipSuccess ||
+                (e = fetch_all(w->rs, (size_t)(w->Cop * w->Kp / 32), sb)) != hipSuccess) return hip_fail(e, "copy R codes");
+            for (int64_t j = 0; j < w->Co; ++j) {
+                unstep_fp4(buf, j, w->Ci, w->Kp, codes.data());
+                unstep_scales(sb, j, w->Ci, w->Kp, scales.data());
+                for (int64_t c = 0; c < w->Ci; ++c) {
+                    const int code = codes[(size_t)(c / 2)] >> (c % 2 * 4) & 15;
+                    const float v = std::ldexp(mag[code & 7], scales[(size_t)(c / 32)] - 127);
+                    r_host[j * w->Ci + c] = code & 8 ? -v : v;
+                }
+            }
+        }
         if (rcodes_host && w->wfmt != 4) {
             if ((e = fetch_all(w->rq, (size_t)(w->Cop * w->Kp / 4 * 3), buf)) != hipSuccess) return hip_fail(e, "copy R codes");
             for (int64_t j = 0; j < w->Co; ++j) unstep_fp6(buf, j, w->Ci, w->Kp, rcodes_host + j * (w->Ci / 4 * 3));

@@ -146,7 +146,7 @@ struct dq_weights {
     int wfmt = 4;              // R's codes: MX-FP4 (4), or MX-FP6 E2M3 (2) / E3M2 (3) for the 6-bit layers
     uint8_t* rq = nullptr;     // Cop x Kp/2    Q4(R) codes (Cop x 3 Kp/4 for Q6(R)), step-major (device)
     uint8_t* rs = nullptr;     // Cop x Kp/32   Q4(R) scale codes, step-major (device)
-    float* r = nullptr;        // [Co][Ci]      fp32 residual R^T (device, for export)
+    float* r = nullptr;        // [Co][Ci]      fp32 residual R^T (device, for export; null for an imported weight)
     uint16_t* l1t = nullptr;   // [rp][Kp]      L1^T bf16 (device)
     uint16_t* l2t = nullptr;   // [Cop][rp]     L2^T bf16 (device)
     std::vector<uint16_t> l1, l2;   // host copies [Ci][rank], [rank][Co]
@@ -228,6 +228,11 @@ dq_status hip_fail(hipError_t e, const char* what);
 // segment has cubes of more than 64 tokens).
 dq_status plan_qact(const dq_weights* w, const dq_geom& geom, int core_group, int core_bits, dq_qact* q,
                     int64_t* max_partials);
+
+// Stores a weight's bf16 factors (host copies and padded device transposes).
+dq_status upload_factors(dq_weights* w, const uint16_t* l1_host, const uint16_t* l2_host);
+// DQ_OK for the index of a gfx950 device (asked of the runtime once per device; norm.hip).
+dq_status known_device(int device);
 
 // Makes a handle's device current for the scope and restores the caller's.
 struct DeviceGuard {

@@ -1,0 +1,302 @@
+// dq_rmsnorm8: residual addition, root-mean-square norm and MX-FP8 encoding
+// of token rows in one pass.
+//
+//   h = x + r, rounded to the stream's type;  s = sum_c h_c^2 in fp64
+//   f = fl32(1 / sqrt(s / C + eps)), formed in fp64 and rounded once
+//   v_c = fl32(fl32(h_c f) g_c);  MX-FP8 of v per 32 (or 64) channels
+//
+// The sum of squares is kept in fp64 so that f does not depend on the order
+// of the sum: every later step is one fp32 rounding per element, so codes and
+// scales are reproducible bit for bit by any implementation (an element next
+// to the border of two codes goes by the last bit of f).
+#include <hip/hip_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstring>
+
+#include "dq.h"
+#include "dq_device.h"
+#include "dq_internal.h"
+
+namespace dq {
+namespace {
+
+constexpr int MAX_NORM_C = 32768;
+
+struct NormArgs {
+    const void* x;
+    const void* r;      // residual or null
+    const void* g;      // gain or null (ones)
+    void* h;            // x + r, or null
+    void* y;            // v in the stream's type, or null
+    uint8_t* codes;     // or null
+    uint8_t* scales;
+    long long N, ldx, ldr, ldh, ldy;
+    int C, wide;        // wide: one scale for 64 channels
+    int g_bf16;
+    double eps;
+};
+
+template <class T> struct Stream;
+template <> struct Stream<uint16_t> {
+    static __device__ __forceinline__ void load(const uint16_t* p, float* v) {
+        const uint4 d = *(const uint4*)p;
+        const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ float round(float v) { return (float)(__bf16)v; }
+    static __device__ __forceinline__ void store(uint16_t* p, const float* v) {
+        v8bf b;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = (__bf16)v[i];
+        *(uint4*)p = __builtin_bit_cast(uint4, b);
+    }
+};
+template <> struct Stream<float> {
+    static __device__ __forceinline__ void load(const float* p, float* v) {
+        const float4 a = ((const float4*)p)[0], b = ((const float4*)p)[1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+    static __device__ __forceinline__ float round(float v) { return v; }
+    static __device__ __forceinline__ void store(float* p, const float* v) {
+        ((float4*)p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        ((float4*)p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+};
+
+// Codes of 8 consecutive values; `a` is the group's largest finite magnitude.
+__device__ __forceinline__ uint2 encode8(const float* v, float scale) {
+    uint2 d;
+    v2s z = {0, 0};
+    v2s a = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(z, v[0], v[1], scale, false);
+    a = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(a, v[2], v[3], scale, true);
+    v2s b = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(z, v[4], v[5], scale, false);
+    b = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(b, v[6], v[7], scale, true);
+    d.x = __builtin_bit_cast(uint32_t, a);
+    d.y = __builtin_bit_cast(uint32_t, b);
+    return d;
+}
+
+// A row is held in registers by TPR threads, CH chunks of 8 channels each
+// (chunk i of thread t: channels 8 (i TPR + t) ..), so it is read once; a
+// group of 32 channels is 4 neighbouring lanes' chunk.
+template <class T, int TPR, int CH>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm8(NormArgs a) {
+    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+    constexpr int WPR = TPR / 64;
+    const int t = threadIdx.x % TPR;
+    const long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
+    const bool live = row < a.N;
+    const int nch = a.C >> 3;
+    float h[CH][8];
+    double s = 0.0;
+    if (live) {
+        const T* xp = (const T*)a.x + row * a.ldx;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int c = i * TPR + t;
+            if (c < nch) {
+                Stream<T>::load(xp + 8 * c, h[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) h[i][j] = 0.0f;
+            }
+        }
+        if (a.r) {
+            const T* rp = (const T*)a.r + row * a.ldr;
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const int c = i * TPR + t;
+                if (c < nch) {
+                    float r[8];
+                    Stream<T>::load(rp + 8 * c, r);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) h[i][j] = Stream<T>::round(h[i][j] + r[j]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s = __builtin_fma((double)h[i][j], (double)h[i][j], s);
+    }
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m, 64);
+    if constexpr (WPR > 1) {
+        __shared__ double part[RPB * WPR];
+        const int w = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) part[w] = s;
+        __syncthreads();
+        s = 0.0;
+#pragma unroll
+        for (int i = 0; i < WPR; ++i) s += part[(w / WPR) * WPR + i];
+    }
+    if (!live) return;
+    const float f = (float)(1.0 / sqrt(s / (double)a.C + a.eps));
+    if (a.h) {
+        T* hp = (T*)a.h + row * a.ldh;
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+            if (i * TPR + t < nch) Stream<T>::store(hp + 8 * (i * TPR + t), h[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int c = i * TPR + t;
+        if (c >= nch) continue;                     // (whole groups: C % 32 == 0, or % 64 with wide scales)
+        float g[8];
+        if (!a.g) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[j] = 1.0f;
+        } else if (a.g_bf16) {
+            Stream<uint16_t>::load((const uint16_t*)a.g + 8 * c, g);
+        } else {
+            Stream<float>::load((const float*)a.g + 8 * c, g);
+        }
+        float v[8];
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] = (h[i][j] * f) * g[j];
+            top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);   // (magnitudes order like their bits)
+        }
+        if (a.y) Stream<T>::store((T*)a.y + row * a.ldy + 8 * c, v);
+        if (!a.codes) continue;
+        uint32_t bad = 0;                           // infinite or NaN elements: the NaN code, not part of the scale
+        if (top >= 0x7f800000u) {
+            top = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t m = __float_as_uint(v[j]) & 0x7fffffffu;
+                if (m >= 0x7f800000u) {
+                    bad |= 1u << j;
+                    v[j] = 0.0f;
+                } else {
+                    top = max(top, m);
+                }
+            }
+        }
+        top = max(top, (uint32_t)__shfl_xor((int)top, 1, 64));
+        top = max(top, (uint32_t)__shfl_xor((int)top, 2, 64));
+        if (a.wide) top = max(top, (uint32_t)__shfl_xor((int)top, 4, 64));
+        const int e = mx_exp_fp8(__uint_as_float(top));
+        uint2 d = encode8(v, pow2f(e));
+        if (bad) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (bad >> j & 1) d.x |= 0x7fu << (8 * j);
+                if (bad >> (j + 4) & 1) d.y |= 0x7fu << (8 * j);
+            }
+        }
+        *(uint2*)(a.codes + row * a.C + 8 * c) = d;
+        if ((t & 3) == 0) a.scales[row * (a.C >> 5) + (c >> 2)] = (uint8_t)(e + 127);
+    }
+}
+
+template <class T, int TPR>
+void launch_norm(const NormArgs& a, hipStream_t st) {
+    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+    const unsigned grid = (unsigned)((a.N + RPB - 1) / RPB);
+    const int threads = TPR < 256 ? 256 : TPR;
+    switch ((a.C / 8 + TPR - 1) / TPR) {
+        case 1: k_rmsnorm8<T, TPR, 1><<<grid, threads, 0, st>>>(a); break;
+        case 2: k_rmsnorm8<T, TPR, 2><<<grid, threads, 0, st>>>(a); break;
+        case 3: k_rmsnorm8<T, TPR, 3><<<grid, threads, 0, st>>>(a); break;
+        default: k_rmsnorm8<T, TPR, 4><<<grid, threads, 0, st>>>(a); break;
+    }
+}
+
+template <class T>
+hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
+    if (a.C <= 2048) launch_norm<T, 64>(a, st);
+    else if (a.C <= 8192) launch_norm<T, 256>(a, st);
+    else launch_norm<T, 1024>(a, st);
+    return hipGetLastError();
+}
+
+// Whether rows of `cols` elements at p (stride ldp) and at q (stride ldq) may
+// share memory in a way other than being the same array: unequal strides in
+// overlapping ranges, or equal strides with overlapping columns.
+bool clashes(const void* p, int64_t ldp, const void* q, int64_t ldq, int64_t n, int64_t cols, int64_t esz) {
+    if (!p || !q || (p == q && ldp == ldq)) return false;
+    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+    const uintptr_t ea = a + (uintptr_t)(((n - 1) * ldp + cols) * esz), eb = b + (uintptr_t)(((n - 1) * ldq + cols) * esz);
+    if (ea <= b || eb <= a) return false;
+    if (ldp != ldq) return true;
+    const uint64_t pitch = (uint64_t)(ldp * esz), d = (a > b ? a - b : b - a) % pitch;
+    return d < (uint64_t)(cols * esz) || pitch - d < (uint64_t)(cols * esz);
+}
+
+}  // namespace
+
+// gfx950 check of a device index, asked of the runtime once per device.
+dq_status known_device(int device) {
+    static std::atomic<uint64_t> known{0};
+    if (device >= 0 && device < 64 && (known.load(std::memory_order_relaxed) >> device & 1)) return DQ_OK;
+    int n = 0;
+    if (hipGetDeviceCount(&n) != hipSuccess || n <= 0) return fail(DQ_ERR_DEVICE, "no HIP device available");
+    if (device < 0 || device >= n) return fail(DQ_ERR_INVALID_ARG, "device index out of range");
+    hipDeviceProp_t prop;
+    if (hipGetDeviceProperties(&prop, device) != hipSuccess) return fail(DQ_ERR_DEVICE, "hipGetDeviceProperties failed");
+    if (std::strncmp(prop.gcnArchName, "gfx950", 6) != 0)
+        return fail(DQ_ERR_UNSUPPORTED, std::string("device is ") + prop.gcnArchName + ", gfx950 required");
+    if (device < 64) known.fetch_or(uint64_t(1) << device, std::memory_order_relaxed);
+    return DQ_OK;
+}
+
+}  // namespace dq
+
+using namespace dq;
+
+extern "C" dq_status dq_rmsnorm8(const void* x_dev, int64_t ldx, const void* res_dev, int64_t ldr, dq_dtype dt,
+                                 const void* gain_dev, dq_dtype gain_dt, double eps, int64_t N, int64_t C, int32_t group,
+                                 void* h_dev, int64_t ldh, uint8_t* codes_dev, uint8_t* scales_dev, void* y_dev,
+                                 int64_t ldy, int32_t device, void* stream) {
+    set_error("");
+    if (dt != DQ_F32 && dt != DQ_BF16) return fail(DQ_ERR_INVALID_ARG, "unknown dtype");
+    if (gain_dev && gain_dt != DQ_F32 && gain_dt != DQ_BF16) return fail(DQ_ERR_INVALID_ARG, "unknown gain dtype");
+    if (group != 32 && group != 64) return fail(DQ_ERR_INVALID_ARG, "group must be 32 or 64");
+    if (!(eps > 0.0) || !std::isfinite(eps) || eps < 1e-60) return fail(DQ_ERR_INVALID_ARG, "eps must be finite and at least 1e-60");
+    if (C < 32 || C % 32 != 0 || C > MAX_NORM_C) return fail(DQ_ERR_SHAPE, "C must be a multiple of 32 in [32, 32768]");
+    if (C % group != 0) return fail(DQ_ERR_SHAPE, "group must divide C");
+    if (N < 0 || N > (int64_t(1) << 31) - 256) return fail(DQ_ERR_SHAPE, "N must be in [0, 2^31 - 256]");
+    if ((codes_dev == nullptr) != (scales_dev == nullptr)) return fail(DQ_ERR_INVALID_ARG, "codes and scales come together");
+    if (N == 0) return DQ_OK;
+    if (!x_dev) return fail(DQ_ERR_INVALID_ARG, "x_dev is NULL");
+    if (!codes_dev && !y_dev) return fail(DQ_ERR_INVALID_ARG, "no output: give codes and scales, or y");
+    if (h_dev && !res_dev) return fail(DQ_ERR_INVALID_ARG, "h_dev without a residual");
+    const int64_t esz = dt == DQ_BF16 ? 2 : 4, lim = int64_t(1) << 40;
+    const struct { const void* p; int64_t ld; const char* name; } rows[] = {
+        {x_dev, ldx, "x_dev"}, {res_dev, ldr, "res_dev"}, {h_dev, ldh, "h_dev"}, {y_dev, ldy, "y_dev"}};
+    for (const auto& b : rows) {
+        if (!b.p) continue;
+        if ((uintptr_t)b.p % 16 != 0) return fail(DQ_ERR_INVALID_ARG, std::string(b.name) + " must be 16-byte aligned");
+        if (b.ld < C || b.ld > lim / N || b.ld * esz % 16 != 0)
+            return fail(DQ_ERR_SHAPE, std::string(b.name) + ": the row stride must be at least C and a multiple of 16 bytes");
+    }
+    if ((uintptr_t)gain_dev % 16 != 0) return fail(DQ_ERR_INVALID_ARG, "gain_dev must be 16-byte aligned");
+    if ((uintptr_t)codes_dev % 8 != 0) return fail(DQ_ERR_INVALID_ARG, "codes_dev must be 8-byte aligned");
+    // (a thread reads its elements of x and the residual before it writes the
+    // same elements, so an output may be one of the inputs, but not overlap it
+    // in another way; outputs may not overlap each other at all)
+    for (const auto& o : {rows[2], rows[3]})
+        for (const auto& i : {rows[0], rows[1]})
+            if (clashes(o.p, o.ld, i.p, i.ld, N, C, esz))
+                return fail(DQ_ERR_INVALID_ARG, std::string(o.name) + " overlaps " + i.name + " without being the same array");
+    if (h_dev && y_dev && (h_dev == y_dev || clashes(h_dev, ldh, y_dev, ldy, N, C, esz)))
+        return fail(DQ_ERR_INVALID_ARG, "h_dev and y_dev overlap");
+    const dq_status st = known_device(device);
+    if (st != DQ_OK) return st;
+    DeviceGuard dg(device);
+    if (!dg.ok) return fail(DQ_ERR_DEVICE, "hipSetDevice failed");
+    const NormArgs a{x_dev, res_dev, gain_dev, h_dev, y_dev, codes_dev, scales_dev, (long long)N, (long long)ldx,
+                     (long long)ldr, (long long)ldh, (long long)ldy, (int)C, group == 64, gain_dt == DQ_BF16, eps};
+    const hipError_t e = dt == DQ_BF16 ? launch_norm<uint16_t>(a, (hipStream_t)stream) : launch_norm<float>(a, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "norm launch");
+    return DQ_OK;
+}

@@ -29,7 +29,8 @@ EXPORTS = ("dq_last_error", "dq_status_str", "dq_lowrank_factors", "dq_prepare_w
            "dq_prepare_weights_w6", "dq_act6_create", "dq_act6_destroy", "dq_quantize_act6", "dq_linear6_forward",
            "dq_linear6", "dq_act6_export", "dq_orbit_prepare", "dq_orbit_destroy", "dq_orbit_export",
            "dq_orbit_act_create", "dq_orbit_act_destroy", "dq_orbit_quantize_act", "dq_orbit_forward", "dq_orbit_linear",
-           "dq_orbit_act_export")
+           "dq_orbit_act_export", "dq_import_weights", "dq_rows_create", "dq_rows_destroy", "dq_linear_rows",
+           "dq_linear_rows8", "dq_rmsnorm8")
 DQ_FP6_E2M3, DQ_FP6_E3M2 = 2, 3
 FP6_FORMATS = {"fp6_e2m3": DQ_FP6_E2M3, "fp6_e3m2": DQ_FP6_E3M2}
 
@@ -97,6 +98,13 @@ def load():
         "dq_orbit_forward": ([P, P, P, P], ctypes.c_int),
         "dq_orbit_linear": ([P, P, ctypes.c_int, P, P, P], ctypes.c_int),
         "dq_orbit_act_export": ([P, P, P, P], ctypes.c_int),
+        "dq_import_weights": ([P, P, I64, I64, I32, P, P, I32, PP], ctypes.c_int),
+        "dq_rows_create": ([P, I64, PP], ctypes.c_int),
+        "dq_rows_destroy": ([P], None),
+        "dq_linear_rows": ([P, P, ctypes.c_int, I64, I64, P, P, ctypes.c_int, I64, P], ctypes.c_int),
+        "dq_linear_rows8": ([P, P, P, I64, P, P, ctypes.c_int, I64, P], ctypes.c_int),
+        "dq_rmsnorm8": ([P, I64, P, I64, ctypes.c_int, P, ctypes.c_int, ctypes.c_double, I64, I64, I32, P, I64, P, P, P, I64,
+                         I32, P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -503,5 +511,146 @@ def dq_orbit_linear(o: Orbit, x, a: OrbitAct, y, stream=None):
 def dq_orbit_act_export(a: OrbitAct, stream=None) -> dict:
     out = dict(codes=np.zeros((a.N, a.weights.Ci // 2), np.uint8), scale=np.zeros(a.N, np.float32))
     _check(load().dq_orbit_act_export(a.handle, _ptr(out["codes"]), _ptr(out["scale"]), _stream(stream)),
-           "dq_orbit_act_export")
+           "dq_orbit_act_export", "dq_import_weights", "dq_rows_create", "dq_rows_destroy", "dq_linear_rows",
+           "dq_linear_rows8", "dq_rmsnorm8")
     return out
+
+
+# ------------------------------------------------------------------- few rows ----
+class Rows:
+    """Owns a dq_rows handle (keeps its weights alive)."""
+
+    def __init__(self, handle: ctypes.c_void_p, weights: Weights, max_rows: int):
+        self.handle = handle
+        self.weights = weights
+        self.max_rows = max_rows
+
+    def __del__(self):
+        if getattr(self, "handle", None) and _LIB is not None:
+            _LIB.dq_rows_destroy(self.handle)
+            self.handle = None
+
+
+def _row_tensor(func: str, name: str, t, shape, dtypes, device: int, align: int, strided: bool = True):
+    """Like _device_tensor, for a matrix whose rows may be strided (unit stride
+    inside a row); returns the row stride in elements."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        _invalid(func, f"{name} must be a torch tensor")
+    if t.dtype not in dtypes:
+        _invalid(func, f"{name} has dtype {t.dtype}; expected one of {[str(d) for d in dtypes]}")
+    if t.shape != shape:
+        _invalid(func, f"{name} has shape {tuple(t.shape)}; expected {tuple(shape)}")
+    n, c = shape
+    ld, one = t.stride()
+    if n <= 1:
+        ld = c                                          # (the stride of a single row means nothing)
+    if one != 1 and c > 1 or ld < c:
+        _invalid(func, f"{name} must have contiguous, non-overlapping rows")
+    if not strided and ld != c:
+        _invalid(func, f"{name} must be contiguous")
+    if not t.is_cuda or t.get_device() != device:
+        _invalid(func, f"{name} is on {t.device}; expected cuda:{device}")
+    if (t.data_ptr() | (ld * t.element_size() if n > 1 else 0)) % align:
+        _invalid(func, f"{name} must have {align}-byte aligned rows")
+    return ld
+
+
+def _stream_on(stream, device: int) -> int:
+    """The given stream, or the current one of `device`."""
+    if stream is None:
+        import torch
+        stream = torch.cuda.current_stream(device)
+    return getattr(stream, "cuda_stream", stream)
+
+
+def _mx8_tensors(func: str, codes, scales, n: int, c: int, device: int):
+    """Row-major E4M3 codes [n][c] and E8M0 scales [n][c/32], as bytes or in torch's 8-bit float types."""
+    import torch
+    _row_tensor(func, "codes", codes, (n, c), (torch.float8_e4m3fn, torch.uint8), device, 8, strided=False)
+    _row_tensor(func, "scales", scales, (n, c // 32), (torch.float8_e8m0fnu, torch.uint8), device, 1, strided=False)
+
+
+def dq_import_weights(rcodes, rscales, l1: Optional[np.ndarray], l2: Optional[np.ndarray], device: int = 0) -> Weights:
+    """A weight already coded, as dq_weights_export returns it: rcodes uint8
+    [Co][Ci/2], rscales uint8 [Co][Ci/32], and the factors' bf16 bits (or
+    neither)."""
+    f = "dq_import_weights"
+    rc, rs = np.ascontiguousarray(rcodes), np.ascontiguousarray(rscales)
+    if rc.dtype != np.uint8 or rs.dtype != np.uint8 or rc.ndim != 2 or rs.ndim != 2:
+        _invalid(f, "rcodes and rscales must be 2-D uint8 arrays")
+    Co, Ci = rc.shape[0], rc.shape[1] * 2
+    if rs.shape != (Co, Ci // 32) or Ci % 32:
+        _invalid(f, f"rscales has shape {rs.shape}; expected {(Co, Ci // 32)}, Ci a multiple of 32")
+    if (l1 is None) != (l2 is None):
+        _invalid(f, "give both factors or neither")
+    rank = 0 if l1 is None else np.asarray(l1).shape[-1]
+    if l1 is not None and np.asarray(l1).ndim != 2:
+        _invalid(f, "l1 must be 2-D [Ci][rank]")
+    l1c = None if l1 is None else _factor(f, "l1", l1, (Ci, rank))
+    l2c = None if l2 is None else _factor(f, "l2", l2, (rank, Co))
+    h = ctypes.c_void_p()
+    _check(load().dq_import_weights(_ptr(rc), _ptr(rs), Ci, Co, rank, _ptr(l1c), _ptr(l2c), device, ctypes.byref(h)), f)
+    return Weights(h)
+
+
+def dq_rows_create(w: Weights, max_rows: int) -> Rows:
+    """Workspace for products of up to `max_rows` rows with `w` (or a weight of the same sizes)."""
+    h = ctypes.c_void_p()
+    _check(load().dq_rows_create(w.handle, max_rows, ctypes.byref(h)), "dq_rows_create")
+    return Rows(h, w, max_rows)
+
+
+def dq_linear_rows(w: Weights, x, a: Rows, y, stream=None):
+    """y [N][Co] (fp32 or bf16) = x Q4(R) + (x L1) L2 for x [N][Ci] in bf16 or
+    fp32; rows of either may be strided."""
+    import torch
+    f = "dq_linear_rows"
+    _check_pair(f, w, a)
+    types = (torch.bfloat16, torch.float32)
+    n = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 2 else 0
+    ldx = _row_tensor(f, "x", x, (n, w.Ci), types, w.device, 16)
+    ldy = _row_tensor(f, "y", y, (n, w.Co), types, w.device, 1)
+    _check(load().dq_linear_rows(w.handle, x.data_ptr(), _dtype_of(x), ldx, n, a.handle, y.data_ptr(), _dtype_of(y), ldy,
+                                 _stream_on(stream, w.device)), f)
+
+
+def dq_linear_rows8(w: Weights, codes, scales, a: Rows, y, stream=None):
+    """dq_linear_rows for rows in MX-FP8: codes [N][Ci] and scales [N][Ci/32]
+    as dq_rmsnorm8 writes them."""
+    import torch
+    f = "dq_linear_rows8"
+    _check_pair(f, w, a)
+    n = codes.shape[0] if isinstance(codes, torch.Tensor) and codes.dim() == 2 else 0
+    _mx8_tensors(f, codes, scales, n, w.Ci, w.device)
+    ldy = _row_tensor(f, "y", y, (n, w.Co), (torch.bfloat16, torch.float32), w.device, 1)
+    _check(load().dq_linear_rows8(w.handle, codes.data_ptr(), scales.data_ptr(), n, a.handle, y.data_ptr(), _dtype_of(y), ldy,
+                                  _stream_on(stream, w.device)), f)
+
+
+def dq_rmsnorm8(x, gain, eps: float, codes=None, scales=None, residual=None, h=None, y=None, group: int = 32, stream=None):
+    """RMS norm of x + residual as MX-FP8 codes [N][C] and scales [N][C/32], as
+    plain values y, or both; h receives x + residual (it, or y, may be x or
+    residual itself).  gain [C] in bf16 or fp32, or None."""
+    import torch
+    f = "dq_rmsnorm8"
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or not x.is_cuda:
+        _invalid(f, "x must be a 2-D torch tensor on a GPU")
+    n, c = x.shape
+    dev = x.get_device()
+    types = (torch.bfloat16, torch.float32)
+    ldx = _row_tensor(f, "x", x, (n, c), types, dev, 16)
+    same = (x.dtype,)
+    ldr, ldh, ldy = (0 if t is None else _row_tensor(f, name, t, (n, c), same, dev, 16)
+                     for name, t in (("residual", residual), ("h", h), ("y", y)))
+    if (codes is None) != (scales is None):
+        _invalid(f, "give both codes and scales or neither")
+    if codes is not None:
+        _mx8_tensors(f, codes, scales, n, c, dev)
+    gdt = DQ_F32
+    if gain is not None:
+        _device_tensor(f, "gain", gain, (c,), types, dev, 16)
+        gdt = _dtype_of(gain)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    _check(load().dq_rmsnorm8(ptr(x), ldx, ptr(residual), ldr, _dtype_of(x), ptr(gain), gdt, eps, n, c, group, ptr(h), ldh,
+                              ptr(codes), ptr(scales), ptr(y), ldy, dev, _stream_on(stream, dev)), f)
