@@ -338,7 +338,8 @@ dq_status dq_import_weights(const uint8_t* rcodes_host, const uint8_t* rscales_h
                             dq_weights** out);
 
 /* Workspace for up to max_rows rows (1 <= max_rows <= 4096) of a 4-bit weight
- * or of any other with the same Ci, Co and rank on its device.  Tuned for up
+ * with Ci <= 65536, or of any other with the same Ci, Co and rank on its
+ * device.  Tuned for up
  * to 64 rows; more are taken 64 at a time, each group reading the weight
  * again.  Must not be used by two streams at once (two captured graphs that
  * share one must not run at once either). */

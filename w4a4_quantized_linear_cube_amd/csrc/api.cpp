@@ -73,6 +73,7 @@ void free_weights(dq_weights* w) {
     (void)hipFree(w->r);
     (void)hipFree(w->l1t);
     (void)hipFree(w->l2t);
+    (void)hipFree(w->l1p);
     delete w;
 }
 
@@ -228,6 +229,16 @@ dq_status upload_factors(dq_weights* w, const uint16_t* l1_host, const uint16_t*
             (e = dalloc(&w->l2t, l2t.size(), &w->bytes)) != hipSuccess) return hip_fail(e, "hipMalloc factors");
         if ((e = hipMemcpy(w->l1t, l1t.data(), l1t.size() * 2, hipMemcpyHostToDevice)) != hipSuccess ||
             (e = hipMemcpy(w->l2t, l2t.data(), l2t.size() * 2, hipMemcpyHostToDevice)) != hipSuccess) return hip_fail(e, "copy factors");
+        if (w->wfmt == 4) {
+            std::vector<uint16_t> l1p(l1t.size(), 0);
+            for (int64_t c = 0; c < Ci; ++c)
+                for (int q = 0; q < rank; ++q) {
+                    const int64_t piece = ((c / 128 * (w->rp / 16) + q / 16) * 4 + c % 32 / 8) * 64 + c % 128 / 32 * 16 + q % 16;
+                    l1p[(size_t)(piece * 8 + c % 8)] = l1_host[c * rank + q];
+                }
+            if ((e = dalloc(&w->l1p, l1p.size(), &w->bytes)) != hipSuccess) return hip_fail(e, "hipMalloc factors");
+            if ((e = hipMemcpy(w->l1p, l1p.data(), l1p.size() * 2, hipMemcpyHostToDevice)) != hipSuccess) return hip_fail(e, "copy factors");
+        }
     } catch (const std::bad_alloc&) {
         return fail(DQ_ERR_OUT_OF_MEMORY, "host allocation failed");
     }

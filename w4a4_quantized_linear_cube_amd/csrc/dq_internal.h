@@ -149,6 +149,8 @@ struct dq_weights {
     float* r = nullptr;        // [Co][Ci]      fp32 residual R^T (device, for export; null for an imported weight)
     uint16_t* l1t = nullptr;   // [rp][Kp]      L1^T bf16 (device)
     uint16_t* l2t = nullptr;   // [Cop][rp]     L2^T bf16 (device)
+    uint16_t* l1p = nullptr;   // L1^T in the order of 16x16x32 matrix operands (4-bit weights, device):
+                               // [Kp/128][rp/16][f][lane][8], lane l: rank l % 16, channels 32 (l / 16) + 8 f .. + 7
     std::vector<uint16_t> l1, l2;   // host copies [Ci][rank], [rank][Co]
     size_t bytes = 0;
 };

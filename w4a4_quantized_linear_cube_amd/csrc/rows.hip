@@ -14,260 +14,590 @@
 #include <cstring>
 #include <memory>
 #include <new>
+#include <type_traits>
 
 #include "dq.h"
 #include "dq_device.h"
 #include "dq_internal.h"
 
-// Workspace of the few-row products: the rows as bf16 matrix operands, and U.
+// Workspace of the few-row products: where workgroups that share a tile meet.
 struct dq_rows {
-    int device = 0, cus = 256;
+    int device = 0;
     int64_t max_rows = 0, Ci = 0, Co = 0, Kp = 0;
     int rp = 0;
-    uint16_t* xp = nullptr;    // operand pieces of 16 rows: [row / 16][Kp / 128][part][4][64 lanes][8]
-    float* u = nullptr;        // [round_up(max_rows, 64)][rp]
+    float* sums = nullptr;     // the K slices' sums of every tile
+    int* arrivals = nullptr;   // slices of a tile that have ended (0 between launches)
 };
 
 namespace dq {
 namespace {
 
-constexpr int WAVES = 8;                  // waves of a workgroup, one share of the K steps each
+constexpr int SPLIT_TARGET = 256;         // workgroups the general form aims at (one for each CU)
 constexpr int X_BF16 = 0, X_F32 = 1, X_MX8 = 2;
 
 struct RowsArgs {
     const void* x;                        // rows (bf16, fp32) or E4M3 codes
     const uint8_t* xs;                    // E8M0 codes of MX-FP8 rows
     long long ldx;
-    int N, Ci, nks, Kp, Co, rp, tiles;
+    int N, Ci, nks, Co, rp, y_bf16, y_wide, tiles, slices, per;
     const uint8_t *rq, *rs;
-    const uint16_t *l1t, *l2t;
-    uint16_t* xp;
-    float* u;
+    const uint4* l1p;
+    const uint16_t* l2t;
+    float* sums;
+    int* arrivals;
     void* y;
     long long ldy;
 };
 
-// 8 consecutive channels of row n as bf16 operand pieces (zeros past N and Ci).
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// 8 consecutive channels of a row as they are loaded.
+template <int XK> struct Piece { uint4 d; };
+template <> struct Piece<X_F32> { uint4 d, hi; };
+template <> struct Piece<X_MX8> { uint2 d; int e; };
+
+// Channels ch .. of row n, zeros past N and Ci or where !live.  The load is
+// made in any case, from the nearest place that exists: a number of loads in
+// flight that does not depend on the lane lets the waits count them.
 template <int XK>
-__device__ __forceinline__ void operand8(const RowsArgs& a, int n, int ch, uint4* out) {
-    constexpr int P = XK == X_F32 ? 3 : 1;
-#pragma unroll
-    for (int p = 0; p < P; ++p) out[p] = make_uint4(0u, 0u, 0u, 0u);
-    if (n >= a.N || ch >= a.Ci) return;
+__device__ __forceinline__ Piece<XK> load_piece(const RowsArgs& a, int n, int ch, bool live = true) {
+    Piece<XK> v;
+    live = live && n < a.N && ch < a.Ci;
+    const long long row = min(n, a.N - 1);
+    ch = min(ch, a.Ci - 8);
     if constexpr (XK == X_BF16) {
-        out[0] = *(const uint4*)((const uint16_t*)a.x + n * a.ldx + ch);
+        v.d = *(const uint4*)((const uint16_t*)a.x + row * a.ldx + ch);
+    } else if constexpr (XK == X_F32) {
+        const uint4* p = (const uint4*)((const float*)a.x + row * a.ldx + ch);
+        v.d = p[0];
+        v.hi = p[1];
+        v.hi = live ? v.hi : make_uint4(0u, 0u, 0u, 0u);
     } else {
-        float v[8];
-        if constexpr (XK == X_F32) {
-            const float4* p = (const float4*)((const float*)a.x + n * a.ldx + ch);
-            const float4 lo = p[0], hi = p[1];
-            v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
-            v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
-        } else {
-            const uint2 d = *(const uint2*)((const uint8_t*)a.x + (long long)n * a.Ci + ch);
-            const int e = a.xs[(long long)n * (a.Ci >> 5) + (ch >> 5)];
-            const float s = e == 255 ? __uint_as_float(0x7fc00000u) : pow2f(e - 127);
-            typedef float v2f __attribute__((ext_vector_type(2)));
-            const v2f f0 = __builtin_amdgcn_cvt_pk_f32_fp8(d.x, false), f1 = __builtin_amdgcn_cvt_pk_f32_fp8(d.x, true);
-            const v2f f2 = __builtin_amdgcn_cvt_pk_f32_fp8(d.y, false), f3 = __builtin_amdgcn_cvt_pk_f32_fp8(d.y, true);
-            v[0] = f0[0] * s; v[1] = f0[1] * s; v[2] = f1[0] * s; v[3] = f1[1] * s;
-            v[4] = f2[0] * s; v[5] = f2[1] * s; v[6] = f3[0] * s; v[7] = f3[1] * s;
-        }
-        // the leading 8 bits, then those of what is left: differences are
-        // exact, so the parts sum to the value (a NaN or infinity is its first
-        // part alone)
-        uint32_t w[P][4];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float left = v[j];
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-                uint32_t b = __float_as_uint(left) >> 16;
-                if (p == 0 && (__float_as_uint(left) & 0x7fffffffu) > 0x7f800000u) b = 0x7fc0u;
-                left = p == 0 && (b & 0x7f80u) == 0x7f80u ? 0.0f : left - __uint_as_float(b << 16);
-                w[p][j >> 1] = j & 1 ? w[p][j >> 1] | (b << 16) : b;
-            }
-        }
-#pragma unroll
-        for (int p = 0; p < P; ++p) out[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+        v.d = *(const uint2*)((const uint8_t*)a.x + row * a.Ci + ch);
+        v.e = a.xs[row * (a.Ci >> 5) + (ch >> 5)];
+        v.e = live ? v.e : 0;
     }
+    v.d = live ? v.d : decltype(v.d){};
+    return v;
 }
 
-// First kernel: workgroups [0, nu) form U for one block of 16 rows and 16 low
-// ranks each; the others lay the rows out as matrix operands.  Piece f of K
-// step ks holds, for lane l, channels 128 ks + 32 (l / 16) + 8 f .. + 7 of row
-// l % 16: the lane quarter l / 16 walks one 32-channel group, as the weight's
-// 16-byte code chunks do.
+// fp32 values as the sum of three bf16 values: the leading 8 bits, then those
+// of what is left.  The differences are exact, so the parts sum to the value;
+// a NaN or an infinity is its first part alone.
+__device__ __forceinline__ void split3(const float* v, uint4* out) {
+    uint32_t w[3][4];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        float left = v[j];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            uint32_t b = __float_as_uint(left) >> 16;
+            if (p == 0 && (__float_as_uint(left) & 0x7fffffffu) > 0x7f800000u) b = 0x7fc0u;
+            left = p == 0 && (b & 0x7f80u) == 0x7f80u ? 0.0f : left - __uint_as_float(b << 16);
+            w[p][j >> 1] = j & 1 ? w[p][j >> 1] | (b << 16) : b;
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < 3; ++p) out[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+}
+
+// ... and as bf16 operand pieces: one, or three parts of fp32 values.
 template <int XK>
-__global__ __launch_bounds__(512) void k_rows_operands(RowsArgs a, int nu) {
-    constexpr int P = XK == X_F32 ? 3 : 1;
-    const int tid = threadIdx.x, lane = tid & 63;
-    if ((int)blockIdx.x >= nu) {
-        const long long id = (long long)(blockIdx.x - nu) * 512 + tid;      // (tb, ks, f, lane)
-        const long long step = id >> 8;
-        const int f = (int)(id >> 6) & 3;
-        const int tb = (int)(step / a.nks), ks = (int)(step % a.nks);
-        if (16 * tb >= a.N) return;
-        uint4 part[P];
-        operand8<XK>(a, 16 * tb + (lane & 15), 128 * ks + 32 * (lane >> 4) + 8 * f, part);
+__device__ __forceinline__ void operand(const Piece<XK>& v, uint4* out) {
+    if constexpr (XK == X_BF16) {
+        out[0] = v.d;
+    } else if constexpr (XK == X_F32) {
+        float f[8];
 #pragma unroll
-        for (int p = 0; p < P; ++p) ((uint4*)a.xp)[((step * P + p) * 4 + f) * 64 + lane] = part[p];
-        return;
-    }
-    __shared__ float red[WAVES][256];
-    const int rb = a.rp >> 4, tb = blockIdx.x / rb, q0 = blockIdx.x % rb * 16, w = tid >> 6;
-    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int ks = w; ks < a.nks; ks += WAVES) {
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            const int ch = 128 * ks + 32 * (lane >> 4) + 8 * f;
-            const uint4 l1 = *(const uint4*)(a.l1t + (long long)(q0 + (lane & 15)) * a.Kp + ch);
-            uint4 part[P];
-            operand8<XK>(a, 16 * tb + (lane & 15), ch, part);
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, l1), __builtin_bit_cast(v8bf, part[p]),
-                                                              acc, 0, 0, 0);
+        for (int i = 0; i < 4; ++i) {
+            f[i] = __uint_as_float(word(v.d, i));
+            f[4 + i] = __uint_as_float(word(v.hi, i));
         }
-    }
-    *(v4f*)&red[w][4 * lane] = acc;
-    __syncthreads();
-    if (tid < 256) {
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < WAVES; ++i) s += red[i][tid];
-        const int n = 16 * tb + ((tid >> 2) & 15), q = q0 + 4 * (tid >> 6) + (tid & 3);
-        a.u[(long long)n * a.rp + q] = s;
+        split3(f, out);
+    } else {
+        // (4 significant bits times a power of two: exact in bf16; scale code 255 makes the group NaN)
+        const float s = pow2f(v.e - 127);
+        const uint32_t lo = v.e == 255 ? 0x7f7f7f7fu : v.d.x, hi = v.e == 255 ? 0x7f7f7f7fu : v.d.y;
+        out[0] = make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false)),
+                            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true)),
+                            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, false)),
+                            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true)));
     }
 }
 
-// Second kernel: a workgroup owns 16 RB output channels of 16 TB rows; its
-// waves share out the K steps and their partial tiles are summed in wave
-// order, so a result does not depend on how the work was scheduled.
-template <int RB, int TB, int P, class YT>
-__global__ __launch_bounds__(64 * WAVES) void k_rows(RowsArgs a) {
-    __shared__ float red[WAVES][RB * TB * 256];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+// The weight of one row and 32 channels as four bf16 operands; exact (2
+// significant bits and a power of two).
+__device__ __forceinline__ v8bf weight8(uint32_t codes, float scale) {
+    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+    const v2bf p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0);
+    const v2bf p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1);
+    const v2bf p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2);
+    const v2bf p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3);
+    return v8bf{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+
+__device__ __forceinline__ v4f mfma(v8bf w, uint4 x, v4f acc) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(v8bf, x), acc, 0, 0, 0);
+}
+
+// U as a matrix operand.  Its 16 x 16 blocks (ranks by rows) come out of the
+// matrix instruction with ranks 4 g .. + 3 of row n in lane 16 g + n; as an
+// operand, lane l needs ranks 8 (l / 16) .. + 7 of row l % 16, which two lanes
+// 16 apart hold, the first of them in place u_place(l) of two blocks' 128.
+__device__ __forceinline__ int u_place(int lane) {
+    const int q = lane >> 4;
+    return (q >> 1) * 64 + 32 * (q & 1) + (lane & 15);
+}
+__device__ __forceinline__ void split_u(v4f u0, v4f u1, uint4* part) {
+    const float f[8] = {u0[0], u0[1], u0[2], u0[3], u1[0], u1[1], u1[2], u1[3]};
+    split3(f, part);
+}
+
+// acc += U L2 for the 32 low ranks from `at` on and output channels row + l % 16.
+__device__ __forceinline__ uint4 load_l2(const RowsArgs& a, int at, int row, int lane) {
+    return *(const uint4*)(a.l2t + (long long)(row + (lane & 15)) * a.rp + at + 8 * (lane >> 4));
+}
+__device__ __forceinline__ v4f low_rank(uint4 l2, const uint4* u, v4f acc) {
+#pragma unroll
+    for (int p = 0; p < 3; ++p) acc = mfma(__builtin_bit_cast(v8bf, l2), u[p], acc);
+    return acc;
+}
+
+// The weight stream of 16 RB output channels from row on.  Lane l reads channel
+// chunk l / 16 (32 channels, 16 bytes of codes and one scale) of row l % 16 in
+// each K step: 1 KB of codes in a row of the step-major layout.
+template <int RB>
+struct Stream {
+    const uint8_t *rq, *rs;
+    int so[RB];
+    __device__ __forceinline__ Stream(const RowsArgs& a, int row, int lane) {
+        const int q = lane >> 4, r0 = (row & 255) + (lane & 15);
+        const size_t block = (size_t)(row >> 8) * a.nks;
+        rq = a.rq + block * 16384 + r0 * 64 + ((q ^ swz4(r0)) << 4);
+        rs = a.rs + block * 1024;
+#pragma unroll
+        for (int i = 0; i < RB; ++i) so[i] = (int)toff_scale(r0 + 16 * i, q);
+    }
+    __device__ __forceinline__ void fetch(int ks, uint4* c, int* e) const {
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+            c[i] = *(const uint4*)(rq + (size_t)ks * 16384 + i * 1024);
+            e[i] = rs[(size_t)ks * 1024 + so[i]];
+        }
+    }
+};
+
+// The outputs of a lane: channels j .. j + 3 of row n.
+__device__ __forceinline__ void store_y(const RowsArgs& a, int n, int j, v4f y) {
+    if (n >= a.N || j >= a.Co) return;
+    typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+    if (a.y_bf16) {
+        __bf16* p = (__bf16*)a.y + n * a.ldy + j;
+        const v4bf b = {(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
+        if (a.y_wide && j + 4 <= a.Co) *(v4bf*)p = b;
+        else
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (j + i < a.Co) p[i] = b[i];
+    } else {
+        float* p = (float*)a.y + n * a.ldy + j;
+        if (a.y_wide && j + 4 <= a.Co) *(v4f*)p = y;
+        else
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (j + i < a.Co) p[i] = y[i];
+    }
+}
+
+// Few row parts and few channels (N16 rows, one part each or three): a wave
+// takes the rows' channels of its own K steps straight from x, G steps at a
+// time, and lays them out as operands in its own LDS rows (17 pieces apart, so
+// that neither the writes by row nor the reads by piece meet in a bank).  The
+// W waves of a workgroup share out the K steps of 16 RB output channels and
+// their partial sums are added in wave order.  With LR (32 low ranks) every
+// workgroup forms U as well: L1 is read again by each, from L2.
+// D steps are in flight.
+template <int XK, int N16, int LR, int RB, int W, int D>
+__global__ __launch_bounds__(64 * W) void k_rows_direct(RowsArgs a) {
+    constexpr int P = XK == X_F32 ? 3 : 1, G = 16 / (N16 * P), NI = (G * N16 + 3) / 4, SUMS = RB + (LR ? 2 : 0);
+    constexpr int SLOTS = 16 * 17 > 64 * SUMS ? 16 * 17 : 64 * SUMS;
+    __shared__ uint4 lds[W][SLOTS];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     // workgroups go to the 8 XCDs in turn; an XCD takes neighbouring tiles,
     // which share the 128-row blocks of the scale layout in its L2
     const int tile = (int)(blockIdx.x & 7) * (gridDim.x >> 3) + (int)(blockIdx.x >> 3);
     if (tile >= a.tiles) return;
-    const int row0 = tile * 16 * RB, q = lane >> 4, r0 = (row0 & 255) + (lane & 15);
-    const int n0 = blockIdx.y * 16 * TB;
-    const size_t block = (size_t)(row0 >> 8) * a.nks;
-    const uint8_t* rq = a.rq + block * 16384 + r0 * 64 + ((q ^ swz4(r0)) << 4);
-    const uint8_t* rs = a.rs + block * 1024;
-    int so[RB];
+    const int row0 = tile * 16 * RB;
+    const int per = (a.nks + W - 1) / W, k0 = w * per, k1 = min(a.nks, k0 + per);
+    v4f acc[SUMS];                                     // RB blocks of output channels, then two of low ranks
 #pragma unroll
-    for (int i = 0; i < RB; ++i) so[i] = (int)toff_scale(r0 + 16 * i, q);
-    const uint4* xp = (const uint4*)a.xp + (size_t)(n0 >> 4) * a.nks * P * 256 + lane;
-    const int per = (a.nks + WAVES - 1) / WAVES, k0 = w * per, k1 = min(a.nks, k0 + per);
-    v4f acc[RB][TB];
+    for (int i = 0; i < SUMS; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    // pieces of G steps: lane l takes piece l % 16 of source rows l / 16, + 4, ..
+    Piece<XK> px[NI];
+    auto load_x = [&](int ks) {
 #pragma unroll
-    for (int i = 0; i < RB; ++i)
-#pragma unroll
-        for (int t = 0; t < TB; ++t) acc[i][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr int U = RB == 1 ? 4 : 2;
-    for (int ks = k0; ks < k1; ks += U) {
-        uint4 c[U][RB];
-        int e[U][RB];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = min(ks + u, k1 - 1);
-#pragma unroll
-            for (int i = 0; i < RB; ++i) {
-                c[u][i] = *(const uint4*)(rq + (size_t)k * 16384 + i * 1024);
-                e[u][i] = rs[(size_t)k * 1024 + so[i]];
-            }
+        for (int i = 0; i < NI; ++i) {
+            const int R = 4 * i + (lane >> 4), g = R / N16;
+            px[i] = load_piece<XK>(a, R % N16, 128 * (ks + g) + 8 * (lane & 15), g < G && ks + g < k1);
         }
+    };
+    uint4* xs = lds[w];
+    auto stage_x = [&]() {
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (ks + u >= k1) break;
+        for (int i = 0; i < NI; ++i) {
+            const int R = 4 * i + (lane >> 4), g = R / N16, n = R % N16;
+            uint4 part[P];
+            operand<XK>(px[i], part);
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                if (g < G) xs[((g * P + p) * N16 + n) * 17 + (lane & 15)] = part[p];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    };
+    const Stream<RB> weight(a, row0, lane);
+    uint4 c[D][RB], l1[D][LR ? 8 : 1];
+    int e[D][RB];
+    auto fetch = [&](int d, int ks) {
+        weight.fetch(ks, c[d], e[d]);
+        if constexpr (LR) {
+#pragma unroll
+            for (int f = 0; f < 8; ++f) l1[d][f] = a.l1p[((long long)ks * 8 + f) * 64 + lane];
+        }
+    };
+    if (k0 < k1) load_x(k0);
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        if (k0 + d < k1) fetch(d, k0 + d);
+    uint4 l2;
+    if constexpr (LR) l2 = load_l2(a, 0, row0 + 16 * (w % RB), lane);
+    const int rd = (lane & (N16 - 1)) * 17 + 4 * (lane >> 4);
+    int staged = G;                                    // steps used of the staged ones
+    for (int ks = k0; ks < k1; ks += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (ks + d >= k1) break;
+            if (staged == G) {
+                stage_x();
+                if (ks + d + G < k1) load_x(ks + d + G);
+                staged = 0;
+            }
+            const int at = staged++ * P * N16 * 17 + rd;
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
-                v8bf wv[RB];
+                uint4 x[P];
+#pragma unroll
+                for (int p = 0; p < P; ++p) x[p] = xs[at + p * N16 * 17 + f];
 #pragma unroll
                 for (int i = 0; i < RB; ++i) {
-                    const float s = pow2f(e[u][i] - 127);
-                    const uint32_t d = f == 0 ? c[u][i].x : f == 1 ? c[u][i].y : f == 2 ? c[u][i].z : c[u][i].w;
-                    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-                    const v2bf p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 0);
-                    const v2bf p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 1);
-                    const v2bf p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 2);
-                    const v2bf p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 3);
-                    wv[i] = v8bf{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+                    const v8bf wv = weight8(word(c[d][i], f), pow2f(e[d][i] - 127));
+#pragma unroll
+                    for (int p = 0; p < P; ++p) acc[i] = mfma(wv, x[p], acc[i]);
                 }
+                if constexpr (LR) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int p = 0; p < P; ++p) acc[RB + i] = mfma(__builtin_bit_cast(v8bf, l1[d][4 * i + f]), x[p], acc[RB + i]);
+                }
+            }
+            if (ks + d + D < k1) fetch(d, ks + d + D);
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int i = 0; i < SUMS; ++i) ((v4f*)lds[w])[i * 64 + lane] = acc[i];
+    __syncthreads();
+    if (w >= RB) return;
+    const int row = row0 + 16 * w;
+    v4f y = ((const v4f*)lds[0])[w * 64 + lane];
+#pragma unroll
+    for (int i = 1; i < W; ++i) y += ((const v4f*)lds[i])[w * 64 + lane];
+    if constexpr (LR) {
+        const int from = RB * 64 + u_place(lane);
+        v4f u0 = {0.0f, 0.0f, 0.0f, 0.0f}, u1 = u0;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            u0 += ((const v4f*)lds[i])[from];
+            u1 += ((const v4f*)lds[i])[from + 16];
+        }
+        uint4 part[3];
+        split_u(u0, u1, part);
+        y = low_rank(l2, part, y);
+    }
+    if ((lane & 15) < N16) store_y(a, lane & 15, row + 4 * (lane >> 4), y);
+}
+
+// Sums that workgroups of one launch hand to each other: stores and loads with
+// the agent scope's cache bit (sc1, 16 in the buffer instructions' last
+// operand) go to and come from where every XCD's caches meet, so no cache
+// needs writing back or invalidating (fences that do that, one a wave, cost
+// 30 to 100 us here).
+typedef unsigned v4u __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t shared_sums(float* p, size_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(p, (short)0, (int)bytes, 0x00020000);
+}
+__device__ __forceinline__ void hand_over(__amdgpu_buffer_rsrc_t r, int at, v4f v) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, v), r, at * 16, 0, 16);
+}
+__device__ __forceinline__ v4f take_over(__amdgpu_buffer_rsrc_t r, int at) {
+    return __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(r, at * 16, 0, 16));
+}
+
+// The general form: a workgroup owns 128 output channels of 16 TB rows over one
+// slice of the K steps, in chunks of CH steps whose operands all its waves
+// share in LDS.  Wave w takes 32 channels (w % 4) of every other step (w / 4).
+// The slice's U is formed too (step w % CH, and of 32 low ranks all, or with
+// CH = 4 the half w / 4) and applied to the slice's sums, both being linear in
+// x, so L1 is read once a tile and step.  The slices' sums meet in the
+// workspace: whichever workgroup of a tile ends last adds them up in slice
+// order, so nothing waits and a result does not depend on the order of arrival.
+// LP: groups of 32 low ranks (1, also for rank 0, or 4).
+template <int XK, int TB, int LP>
+__global__ __launch_bounds__(512, LP == 1 ? 4 : 2) void k_rows_split(RowsArgs a) {
+    constexpr int P = XK == X_F32 ? 3 : 1, CH = 4, J = CH / 2, NP = CH * TB / 2, BLK = 16 * 17;
+    constexpr int UB = CH / 4, US = 8 / CH;            // blocks of 16 ranks a wave forms of 32; ranks' share of a step
+    static_assert(CH * P * TB * BLK >= 8 * TB * 64 * (1 + UB), "sums and U reuse the operands' LDS");
+    __shared__ uint4 lds[CH * P * TB * BLK];
+    __shared__ int arrived;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // the slices of a tile go to one XCD (workgroups go to the 8 XCDs in turn)
+    const int turn = (int)(blockIdx.x >> 3), tile = (int)(blockIdx.x & 7) + 8 * (turn / a.slices), slice = turn % a.slices;
+    if (tile >= a.tiles) return;
+    const int n0 = (int)blockIdx.y * 16 * TB, wk = w >> 2, row0 = tile * 128 + 32 * (w & 3);
+    const int k0 = slice * a.per, k1 = min(a.nks, k0 + a.per), passes = a.rp >> 5;
+    const int ug = w % CH, ub = US == 1 ? 0 : wk;      // step of a chunk and first rank block of this wave's U
+    v4f acc[TB][2], u[LP][UB][TB];
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+        acc[t][0] = acc[t][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int r = 0; r < LP; ++r)
+#pragma unroll
+            for (int i = 0; i < UB; ++i) u[r][i][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    // thread t takes piece t % 16 of token rows t / 16, + 32, .. of a chunk (16 TB rows a step)
+    Piece<XK> px[NP];
+    auto load_x = [&](int ks) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int R = 32 * i + (tid >> 4);
+            px[i] = load_piece<XK>(a, n0 + R % (16 * TB), 128 * (ks + R / (16 * TB)) + 8 * (tid & 15));
+        }
+    };
+    auto stage_x = [&]() {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int R = 32 * i + (tid >> 4), g = R / (16 * TB), n = R % (16 * TB);
+            uint4 part[P];
+            operand<XK>(px[i], part);
+#pragma unroll
+            for (int p = 0; p < P; ++p) lds[((g * P + p) * TB * 16 + n) * 17 + (tid & 15)] = part[p];
+        }
+    };
+    const Stream<2> weight(a, row0, lane);
+    uint4 c[J][2], l1[UB * 4];
+    int e[J][2];
+    auto load_u = [&](int ks, int r) {                 // (places past the slice: its last step again, not used)
+        const long long at = ((long long)min(ks + ug, k1 - 1) * (a.rp >> 4) + 2 * r + ub) * 256 + lane;
+#pragma unroll
+        for (int i = 0; i < UB * 4; ++i) l1[i] = a.l1p[at + i * 64];
+    };
+    const int rd = (lane & 15) * 17 + 4 * (lane >> 4);
+    auto chunk = [&](int ks, auto more) {
+        constexpr bool MORE = decltype(more)::value;   // another chunk follows
+        stage_x();
+        __syncthreads();
+        if constexpr (MORE) load_x(ks + CH);
+        auto form_u = [&](int r) {
+#pragma unroll
+            for (int i = 0; i < UB; ++i)
+#pragma unroll
+                for (int f = 0; f < 4; ++f)
+#pragma unroll
+                    for (int t = 0; t < TB; ++t)
+#pragma unroll
+                        for (int p = 0; p < P; ++p)
+                            u[r][i][t] = mfma(__builtin_bit_cast(v8bf, l1[4 * i + f]), lds[((ug * P + p) * TB + t) * BLK + rd + f],
+                                              u[r][i][t]);
+        };
+        if (passes && (MORE || ks + ug < k1)) {
+            form_u(0);
+#pragma unroll
+            for (int r = 1; r < LP; ++r)
+                if (r < passes) {
+                    load_u(ks, r);
+                    form_u(r);
+                }
+        }
+        if constexpr (MORE)
+            if (passes) load_u(ks + CH, 0);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int g = 2 * j + wk;
+            if (!MORE && ks + g >= k1) break;
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                const v8bf w0 = weight8(word(c[j][0], f), pow2f(e[j][0] - 127));
+                const v8bf w1 = weight8(word(c[j][1], f), pow2f(e[j][1] - 127));
 #pragma unroll
                 for (int t = 0; t < TB; ++t)
 #pragma unroll
                     for (int p = 0; p < P; ++p) {
-                        // (row blocks past N, read by the last group, lie in the workspace; their results are not stored)
-                        const v8bf xv = __builtin_bit_cast(v8bf, xp[(((size_t)t * a.nks + ks + u) * P + p) * 256 + f * 64]);
-#pragma unroll
-                        for (int i = 0; i < RB; ++i)
-                            acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[i], xv, acc[i][t], 0, 0, 0);
+                        const uint4 x = lds[((g * P + p) * TB + t) * BLK + rd + f];
+                        acc[t][0] = mfma(w0, x, acc[t][0]);
+                        acc[t][1] = mfma(w1, x, acc[t][1]);
                     }
             }
+            if constexpr (MORE) weight.fetch(min(ks + CH + g, k1 - 1), c[j], e[j]);
         }
+        __syncthreads();                               // (the operands are read)
+    };
+    const int row = row0 + 16 * wk;                    // the 16 channels this wave finishes
+    load_x(k0);
+    uint4 l2 = make_uint4(0u, 0u, 0u, 0u);
+    if (passes) {
+        load_u(k0, 0);
+        l2 = load_l2(a, 0, row, lane);
     }
 #pragma unroll
-    for (int i = 0; i < RB; ++i)
+    for (int j = 0; j < J; ++j) weight.fetch(min(k0 + 2 * j + wk, k1 - 1), c[j], e[j]);
+    int ks = k0;
+    for (; ks + CH < k1; ks += CH) chunk(ks, std::true_type());
+    chunk(ks, std::false_type());
+    // each wave finishes the 16 channels wk of its 32: the other half goes to
+    // its partner (w ^ 4) through LDS, and its share of U to every wave
+    v4f *part = (v4f*)lds, *us = part + 8 * TB * 64;
 #pragma unroll
-        for (int t = 0; t < TB; ++t) *(v4f*)&red[w][((i * TB + t) * 64 + lane) * 4] = acc[i][t];
-    __syncthreads();
-    for (int o = tid; o < RB * TB * 256; o += 64 * WAVES) {
-        const int l = (o >> 2) & 63, unit = o >> 8;
-        const int n = n0 + unit % TB * 16 + (l & 15), j = row0 + unit / TB * 16 + 4 * (l >> 4) + (o & 3);
-        if (n >= a.N || j >= a.Co) continue;
-        float s = 0.0f;
+    for (int t = 0; t < TB; ++t) part[(w * TB + t) * 64 + lane] = wk ? acc[t][0] : acc[t][1];
+    v4f y[TB];
 #pragma unroll
-        for (int i = 0; i < WAVES; ++i) s += red[i][o];
-        if (a.rp) {
-            const float* u = a.u + (long long)n * a.rp;
-            const uint16_t* l2 = a.l2t + (long long)j * a.rp;
-            float lr = 0.0f;
-            for (int i = 0; i < a.rp; i += 8) {
-                float b[8];
-                const uint4 d = *(const uint4*)(l2 + i);
-                const uint32_t wd[4] = {d.x, d.y, d.z, d.w};
+    for (int r = 0; r < LP; ++r) {
+        if (r && r >= passes) break;
+        if (r) {
+            l2 = load_l2(a, 32 * r, row, lane);
+            __syncthreads();
+        }
+        if (passes) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    b[2 * k] = __uint_as_float(wd[k] << 16);
-                    b[2 * k + 1] = __uint_as_float(wd[k] & 0xffff0000u);
-                }
+            for (int i = 0; i < UB; ++i)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) lr = __builtin_fmaf(u[i + k], b[k], lr);
+                for (int t = 0; t < TB; ++t) us[((w * UB + i) * TB + t) * 64 + lane] = u[r][i][t];
+        }
+        __syncthreads();
+        if (r == 0) {
+#pragma unroll
+            for (int t = 0; t < TB; ++t) {
+                const v4f other = part[((w ^ 4) * TB + t) * 64 + lane];
+                y[t] = wk ? other + acc[t][1] : acc[t][0] + other;
             }
-            s += lr;
         }
-        if constexpr (sizeof(YT) == 2) ((__bf16*)a.y)[n * a.ldy + j] = (__bf16)s;
-        else ((float*)a.y)[n * a.ldy + j] = s;
+        if (!passes) break;
+        // rank block b of 32 lies in the waves' place b (UB = 2), or in the half b of the waves (UB = 1)
+        const int from = u_place(lane), b = from >> 6, base = (UB == 2 ? b : 4 * b) * TB * 64 + (from & 63);
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+            v4f u0 = {0.0f, 0.0f, 0.0f, 0.0f}, u1 = u0;
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                u0 += us[base + (i * UB * TB + t) * 64];
+                u1 += us[base + (i * UB * TB + t) * 64 + 16];
+            }
+            uint4 up[3];
+            split_u(u0, u1, up);
+            y[t] = low_rank(l2, up, y[t]);
+        }
     }
+    if (a.slices > 1) {
+        const long long unit = (long long)blockIdx.y * a.tiles + tile;
+        const int size = 8 * TB * 64, mine = w * TB * 64 + lane;        // 16-byte places of one slice's sums
+        const __amdgpu_buffer_rsrc_t sums = shared_sums(a.sums + unit * a.slices * size * 4, (size_t)a.slices * size * 16);
+#pragma unroll
+        for (int t = 0; t < TB; ++t) hand_over(sums, slice * size + mine + t * 64, y[t]);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (every wave's sums have arrived before the workgroup says so)
+        __syncthreads();
+        if (tid == 0) arrived = __hip_atomic_fetch_add(a.arrivals + unit, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        if (arrived != a.slices - 1) return;
+        for (int i = 0; i < a.slices; i += 8) {        // (8 slices' loads in flight)
+#pragma unroll
+            for (int t = 0; t < TB; ++t) {
+                v4f v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = take_over(sums, min(i + k, a.slices - 1) * size + mine + t * 64);
+                if (i == 0) y[t] = v[0];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (i + k > 0 && i + k < a.slices) y[t] += v[k];
+            }
+        }
+        if (tid == 0) a.arrivals[unit] = 0;            // (for the next launch)
+    }
+#pragma unroll
+    for (int t = 0; t < TB; ++t) store_y(a, n0 + 16 * t + (lane & 15), row + 4 * (lane >> 4), y[t]);
 }
 
-template <int RB, int TB, int P>
-void launch_tiles(RowsArgs a, int y_bf16, hipStream_t st) {
+template <int XK, int N16, int LR, int RB, int W, int D>
+void launch_direct(RowsArgs a, hipStream_t st) {
     a.tiles = (a.Co + 16 * RB - 1) / (16 * RB);
-    const dim3 grid((unsigned)round_up(a.tiles, 8), (unsigned)((a.N + 16 * TB - 1) / (16 * TB)));
-    if (y_bf16) k_rows<RB, TB, P, uint16_t><<<grid, 64 * WAVES, 0, st>>>(a);
-    else k_rows<RB, TB, P, float><<<grid, 64 * WAVES, 0, st>>>(a);
+    k_rows_direct<XK, N16, LR, RB, W, D><<<(unsigned)round_up(a.tiles, 8), 64 * W, 0, st>>>(a);
+}
+
+// How the general form splits N rows of a weight: 16 tb rows to a tile, K
+// slices of `per` steps.
+struct SplitPlan {
+    int tb, groups, tiles, slices, per;
+    int64_t units() const { return (int64_t)groups * tiles; }
+    int64_t sum_floats() const { return slices > 1 ? units() * slices * 8 * tb * 256 : 0; }
+};
+// `parts` of a row: three for fp32 rows, whose larger operands leave LDS for
+// 16 rows at a time.
+SplitPlan plan_split(int64_t N, int64_t Co, int nks, int parts) {
+    SplitPlan p;
+    p.tb = N <= 16 || parts > 1 ? 1 : 2;
+    p.groups = (int)((N + 16 * p.tb - 1) / (16 * p.tb));
+    p.tiles = (int)((Co + 127) / 128);
+    const int64_t target = parts > 1 && p.groups > 1 ? 2 * SPLIT_TARGET : SPLIT_TARGET;
+    const int64_t most = std::max<int64_t>(1, target / p.units());
+    p.per = (int)std::max<int64_t>(std::min(nks, 2), (nks + most - 1) / most);
+    p.slices = (nks + p.per - 1) / p.per;
+    return p;
+}
+
+template <int XK, int TB>
+void launch_split(RowsArgs a, const SplitPlan& p, hipStream_t st) {
+    a.tiles = p.tiles;
+    a.slices = p.slices;
+    a.per = p.per;
+    const dim3 grid((unsigned)(round_up(p.tiles, 8) * p.slices), (unsigned)p.groups);
+    if (a.rp <= 32) k_rows_split<XK, TB, 1><<<grid, 512, 0, st>>>(a);
+    else k_rows_split<XK, TB, 4><<<grid, 512, 0, st>>>(a);
 }
 
 template <int XK>
-hipError_t launch_rows_product(const RowsArgs& a, int y_bf16, hipStream_t st) {
+hipError_t launch_rows_product(const RowsArgs& a, hipStream_t st) {
     constexpr int P = XK == X_F32 ? 3 : 1;
-    const int tbs = (a.N + 15) / 16, nu = tbs * (a.rp / 16);
-    const long long pieces = (long long)tbs * a.nks * 256;
-    k_rows_operands<XK><<<(unsigned)(nu + (pieces + 511) / 512), 512, 0, st>>>(a, nu);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (tbs == 1) {
-        if (a.Co >= 16 * 1024) launch_tiles<2, 1, P>(a, y_bf16, st);
-        else launch_tiles<1, 1, P>(a, y_bf16, st);
-    } else if (tbs == 2) {
-        launch_tiles<2, 2, P>(a, y_bf16, st);
+    const SplitPlan p = plan_split(a.N, a.Co, a.nks, P);
+    const bool direct = a.N <= (P == 1 ? 16 : 4) && (a.rp == 0 || (a.rp == 32 && a.nks <= 60)) && !(P == 1 && p.slices == 1);
+    if (direct) {
+        const auto go = [&](auto lr, auto rb) {
+            constexpr int LR = decltype(lr)::value, RB = decltype(rb)::value, D = LR || P == 3 ? 1 : 2;
+            if (a.N == 1) launch_direct<XK, 1, LR, RB, 8, D>(a, st);
+            else if (a.N <= 4) launch_direct<XK, 4, LR, RB, 8, D>(a, st);
+            else if constexpr (P == 1) launch_direct<XK, 16, LR, RB, 8, D>(a, st);
+        };
+        const std::integral_constant<int, 0> none;
+        const std::integral_constant<int, 1> some;
+        const std::integral_constant<int, 2> two;
+        const std::integral_constant<int, 4> four;
+        if (a.Co >= 8192) a.rp ? go(some, four) : go(none, four);
+        else a.rp ? go(some, two) : go(none, two);
     } else {
-        launch_tiles<2, 4, P>(a, y_bf16, st);
+        if (p.tb == 1) launch_split<XK, 1>(a, p, st);
+        else if constexpr (P == 1) launch_split<XK, 2>(a, p, st);
     }
     return hipGetLastError();
 }
@@ -299,8 +629,8 @@ hipError_t zalloc(T** p, size_t count, size_t* total) {
 void free_rows(dq_rows* a) {
     if (!a) return;
     DeviceGuard dg(a->device);
-    (void)hipFree(a->xp);
-    (void)hipFree(a->u);
+    (void)hipFree(a->sums);
+    (void)hipFree(a->arrivals);
     delete a;
 }
 
@@ -319,22 +649,24 @@ dq_status check_rows(const dq_weights* w, const dq_rows* a, int64_t N, const voi
     return DQ_OK;
 }
 
-RowsArgs rows_args(const dq_weights* w, dq_rows* a, int64_t N, void* y, int64_t ldy) {
+RowsArgs rows_args(const dq_weights* w, dq_rows* a, int64_t N, void* y, dq_dtype ydt, int64_t ldy) {
     RowsArgs r{};
     r.N = (int)N;
     r.Ci = (int)w->Ci;
     r.nks = (int)(w->Kp / 128);
-    r.Kp = (int)w->Kp;
     r.Co = (int)w->Co;
     r.rp = w->rp;
     r.rq = w->rq;
     r.rs = w->rs;
-    r.l1t = w->l1t;
+    r.l1p = (const uint4*)w->l1p;
     r.l2t = w->l2t;
-    r.xp = a->xp;
-    r.u = a->u;
+    r.sums = a->sums;
+    r.arrivals = a->arrivals;
     r.y = y;
     r.ldy = ldy;
+    r.y_bf16 = ydt == DQ_BF16;
+    const int four = ydt == DQ_BF16 ? 8 : 16;       // bytes of a lane's four outputs
+    r.y_wide = (uintptr_t)y % four == 0 && ldy % 4 == 0;
     return r;
 }
 
@@ -404,6 +736,7 @@ dq_status dq_rows_create(const dq_weights* w, int64_t max_rows, dq_rows** out) {
     if (!w) return fail(DQ_ERR_INVALID_ARG, "weights handle is NULL");
     if (w->wfmt != 4) return fail(DQ_ERR_INVALID_ARG, "a 6-bit weight takes the 6-bit entry points");
     if (max_rows < 1 || max_rows > 4096) return fail(DQ_ERR_SHAPE, "max_rows must be in [1, 4096]");
+    if (w->Ci > 65536) return fail(DQ_ERR_SHAPE, "Ci must be <= 65536 for few-row products");
     DeviceGuard dg(w->device);
     if (!dg.ok) return fail(DQ_ERR_DEVICE, "hipSetDevice failed");
     auto* a = new (std::nothrow) dq_rows();
@@ -416,11 +749,16 @@ dq_status dq_rows_create(const dq_weights* w, int64_t max_rows, dq_rows** out) {
     a->Kp = w->Kp;
     a->rp = w->rp;
     size_t bytes = 0;
-    // (three parts for fp32 rows; whole groups of 64 rows, which the widest tile reads)
-    const int64_t rows = round_up(max_rows, max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : 64);
+    int64_t floats = 0, units = 0;                      // the largest need of any row count up to max_rows
+    for (int64_t n = 16; n < max_rows + 16; n += 16)
+        for (const int parts : {1, 3}) {
+            const SplitPlan p = plan_split(std::min(n, max_rows), w->Co, (int)(w->Kp / 128), parts);
+            floats = std::max(floats, p.sum_floats());
+            units = std::max(units, p.units());
+        }
     hipError_t e;
-    if ((e = zalloc(&a->xp, (size_t)(rows * w->Kp * 3), &bytes)) != hipSuccess ||
-        (e = zalloc(&a->u, (size_t)(rows * w->rp), &bytes)) != hipSuccess)
+    if ((e = zalloc(&a->sums, (size_t)floats, &bytes)) != hipSuccess ||
+        (e = zalloc(&a->arrivals, (size_t)units, &bytes)) != hipSuccess)
         return hip_fail(e, "hipMalloc workspace");
     if ((e = hipDeviceSynchronize()) != hipSuccess) return hip_fail(e, "workspace init");
     *out = guard.release();
@@ -442,11 +780,11 @@ dq_status dq_linear_rows(const dq_weights* w, const void* x_dev, dq_dtype dt, in
         return fail(DQ_ERR_SHAPE, "the row stride of x must be at least Ci and a multiple of 16 bytes");
     DeviceGuard dg(a->device);
     if (!dg.ok) return fail(DQ_ERR_DEVICE, "hipSetDevice failed");
-    RowsArgs r = rows_args(w, a, N, y_dev, ldy);
+    RowsArgs r = rows_args(w, a, N, y_dev, ydt, ldy);
     r.x = x_dev;
     r.ldx = ldx;
-    const hipError_t e = dt == DQ_BF16 ? launch_rows_product<X_BF16>(r, ydt == DQ_BF16, (hipStream_t)stream)
-                                       : launch_rows_product<X_F32>(r, ydt == DQ_BF16, (hipStream_t)stream);
+    const hipError_t e = dt == DQ_BF16 ? launch_rows_product<X_BF16>(r, (hipStream_t)stream)
+                                       : launch_rows_product<X_F32>(r, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "product launch");
     return DQ_OK;
 }
@@ -461,10 +799,10 @@ dq_status dq_linear_rows8(const dq_weights* w, const uint8_t* codes_dev, const u
     if ((uintptr_t)codes_dev % 8 != 0) return fail(DQ_ERR_INVALID_ARG, "codes_dev must be 8-byte aligned");
     DeviceGuard dg(a->device);
     if (!dg.ok) return fail(DQ_ERR_DEVICE, "hipSetDevice failed");
-    RowsArgs r = rows_args(w, a, N, y_dev, ldy);
+    RowsArgs r = rows_args(w, a, N, y_dev, ydt, ldy);
     r.x = codes_dev;
     r.xs = scales_dev;
-    const hipError_t e = launch_rows_product<X_MX8>(r, ydt == DQ_BF16, (hipStream_t)stream);
+    const hipError_t e = launch_rows_product<X_MX8>(r, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "product launch");
     return DQ_OK;
 }
