@@ -72,7 +72,7 @@ def test_import_refusals(lib):
 
 
 W = SimpleNamespace(Ci=64, Co=96, rank=16, device=0, handle=None)
-R = SimpleNamespace(weights=W, handle=None, max_rows=8)
+R = SimpleNamespace(weights=W, handle=None, max_rows=8, pair=None)
 
 
 def _raises(fn, *args, match, **kw):
@@ -80,7 +80,7 @@ def _raises(fn, *args, match, **kw):
         fn(*args, **kw)
 
 
-def test_binding_refusals():
+def test_binding_refusals(lib):
     y = torch.zeros(3, 96)
     f = dq.dq_linear_rows
     _raises(f, W, torch.zeros(3, 64, dtype=torch.float16), R, y, match="dtype")

@@ -16,6 +16,7 @@ import numpy as np
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
+_CALL = None            # the native marshalling of the small calls (csrc/binding.cpp)
 
 DQ_F32, DQ_BF16 = 0, 1
 STATUS = {0: "DQ_OK", 1: "DQ_ERR_INVALID_ARG", 2: "DQ_ERR_SHAPE", 3: "DQ_ERR_UNSUPPORTED",
@@ -50,8 +51,8 @@ def library_path() -> str:
 
 
 def load():
-    """Load libdq.so (raises if it has not been built)."""
-    global _LIB
+    """Load libdq.so and the binding's native part (raises if they have not been built)."""
+    global _LIB, _CALL
     if _LIB is not None:
         return _LIB
     path = library_path()
@@ -110,6 +111,9 @@ def load():
         f = getattr(lib, name)
         f.argtypes = args
         f.restype = res
+    import torch  # noqa: F401  (the native part links against its libraries)
+    from . import _dqcall
+    _CALL = _dqcall
     _LIB = lib
     return lib
 
@@ -524,11 +528,17 @@ class Rows:
         self.handle = handle
         self.weights = weights
         self.max_rows = max_rows
+        self.pair = (weights.handle.value, handle.value, weights.Ci, weights.Co, weights.device)
 
     def __del__(self):
         if getattr(self, "handle", None) and _LIB is not None:
             _LIB.dq_rows_destroy(self.handle)
             self.handle = None
+
+
+def _native():
+    load()
+    return _CALL
 
 
 def _row_tensor(func: str, name: str, t, shape, dtypes, device: int, align: int, strided: bool = True):
@@ -604,8 +614,13 @@ def dq_rows_create(w: Weights, max_rows: int) -> Rows:
 def dq_linear_rows(w: Weights, x, a: Rows, y, stream=None):
     """y [N][Co] (fp32 or bf16) = x Q4(R) + (x L1) L2 for x [N][Ci] in bf16 or
     fp32; rows of either may be strided."""
-    import torch
     f = "dq_linear_rows"
+    if a.weights is w and _CALL is not None:
+        status = _CALL.linear_rows(a.pair, x, y, None if stream is None else getattr(stream, "cuda_stream", stream))
+        if status is not None:
+            return _check(status, f) if status else None
+    # (not such tensors: the checks below say what is wrong)
+    import torch
     _check_pair(f, w, a)
     types = (torch.bfloat16, torch.float32)
     n = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 2 else 0
@@ -618,8 +633,12 @@ def dq_linear_rows(w: Weights, x, a: Rows, y, stream=None):
 def dq_linear_rows8(w: Weights, codes, scales, a: Rows, y, stream=None):
     """dq_linear_rows for rows in MX-FP8: codes [N][Ci] and scales [N][Ci/32]
     as dq_rmsnorm8 writes them."""
-    import torch
     f = "dq_linear_rows8"
+    if a.weights is w and _CALL is not None:
+        status = _CALL.linear_rows8(a.pair, codes, scales, y, None if stream is None else getattr(stream, "cuda_stream", stream))
+        if status is not None:
+            return _check(status, f) if status else None
+    import torch
     _check_pair(f, w, a)
     n = codes.shape[0] if isinstance(codes, torch.Tensor) and codes.dim() == 2 else 0
     _mx8_tensors(f, codes, scales, n, w.Ci, w.device)
@@ -632,8 +651,12 @@ def dq_rmsnorm8(x, gain, eps: float, codes=None, scales=None, residual=None, h=N
     """RMS norm of x + residual as MX-FP8 codes [N][C] and scales [N][C/32], as
     plain values y, or both; h receives x + residual (it, or y, may be x or
     residual itself).  gain [C] in bf16 or fp32, or None."""
-    import torch
     f = "dq_rmsnorm8"
+    status = (_CALL or _native()).rmsnorm8(x, gain, eps, codes, scales, residual, h, y, group,
+                                           None if stream is None else getattr(stream, "cuda_stream", stream))
+    if status is not None:
+        return _check(status, f) if status else None
+    import torch
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or not x.is_cuda:
         _invalid(f, "x must be a 2-D torch tensor on a GPU")
     n, c = x.shape
