@@ -51,10 +51,12 @@ def _compare(want, codes, scales, h=None, y=None, dtype="bf16"):
 
 
 # Every number of 8-channel chunks a thread can hold, at both ends of each
-# block width (64, 256 and 1024 threads to a row), rows that do not fill a
-# workgroup, one row, many rows.
+# width (threads to a row), rows that do not fill a workgroup, one row, many
+# rows: those of up to 3 2^20 elements take one form, larger ones another.
 SHAPES = [(1, 32), (3, 32), (5, 64), (7, 512), (4, 544), (9, 1024), (2, 1536), (6, 2048), (1, 2080), (3, 4096), (2, 5120),
-          (2, 6176), (3, 8192), (1, 8224), (2, 13824), (1, 16384), (2, 24608), (1, 32768), (1031, 96), (517, 1536), (130, 5120)]
+          (2, 6176), (3, 8192), (1, 8224), (2, 13824), (1, 16384), (2, 24608), (1, 32768), (1031, 96), (517, 1536), (130, 5120),
+          (32801, 96), (6200, 512), (3111, 1024), (2051, 1536), (1541, 2048), (1513, 2080), (771, 4096), (615, 5120), (387, 8192),
+          (383, 8224), (229, 13824), (193, 16384), (129, 24608), (97, 32768)]
 
 
 @pytest.mark.parametrize("n,c", SHAPES)

@@ -38,11 +38,19 @@ struct NormArgs {
     double eps;
 };
 
+typedef uint32_t v4w __attribute__((ext_vector_type(4)));
+typedef uint32_t v2w __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ v4w get16(const void* p) { return *(const v4w*)p; }
+template <bool NT, class V>
+__device__ __forceinline__ void put(void* p, V v) {
+    if constexpr (NT) __builtin_nontemporal_store(v, (V*)p);
+    else *(V*)p = v;
+}
+
 template <class T> struct Stream;
 template <> struct Stream<uint16_t> {
     static __device__ __forceinline__ void load(const uint16_t* p, float* v) {
-        const uint4 d = *(const uint4*)p;
-        const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+        const v4w w = get16(p);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[2 * i] = __uint_as_float(w[i] << 16);
@@ -50,43 +58,54 @@ template <> struct Stream<uint16_t> {
         }
     }
     static __device__ __forceinline__ float round(float v) { return (float)(__bf16)v; }
-    static __device__ __forceinline__ void store(uint16_t* p, const float* v) {
+    template <bool NT> static __device__ __forceinline__ void store(uint16_t* p, const float* v) {
         v8bf b;
 #pragma unroll
         for (int i = 0; i < 8; ++i) b[i] = (__bf16)v[i];
-        *(uint4*)p = __builtin_bit_cast(uint4, b);
+        put<NT>(p, __builtin_bit_cast(v4w, b));
     }
 };
 template <> struct Stream<float> {
     static __device__ __forceinline__ void load(const float* p, float* v) {
-        const float4 a = ((const float4*)p)[0], b = ((const float4*)p)[1];
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        const v4w a = get16(p), b = get16(p + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = __uint_as_float(a[i]);
+            v[4 + i] = __uint_as_float(b[i]);
+        }
     }
     static __device__ __forceinline__ float round(float v) { return v; }
-    static __device__ __forceinline__ void store(float* p, const float* v) {
-        ((float4*)p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        ((float4*)p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    template <bool NT> static __device__ __forceinline__ void store(float* p, const float* v) {
+        put<NT>(p, v4f{v[0], v[1], v[2], v[3]});
+        put<NT>(p + 4, v4f{v[4], v[5], v[6], v[7]});
     }
 };
 
-// Codes of 8 consecutive values; `a` is the group's largest finite magnitude.
-__device__ __forceinline__ uint2 encode8(const float* v, float scale) {
-    uint2 d;
+// Codes of 8 consecutive values, each v / scale rounded to nearest even.
+__device__ __forceinline__ v2w encode8(const float* v, float scale) {
     v2s z = {0, 0};
     v2s a = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(z, v[0], v[1], scale, false);
     a = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(a, v[2], v[3], scale, true);
     v2s b = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(z, v[4], v[5], scale, false);
     b = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(b, v[6], v[7], scale, true);
-    d.x = __builtin_bit_cast(uint32_t, a);
-    d.y = __builtin_bit_cast(uint32_t, b);
-    return d;
+    return v2w{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
+}
+
+__device__ __forceinline__ void load_gain(const NormArgs& a, int c, float* g) {
+    if (!a.g) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = 1.0f;
+    } else if (a.g_bf16) {
+        Stream<uint16_t>::load((const uint16_t*)a.g + 8 * c, g);
+    } else {
+        Stream<float>::load((const float*)a.g + 8 * c, g);
+    }
 }
 
 // A row is held in registers by TPR threads, CH chunks of 8 channels each
 // (chunk i of thread t: channels 8 (i TPR + t) ..), so it is read once; a
 // group of 32 channels is 4 neighbouring lanes' chunk.
-template <class T, int TPR, int CH>
+template <class T, int TPR, int CH, bool NT>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm8(NormArgs a) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
     constexpr int WPR = TPR / 64;
@@ -143,29 +162,21 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm8(NormArgs a) 
         T* hp = (T*)a.h + row * a.ldh;
 #pragma unroll
         for (int i = 0; i < CH; ++i)
-            if (i * TPR + t < nch) Stream<T>::store(hp + 8 * (i * TPR + t), h[i]);
+            if (i * TPR + t < nch) Stream<T>::template store<NT>(hp + 8 * (i * TPR + t), h[i]);
     }
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int c = i * TPR + t;
         if (c >= nch) continue;                     // (whole groups: C % 32 == 0, or % 64 with wide scales)
-        float g[8];
-        if (!a.g) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) g[j] = 1.0f;
-        } else if (a.g_bf16) {
-            Stream<uint16_t>::load((const uint16_t*)a.g + 8 * c, g);
-        } else {
-            Stream<float>::load((const float*)a.g + 8 * c, g);
-        }
-        float v[8];
+        float g[8], v[8];
+        load_gain(a, c, g);
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             v[j] = (h[i][j] * f) * g[j];
             top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);   // (magnitudes order like their bits)
         }
-        if (a.y) Stream<T>::store((T*)a.y + row * a.ldy + 8 * c, v);
+        if (a.y) Stream<T>::template store<NT>((T*)a.y + row * a.ldy + 8 * c, v);
         if (!a.codes) continue;
         uint32_t bad = 0;                           // infinite or NaN elements: the NaN code, not part of the scale
         if (top >= 0x7f800000u) {
@@ -185,37 +196,54 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm8(NormArgs a) 
         top = max(top, (uint32_t)__shfl_xor((int)top, 2, 64));
         if (a.wide) top = max(top, (uint32_t)__shfl_xor((int)top, 4, 64));
         const int e = mx_exp_fp8(__uint_as_float(top));
-        uint2 d = encode8(v, pow2f(e));
+        v2w d = encode8(v, pow2f(e));
         if (bad) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (bad >> j & 1) d.x |= 0x7fu << (8 * j);
-                if (bad >> (j + 4) & 1) d.y |= 0x7fu << (8 * j);
+                if (bad >> j & 1) d[0] |= 0x7fu << (8 * j);
+                if (bad >> (j + 4) & 1) d[1] |= 0x7fu << (8 * j);
             }
         }
-        *(uint2*)(a.codes + row * a.C + 8 * c) = d;
+        put<NT>(a.codes + row * a.C + 8 * c, d);
         if ((t & 3) == 0) a.scales[row * (a.C >> 5) + (c >> 2)] = (uint8_t)(e + 127);
     }
 }
 
-template <class T, int TPR>
+// C / 8 chunks over TPR threads: MIN to 4 each.
+template <class T, int TPR, int MIN, bool NT>
 void launch_norm(const NormArgs& a, hipStream_t st) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
     const unsigned grid = (unsigned)((a.N + RPB - 1) / RPB);
-    const int threads = TPR < 256 ? 256 : TPR;
-    switch ((a.C / 8 + TPR - 1) / TPR) {
-        case 1: k_rmsnorm8<T, TPR, 1><<<grid, threads, 0, st>>>(a); break;
-        case 2: k_rmsnorm8<T, TPR, 2><<<grid, threads, 0, st>>>(a); break;
-        case 3: k_rmsnorm8<T, TPR, 3><<<grid, threads, 0, st>>>(a); break;
-        default: k_rmsnorm8<T, TPR, 4><<<grid, threads, 0, st>>>(a); break;
-    }
+    const int threads = TPR < 256 ? 256 : TPR, ch = (a.C / 8 + TPR - 1) / TPR;
+    if constexpr (MIN <= 1) if (ch == 1) return k_rmsnorm8<T, TPR, 1, NT><<<grid, threads, 0, st>>>(a);
+    if constexpr (MIN <= 2) if (ch == 2) return k_rmsnorm8<T, TPR, 2, NT><<<grid, threads, 0, st>>>(a);
+    if constexpr (MIN <= 3) if (ch == 3) return k_rmsnorm8<T, TPR, 3, NT><<<grid, threads, 0, st>>>(a);
+    k_rmsnorm8<T, TPR, 4, NT><<<grid, threads, 0, st>>>(a);
 }
 
+// Few rows are bound by their own latency, so a row gets as many threads as it
+// has chunks; many by HBM, so a thread holds up to four chunks, and the
+// outputs bypass the caches.  Measured in bf16 with a residual, few / many form:
+//   1 x 5120 3.2 / 4.2 us; 64 x 1536 2.8 / 4.5 us; 256 x 5120 with plain values
+//   4.6 / 5.3 us; 1024 x 5120 the same 11.2 / 8.8 us; 4096 x 1536 10.2 / 10.0 us.
+// Bypassing stores on 75600 x 5120: 480 -> 466 us (5.8 TB/s); bypassing loads
+// as well gain another 2 % there, but lose 12 % where the rows are still in the
+// memory-side cache (32760 x 1536 fp32: 44 -> 49 us), so they stay plain.
+// Threads to a long row: 20000 x 13824 takes 358 us with 512, 368 us with 256.
 template <class T>
 hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
-    if (a.C <= 2048) launch_norm<T, 64>(a, st);
-    else if (a.C <= 8192) launch_norm<T, 256>(a, st);
-    else launch_norm<T, 1024>(a, st);
+    if (a.N * a.C <= (3ll << 20)) {
+        if (a.C <= 2048) launch_norm<T, 256, 1, false>(a, st);
+        else launch_norm<T, 1024, 1, false>(a, st);
+    } else if (a.C <= 2048) {
+        launch_norm<T, 64, 1, true>(a, st);
+    } else if (a.C <= 8192) {
+        launch_norm<T, 256, 2, true>(a, st);
+    } else if (a.C <= 16384) {
+        launch_norm<T, 512, 3, true>(a, st);
+    } else {
+        launch_norm<T, 1024, 3, true>(a, st);
+    }
     return hipGetLastError();
 }
 

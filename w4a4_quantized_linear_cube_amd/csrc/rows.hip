@@ -350,17 +350,17 @@ __device__ __forceinline__ v4f take_over(__amdgpu_buffer_rsrc_t r, int at) {
 // The general form: a workgroup owns 128 output channels of 16 TB rows over one
 // slice of the K steps, in chunks of CH steps whose operands all its waves
 // share in LDS.  Wave w takes 32 channels (w % 4) of every other step (w / 4).
-// The slice's U is formed too (step w % CH, and of 32 low ranks all, or with
-// CH = 4 the half w / 4) and applied to the slice's sums, both being linear in
-// x, so L1 is read once a tile and step.  The slices' sums meet in the
-// workspace: whichever workgroup of a tile ends last adds them up in slice
-// order, so nothing waits and a result does not depend on the order of arrival.
+// The slice's U is formed too (wave w: step w % 4 of a chunk, 16 of each 32
+// low ranks, w / 4) and applied to the slice's sums, both being linear in x, so
+// L1 is read once a tile and step.  The slices' sums meet in the workspace:
+// whichever workgroup of a tile ends last adds them up in slice order, so
+// nothing waits and a result does not depend on the order of arrival.
 // LP: groups of 32 low ranks (1, also for rank 0, or 4).
 template <int XK, int TB, int LP>
 __global__ __launch_bounds__(512, LP == 1 ? 4 : 2) void k_rows_split(RowsArgs a) {
     constexpr int P = XK == X_F32 ? 3 : 1, CH = 4, J = CH / 2, NP = CH * TB / 2, BLK = 16 * 17;
-    constexpr int UB = CH / 4, US = 8 / CH;            // blocks of 16 ranks a wave forms of 32; ranks' share of a step
-    static_assert(CH * P * TB * BLK >= 8 * TB * 64 * (1 + UB), "sums and U reuse the operands' LDS");
+    constexpr int OUT = 8 * TB * 64;                   // 16-byte places of the tile's sums
+    static_assert(CH * P * TB * BLK >= 2 * OUT, "sums and U reuse the operands' LDS");
     __shared__ uint4 lds[CH * P * TB * BLK];
     __shared__ int arrived;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -368,18 +368,16 @@ __global__ __launch_bounds__(512, LP == 1 ? 4 : 2) void k_rows_split(RowsArgs a)
     const int turn = (int)(blockIdx.x >> 3), tile = (int)(blockIdx.x & 7) + 8 * (turn / a.slices), slice = turn % a.slices;
     if (tile >= a.tiles) return;
     const int n0 = (int)blockIdx.y * 16 * TB, wk = w >> 2, row0 = tile * 128 + 32 * (w & 3);
-    const int k0 = slice * a.per, k1 = min(a.nks, k0 + a.per), passes = a.rp >> 5;
-    const int ug = w % CH, ub = US == 1 ? 0 : wk;      // step of a chunk and first rank block of this wave's U
-    v4f acc[TB][2], u[LP][UB][TB];
+    const int row = row0 + 16 * wk;                    // the 16 channels this wave finishes
+    const int k0 = slice * a.per, k1 = min(a.nks, k0 + a.per), passes = a.rp >> 5, ug = w % CH;
+    v4f acc[TB][2], u[LP][TB];
 #pragma unroll
     for (int t = 0; t < TB; ++t) {
         acc[t][0] = acc[t][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int r = 0; r < LP; ++r)
-#pragma unroll
-            for (int i = 0; i < UB; ++i) u[r][i][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int r = 0; r < LP; ++r) u[r][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    // thread t takes piece t % 16 of token rows t / 16, + 32, .. of a chunk (16 TB rows a step)
+    // thread t takes piece t % 16 of rows t / 16, + 32, .. of a chunk (16 TB rows a step)
     Piece<XK> px[NP];
     auto load_x = [&](int ks) {
 #pragma unroll
@@ -399,12 +397,12 @@ __global__ __launch_bounds__(512, LP == 1 ? 4 : 2) void k_rows_split(RowsArgs a)
         }
     };
     const Stream<2> weight(a, row0, lane);
-    uint4 c[J][2], l1[UB * 4];
+    uint4 c[J][2], l1[4];
     int e[J][2];
     auto load_u = [&](int ks, int r) {                 // (places past the slice: its last step again, not used)
-        const long long at = ((long long)min(ks + ug, k1 - 1) * (a.rp >> 4) + 2 * r + ub) * 256 + lane;
+        const uint4* p = a.l1p + ((long long)min(ks + ug, k1 - 1) * (a.rp >> 4) + 2 * r + wk) * 256 + lane;
 #pragma unroll
-        for (int i = 0; i < UB * 4; ++i) l1[i] = a.l1p[at + i * 64];
+        for (int f = 0; f < 4; ++f) l1[f] = p[f * 64];
     };
     const int rd = (lane & 15) * 17 + 4 * (lane >> 4);
     auto chunk = [&](int ks, auto more) {
@@ -414,15 +412,12 @@ __global__ __launch_bounds__(512, LP == 1 ? 4 : 2) void k_rows_split(RowsArgs a)
         if constexpr (MORE) load_x(ks + CH);
         auto form_u = [&](int r) {
 #pragma unroll
-            for (int i = 0; i < UB; ++i)
+            for (int f = 0; f < 4; ++f)
 #pragma unroll
-                for (int f = 0; f < 4; ++f)
+                for (int t = 0; t < TB; ++t)
 #pragma unroll
-                    for (int t = 0; t < TB; ++t)
-#pragma unroll
-                        for (int p = 0; p < P; ++p)
-                            u[r][i][t] = mfma(__builtin_bit_cast(v8bf, l1[4 * i + f]), lds[((ug * P + p) * TB + t) * BLK + rd + f],
-                                              u[r][i][t]);
+                    for (int p = 0; p < P; ++p)
+                        u[r][t] = mfma(__builtin_bit_cast(v8bf, l1[f]), lds[((ug * P + p) * TB + t) * BLK + rd + f], u[r][t]);
         };
         if (passes && (MORE || ks + ug < k1)) {
             form_u(0);
@@ -456,7 +451,6 @@ __global__ __launch_bounds__(512, LP == 1 ? 4 : 2) void k_rows_split(RowsArgs a)
         }
         __syncthreads();                               // (the operands are read)
     };
-    const int row = row0 + 16 * wk;                    // the 16 channels this wave finishes
     load_x(k0);
     uint4 l2 = make_uint4(0u, 0u, 0u, 0u);
     if (passes) {
@@ -468,9 +462,9 @@ __global__ __launch_bounds__(512, LP == 1 ? 4 : 2) void k_rows_split(RowsArgs a)
     int ks = k0;
     for (; ks + CH < k1; ks += CH) chunk(ks, std::true_type());
     chunk(ks, std::false_type());
-    // each wave finishes the 16 channels wk of its 32: the other half goes to
-    // its partner (w ^ 4) through LDS, and its share of U to every wave
-    v4f *part = (v4f*)lds, *us = part + 8 * TB * 64;
+    // each wave finishes 16 of its 32 channels: the other half goes to its
+    // partner (w ^ 4) through LDS, and its share of U to every wave
+    v4f *part = (v4f*)lds, *us = part + OUT;
 #pragma unroll
     for (int t = 0; t < TB; ++t) part[(w * TB + t) * 64 + lane] = wk ? acc[t][0] : acc[t][1];
     v4f y[TB];
@@ -481,12 +475,8 @@ __global__ __launch_bounds__(512, LP == 1 ? 4 : 2) void k_rows_split(RowsArgs a)
             l2 = load_l2(a, 32 * r, row, lane);
             __syncthreads();
         }
-        if (passes) {
 #pragma unroll
-            for (int i = 0; i < UB; ++i)
-#pragma unroll
-                for (int t = 0; t < TB; ++t) us[((w * UB + i) * TB + t) * 64 + lane] = u[r][i][t];
-        }
+        for (int t = 0; t < TB; ++t) us[(w * TB + t) * 64 + lane] = u[r][t];
         __syncthreads();
         if (r == 0) {
 #pragma unroll
@@ -496,15 +486,15 @@ __global__ __launch_bounds__(512, LP == 1 ? 4 : 2) void k_rows_split(RowsArgs a)
             }
         }
         if (!passes) break;
-        // rank block b of 32 lies in the waves' place b (UB = 2), or in the half b of the waves (UB = 1)
-        const int from = u_place(lane), b = from >> 6, base = (UB == 2 ? b : 4 * b) * TB * 64 + (from & 63);
+        // rank block b of 32 lies with the waves 4 b .. 4 b + 3, a share of the steps each
+        const int from = u_place(lane), base = 4 * (from >> 6) * TB * 64 + (from & 63);
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
             v4f u0 = {0.0f, 0.0f, 0.0f, 0.0f}, u1 = u0;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
-                u0 += us[base + (i * UB * TB + t) * 64];
-                u1 += us[base + (i * UB * TB + t) * 64 + 16];
+                u0 += us[base + (i * TB + t) * 64];
+                u1 += us[base + (i * TB + t) * 64 + 16];
             }
             uint4 up[3];
             split_u(u0, u1, up);
@@ -513,26 +503,27 @@ __global__ __launch_bounds__(512, LP == 1 ? 4 : 2) void k_rows_split(RowsArgs a)
     }
     if (a.slices > 1) {
         const long long unit = (long long)blockIdx.y * a.tiles + tile;
-        const int size = 8 * TB * 64, mine = w * TB * 64 + lane;        // 16-byte places of one slice's sums
-        const __amdgpu_buffer_rsrc_t sums = shared_sums(a.sums + unit * a.slices * size * 4, (size_t)a.slices * size * 16);
+        const int mine = w * TB * 64 + lane;
+        const __amdgpu_buffer_rsrc_t sums = shared_sums(a.sums + unit * a.slices * OUT * 4, (size_t)a.slices * OUT * 16);
 #pragma unroll
-        for (int t = 0; t < TB; ++t) hand_over(sums, slice * size + mine + t * 64, y[t]);
+        for (int t = 0; t < TB; ++t) hand_over(sums, slice * OUT + mine + t * 64, y[t]);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (every wave's sums have arrived before the workgroup says so)
         __syncthreads();
         if (tid == 0) arrived = __hip_atomic_fetch_add(a.arrivals + unit, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         __syncthreads();
         if (arrived != a.slices - 1) return;
-        for (int i = 0; i < a.slices; i += 8) {        // (8 slices' loads in flight)
+        for (int s = 0; s < a.slices; s += 4) {        // (4 slices' loads in flight)
+            v4f v[4][TB];
 #pragma unroll
-            for (int t = 0; t < TB; ++t) {
-                v4f v[8];
+            for (int i = 0; i < 4; ++i)
+                if (s + i < a.slices)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = take_over(sums, min(i + k, a.slices - 1) * size + mine + t * 64);
-                if (i == 0) y[t] = v[0];
+                    for (int t = 0; t < TB; ++t) v[i][t] = take_over(sums, (s + i) * OUT + mine + t * 64);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (i + k > 0 && i + k < a.slices) y[t] += v[k];
-            }
+            for (int i = 0; i < 4; ++i)
+                if (s + i < a.slices)
+#pragma unroll
+                    for (int t = 0; t < TB; ++t) y[t] = s + i ? y[t] + v[i][t] : v[i][t];
         }
         if (tid == 0) a.arrivals[unit] = 0;            // (for the next launch)
     }
