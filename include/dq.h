@@ -352,7 +352,8 @@ void dq_rows_destroy(dq_rows* a);
  *   x_dev [N][Ci] of dtype dt, rows ldx elements apart (ldx >= Ci), 16-byte
  *         aligned rows
  *   y_dev [N][Co] of dtype ydt, rows ldy elements apart (ldy >= Co), every
- *         element of the N rows written, nothing else; must not overlap x
+ *         element of the N rows written, nothing else; must not share memory
+ *         with x (DQ_ERR_INVALID_ARG)
  * fp32 x is taken at its full precision.  Asynchronous on `stream`; allocates
  * nothing and can be captured into a HIP graph. */
 dq_status dq_linear_rows(const dq_weights* w, const void* x_dev, dq_dtype dt, int64_t ldx, int64_t N, dq_rows* a,
@@ -376,7 +377,8 @@ dq_status dq_linear_rows8(const dq_weights* w, const uint8_t* codes_dev, const u
  *   x_dev, res_dev (or NULL), h_dev (or NULL), y_dev (or NULL; v rounded to dt):
  *         [N][C] of dtype dt, rows ld elements apart (ld >= C), 16-byte
  *         aligned rows; h_dev and y_dev may be x_dev or res_dev themselves
- *         (same stride), else they must not overlap them or each other
+ *         (same stride), otherwise no output may share memory with an input
+ *         or another output (DQ_ERR_INVALID_ARG; slices of one wider buffer do not)
  *   gain_dev [C] of dtype gain_dt, 16-byte aligned, or NULL for ones
  *   codes_dev [N][C] 8-byte aligned and scales_dev [N][C/32], dense, or both NULL
  * All on `device`.  Requires C a multiple of `group`, C <= 32768, eps in

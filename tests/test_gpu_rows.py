@@ -71,7 +71,10 @@ def _check(y, x64, rc, rs, l1, l2, parts, ytype):
 SHAPES = [  # n, ci, co, rank
     (1, 32, 1, 0), (1, 256, 16, 1), (1, 1536, 1536, 32), (2, 96, 33, 8), (5, 416, 257, 16), (15, 128, 300, 32), (16, 2080, 1000, 40),
     (1, 5120, 13824, 32), (3, 1024, 16400, 128), (17, 1184, 515, 32), (32, 640, 1027, 64), (33, 992, 260, 0), (47, 2080, 4999, 16),
-    (64, 1536, 770, 32), (65, 544, 300, 32), (130, 288, 290, 96), (8, 13824, 640, 32), (64, 13824, 129, 128)]
+    (64, 1536, 770, 32), (65, 544, 300, 32), (130, 288, 290, 96), (8, 13824, 640, 32), (64, 13824, 129, 128),
+    # every form by rows, rank and output channels: 1, up to 4, up to 16 rows; rank none or up to 32; below 8192 outputs and above
+    (1, 992, 300, 0), (4, 992, 301, 0), (16, 992, 302, 0), (1, 640, 8200, 0), (4, 640, 8201, 0), (12, 640, 8202, 0),
+    (1, 640, 8199, 32), (2, 640, 8200, 17), (16, 640, 8201, 32), (5, 1600, 17000, 32), (1, 20480, 96, 0), (3, 20480, 50, 32), (20, 7712, 33, 5)]
 
 
 @pytest.mark.parametrize("n,ci,co,rank", SHAPES)
@@ -130,6 +133,43 @@ def test_fp32_rows_keep_all_their_bits(dqm):
     dqm.dq_linear_rows(w, torch.from_numpy(x).to(DEV), dqm.dq_rows_create(w, n), y)
     want, _, _ = rows.product(x, rc, rs, None, None)
     assert np.array_equal(y.cpu().numpy().astype(np.float64), want)
+
+
+@pytest.mark.parametrize("code", [0, 1, 3, 64, 190, 250, 252])
+def test_extreme_weight_scales(dqm, code):
+    """Scales 2^-127 to 2^125 against rows that bring the products back to the
+    size of 1: one nonzero channel a row, so each output is one exact product
+    (weights below 2^-126 are subnormal in bf16, and must not vanish)."""
+    ci, co, n = 160, 64, 5
+    rng = np.random.default_rng(code)
+    rc, rs = rng.integers(0, 256, (co, ci // 2), dtype=np.uint8), np.full((co, ci // 32), code, np.uint8)
+    w = dqm.dq_import_weights(rc, rs, None, None)
+    x = np.zeros((n, ci), np.float32)
+    at = rng.integers(0, ci, n)
+    x[np.arange(n), at] = np.ldexp(rng.integers(1, 8, n).astype(np.float32), 127 - code if code > 10 else 120)
+    want, _, _ = rows.product(x, rc, rs, None, None)
+    a = dqm.dq_rows_create(w, 40)
+    for t in (torch.float32, torch.bfloat16):
+        for m in (n, 8 * n):                                  # a form of its own for many rows
+            y = torch.empty(m, co, device=DEV)
+            dqm.dq_linear_rows(w, torch.from_numpy(np.tile(x, (m // n, 1))).to(t).to(DEV), a, y)
+            assert np.array_equal(y.cpu().numpy().astype(np.float64), np.tile(want, (m // n, 1)))
+
+
+def test_two_workspaces_on_two_streams(dqm):
+    """Calls that overlap on one GPU, each with its own workspace."""
+    w, rc, rs, l1, l2 = _weight(dqm, 4096, 640, 32, 31)
+    cases = []
+    for i, n in enumerate((3, 24, 64)):
+        args, x64 = _x(n, 4096, "bf16", i)
+        cases.append((torch.cuda.Stream(), args, x64, dqm.dq_rows_create(w, n), torch.full((n, 640), float("nan"), device=DEV)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for stream, args, _, a, y in cases:
+            dqm.dq_linear_rows(w, *args, a, y, stream)
+    torch.cuda.synchronize()
+    for _, _, x64, _, y in cases:
+        _check(y, x64, rc, rs, l1, l2, 1, "f32")
 
 
 def test_low_rank_alone(dqm):
@@ -324,6 +364,14 @@ def test_refused_on_device(dqm):
     six = dqm.dq_prepare_weights_w6(torch.zeros(40, 64), None, None)
     with pytest.raises(dqm.DQError, match="6-bit"):
         dqm.dq_rows_create(six, 4)
+    with pytest.raises(dqm.DQError, match="overlaps"):
+        both = torch.zeros(4, 104, device=DEV)
+        f(w, both[:, :64], a, both[:, 60:100])
+    codes, scales = torch.zeros(4, 64, dtype=torch.uint8, device=DEV), torch.zeros(4, 2, dtype=torch.uint8, device=DEV)
+    with pytest.raises(dqm.DQError, match="shape"):
+        dqm.dq_linear_rows8(w, codes, scales[:, :1], a, y[:4])
+    with pytest.raises(dqm.DQError, match="cuda:0"):
+        dqm.dq_linear_rows8(w, codes, scales.cpu(), a, y[:4])
     f(w, x[:0], a, y[:0])                                     # no rows: nothing happens
     torch.cuda.synchronize()
     assert (y == 2.0).all()

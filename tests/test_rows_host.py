@@ -2,6 +2,7 @@
 of the binding, and the oracle they are compared with."""
 import ctypes
 import math
+import os
 from types import SimpleNamespace
 
 import numpy as np
@@ -11,6 +12,8 @@ import torch
 from oracle import mx, rows
 from w4a4_quantized_linear_cube_amd import dq
 
+INTERNAL = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "w4a4_quantized_linear_cube_amd", "csrc",
+                        "dq_internal.h")
 A16 = 1 << 20            # an address that is never followed: every call below is refused first
 
 
@@ -35,10 +38,54 @@ def _norm(lib, **kw):
     (1, dict(y=A16 + 64, ldy=64, N=1)),                                 # half a row behind x
     (1, dict(r=4 * A16, ldr=64, h=5 * A16, ldh=64, y=5 * A16, ldy=64)),
     (1, dict(ldx=192, y=A16 + 64, ldy=192)),                            # overlapping columns of one wide buffer
+    (1, dict(ldx=192, y=A16 - 64, ldy=192)),                            # the same from below
+    (1, dict(ldx=192, y=A16 + 192 * 2 - 16, ldy=192)),                  # one row on, less 8 columns
+    (1, dict(codes=A16)), (1, dict(scales=A16 + 511)), (1, dict(codes=2 * A16, scales=2 * A16 + 255)),
+    (1, dict(g=A16 * 2 + 240, gdt=0)), (1, dict(y=2 * A16 + 16, ldy=64)), (1, dict(g=5 * A16, gdt=1, y=5 * A16 - 368, ldy=64)),
 ])
 def test_norm_refusals(lib, status, kw):
     assert _norm(lib, **kw) == status, lib.dq_last_error().decode()
     assert lib.dq_last_error().decode()
+
+
+def test_overlap_rule_against_brute_force(tmp_path):
+    """The rule that the refusals use, on small arrays: bytes that both hold, by
+    listing them; equal pitches exactly, unequal ones by their ranges."""
+    import shutil
+    import subprocess
+    if shutil.which("g++") is None:
+        pytest.skip("needs g++")
+    src = open(INTERNAL).read()
+    body = src[src.index("struct Span {"):src.index("// Makes a handle's device current")]
+    prog = tmp_path / "overlap.cpp"
+    prog.write_text("#include <cstdint>\n#include <cstdio>\n#include <set>\n" + body + """
+int main() {
+    long bad = 0, n = 0;
+    char* base = (char*)4096;
+    for (long pa = 1; pa <= 7; ++pa) for (long wa = 1; wa <= pa; ++wa) for (long pb = pa; pb <= pa + 1; ++pb)
+    for (long wb = 1; wb <= pb; ++wb) for (long at = -24; at <= 24; ++at) for (long ra = 1; ra <= 3; ++ra) for (long rb = 1; rb <= 3; ++rb) {
+        std::set<long> held;
+        for (long r = 0; r < ra; ++r) for (long c = 0; c < wa; ++c) held.insert(r * pa + c);
+        bool real = false;
+        for (long r = 0; r < rb; ++r) for (long c = 0; c < wb; ++c) real |= held.count(at + r * pb + c) > 0;
+        const bool said = overlap(Span{base, ra, pa, wa}, Span{base + at, rb, pb, wb});
+        const bool ranges = at < (ra - 1) * pa + wa && at + (rb - 1) * pb + wb > 0;
+        const bool back = overlap(Span{base + at, rb, pb, wb}, Span{base, ra, pa, wa});
+        if ((real && !said) || said != back || (said && !ranges)) ++bad;             // never missed, the same both ways
+        if (pa == pb && ra == rb && ra > 1 && said && !real && ranges) {             // slices side by side are let through
+            const long d = ((at % pa) + pa) % pa;
+            if (d >= wa && d + wb <= pa) ++bad;
+        }
+        ++n;
+    }
+    printf("%ld of %ld wrong\\n", bad, n);
+    return bad != 0;
+}
+""")
+    exe = tmp_path / "overlap"
+    subprocess.run(["g++", "-std=c++17", "-O1", str(prog), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
 
 
 def test_norm_of_no_rows(lib):

@@ -236,6 +236,24 @@ dq_status upload_factors(dq_weights* w, const uint16_t* l1_host, const uint16_t*
 // DQ_OK for the index of a gfx950 device (asked of the runtime once per device; norm.hip).
 dq_status known_device(int device);
 
+// A caller's array: n rows of `bytes` bytes, `pitch` bytes apart (none where p is null).
+struct Span {
+    const void* p;
+    int64_t n, pitch, bytes;
+};
+// Whether two arrays share memory: their ranges meet, except where rows of one
+// pitch hold disjoint columns (slices of one wider buffer).
+inline bool overlap(const Span& a, const Span& b) {
+    if (!a.p || !b.p) return false;
+    const uintptr_t pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
+    const uintptr_t ea = pa + (uintptr_t)((a.n - 1) * a.pitch + a.bytes), eb = pb + (uintptr_t)((b.n - 1) * b.pitch + b.bytes);
+    if (ea <= pb || eb <= pa) return false;
+    if (a.pitch != b.pitch) return true;
+    const uint64_t pitch = (uint64_t)a.pitch, d = (uint64_t)(pb - pa) % pitch;   // where b's columns begin in a's rows
+    const uint64_t e = pb >= pa ? d : (pitch - (uint64_t)(pa - pb) % pitch) % pitch;
+    return e < (uint64_t)a.bytes || e + (uint64_t)b.bytes > pitch;
+}
+
 // Makes a handle's device current for the scope and restores the caller's.
 struct DeviceGuard {
     int prev = -1;

@@ -247,19 +247,6 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Whether rows of `cols` elements at p (stride ldp) and at q (stride ldq) may
-// share memory in a way other than being the same array: unequal strides in
-// overlapping ranges, or equal strides with overlapping columns.
-bool clashes(const void* p, int64_t ldp, const void* q, int64_t ldq, int64_t n, int64_t cols, int64_t esz) {
-    if (!p || !q || (p == q && ldp == ldq)) return false;
-    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-    const uintptr_t ea = a + (uintptr_t)(((n - 1) * ldp + cols) * esz), eb = b + (uintptr_t)(((n - 1) * ldq + cols) * esz);
-    if (ea <= b || eb <= a) return false;
-    if (ldp != ldq) return true;
-    const uint64_t pitch = (uint64_t)(ldp * esz), d = (a > b ? a - b : b - a) % pitch;
-    return d < (uint64_t)(cols * esz) || pitch - d < (uint64_t)(cols * esz);
-}
-
 }  // namespace
 
 // gfx950 check of a device index, asked of the runtime once per device.
@@ -310,14 +297,18 @@ extern "C" dq_status dq_rmsnorm8(const void* x_dev, int64_t ldx, const void* res
     if ((uintptr_t)gain_dev % 16 != 0) return fail(DQ_ERR_INVALID_ARG, "gain_dev must be 16-byte aligned");
     if ((uintptr_t)codes_dev % 8 != 0) return fail(DQ_ERR_INVALID_ARG, "codes_dev must be 8-byte aligned");
     // (a thread reads its elements of x and the residual before it writes the
-    // same elements, so an output may be one of the inputs, but not overlap it
-    // in another way; outputs may not overlap each other at all)
-    for (const auto& o : {rows[2], rows[3]})
-        for (const auto& i : {rows[0], rows[1]})
-            if (clashes(o.p, o.ld, i.p, i.ld, N, C, esz))
-                return fail(DQ_ERR_INVALID_ARG, std::string(o.name) + " overlaps " + i.name + " without being the same array");
-    if (h_dev && y_dev && (h_dev == y_dev || clashes(h_dev, ldh, y_dev, ldy, N, C, esz)))
-        return fail(DQ_ERR_INVALID_ARG, "h_dev and y_dev overlap");
+    // same elements, so h or y may be one of them; nothing else may share memory)
+    const struct { Span s; const char* name; } all[] = {
+        {{x_dev, N, ldx * esz, C * esz}, "x_dev"}, {{res_dev, N, ldr * esz, C * esz}, "res_dev"},
+        {{gain_dev, 1, C * 4, C * (gain_dt == DQ_BF16 ? 2 : 4)}, "gain_dev"},
+        {{h_dev, N, ldh * esz, C * esz}, "h_dev"}, {{y_dev, N, ldy * esz, C * esz}, "y_dev"},
+        {{codes_dev, N, C, C}, "codes_dev"}, {{scales_dev, N, C / 32, C / 32}, "scales_dev"}};
+    for (int o = 3; o < 7; ++o)
+        for (int i = 0; i < o; ++i) {
+            const bool in_place = o < 5 && i < 2 && all[o].s.p == all[i].s.p && all[o].s.pitch == all[i].s.pitch;
+            if (!in_place && overlap(all[o].s, all[i].s))
+                return fail(DQ_ERR_INVALID_ARG, std::string(all[o].name) + " overlaps " + all[i].name);
+        }
     const dq_status st = known_device(device);
     if (st != DQ_OK) return st;
     DeviceGuard dg(device);

@@ -657,7 +657,7 @@ RowsArgs rows_args(const dq_weights* w, dq_rows* a, int64_t N, void* y, dq_dtype
     r.ldy = ldy;
     r.y_bf16 = ydt == DQ_BF16;
     const int four = ydt == DQ_BF16 ? 8 : 16;       // bytes of a lane's four outputs
-    r.y_wide = (uintptr_t)y % four == 0 && ldy % 4 == 0;
+    r.y_wide = (uintptr_t)y % four == 0 && (N == 1 || ldy % 4 == 0);
     return r;
 }
 
@@ -769,6 +769,8 @@ dq_status dq_linear_rows(const dq_weights* w, const void* x_dev, dq_dtype dt, in
     if ((uintptr_t)x_dev % 16 != 0) return fail(DQ_ERR_INVALID_ARG, "x_dev must be 16-byte aligned");
     if (ldx < w->Ci || ldx > (int64_t(1) << 40) / N || ldx * (dt == DQ_BF16 ? 2 : 4) % 16 != 0)
         return fail(DQ_ERR_SHAPE, "the row stride of x must be at least Ci and a multiple of 16 bytes");
+    const int64_t xs = dt == DQ_BF16 ? 2 : 4, ys = ydt == DQ_BF16 ? 2 : 4;
+    if (overlap({x_dev, N, ldx * xs, w->Ci * xs}, {y_dev, N, ldy * ys, w->Co * ys})) return fail(DQ_ERR_INVALID_ARG, "y_dev overlaps x_dev");
     DeviceGuard dg(a->device);
     if (!dg.ok) return fail(DQ_ERR_DEVICE, "hipSetDevice failed");
     RowsArgs r = rows_args(w, a, N, y_dev, ydt, ldy);
@@ -788,6 +790,10 @@ dq_status dq_linear_rows8(const dq_weights* w, const uint8_t* codes_dev, const u
     if (N == 0) return DQ_OK;
     if (!codes_dev || !scales_dev) return fail(DQ_ERR_INVALID_ARG, "codes_dev or scales_dev is NULL");
     if ((uintptr_t)codes_dev % 8 != 0) return fail(DQ_ERR_INVALID_ARG, "codes_dev must be 8-byte aligned");
+    const int64_t ys = ydt == DQ_BF16 ? 2 : 4;
+    const Span y{y_dev, N, ldy * ys, w->Co * ys};
+    if (overlap({codes_dev, N, w->Ci, w->Ci}, y) || overlap({scales_dev, N, w->Ci / 32, w->Ci / 32}, y))
+        return fail(DQ_ERR_INVALID_ARG, "y_dev overlaps the codes or scales");
     DeviceGuard dg(a->device);
     if (!dg.ok) return fail(DQ_ERR_DEVICE, "hipSetDevice failed");
     RowsArgs r = rows_args(w, a, N, y_dev, ydt, ldy);
