@@ -74,7 +74,8 @@ SHAPES = [  # n, ci, co, rank
     (64, 1536, 770, 32), (65, 544, 300, 32), (130, 288, 290, 96), (8, 13824, 640, 32), (64, 13824, 129, 128),
     # every form by rows, rank and output channels: 1, up to 4, up to 16 rows; rank none or up to 32; below 8192 outputs and above
     (1, 992, 300, 0), (4, 992, 301, 0), (16, 992, 302, 0), (1, 640, 8200, 0), (4, 640, 8201, 0), (12, 640, 8202, 0),
-    (1, 640, 8199, 32), (2, 640, 8200, 17), (16, 640, 8201, 32), (5, 1600, 17000, 32), (1, 20480, 96, 0), (3, 20480, 50, 32), (20, 7712, 33, 5)]
+    (1, 640, 8199, 32), (2, 640, 8200, 17), (16, 640, 8201, 32), (5, 1600, 17000, 32), (64, 3104, 10300, 32), (33, 3104, 10241, 100),
+    (50, 3104, 10250, 0), (1, 20480, 96, 0), (3, 20480, 50, 32), (20, 7712, 33, 5)]
 
 
 @pytest.mark.parametrize("n,ci,co,rank", SHAPES)

@@ -347,33 +347,34 @@ __device__ __forceinline__ v4f take_over(__amdgpu_buffer_rsrc_t r, int at) {
     return __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(r, at * 16, 0, 16));
 }
 
-// The general form: a workgroup owns 128 output channels of 16 TB rows over one
-// slice of the K steps, in chunks of CH steps whose operands all its waves
-// share in LDS.  Wave w takes 32 channels (w % 4) of every other step (w / 4).
+// The general form: a workgroup owns 64 RB output channels of 16 TB rows over
+// one slice of the K steps, in chunks of CH steps whose operands all its waves
+// share in LDS.  Wave w takes 16 RB channels (w % 4) of every other step (w / 4).
 // The slice's U is formed too (wave w: step w % 4 of a chunk, 16 of each 32
 // low ranks, w / 4) and applied to the slice's sums, both being linear in x, so
 // L1 is read once a tile and step.  The slices' sums meet in the workspace:
 // whichever workgroup of a tile ends last adds them up in slice order, so
 // nothing waits and a result does not depend on the order of arrival.
 // LP: groups of 32 low ranks (1, also for rank 0, or 4).
-template <int XK, int TB, int LP>
-__global__ __launch_bounds__(512, LP == 1 ? 4 : 2) void k_rows_split(RowsArgs a) {
+template <int XK, int TB, int LP, int RB>
+__global__ __launch_bounds__(512, LP == 1 && RB == 2 ? 4 : 2) void k_rows_split(RowsArgs a) {
     constexpr int P = XK == X_F32 ? 3 : 1, CH = 4, J = CH / 2, NP = CH * TB / 2, BLK = 16 * 17;
-    constexpr int OUT = 8 * TB * 64;                   // 16-byte places of the tile's sums
-    static_assert(CH * P * TB * BLK >= 2 * OUT, "sums and U reuse the operands' LDS");
-    __shared__ uint4 lds[CH * P * TB * BLK];
+    constexpr int HB = RB / 2, OUT = 8 * TB * HB * 64; // blocks of channels a wave finishes; 16-byte places of the tile's sums
+    constexpr int ALL = OUT + 8 * TB * 64;             // ... with U's shares, where the operands were
+    __shared__ uint4 lds[CH * P * TB * BLK > ALL ? CH * P * TB * BLK : ALL];
     __shared__ int arrived;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     // the slices of a tile go to one XCD (workgroups go to the 8 XCDs in turn)
     const int turn = (int)(blockIdx.x >> 3), tile = (int)(blockIdx.x & 7) + 8 * (turn / a.slices), slice = turn % a.slices;
     if (tile >= a.tiles) return;
-    const int n0 = (int)blockIdx.y * 16 * TB, wk = w >> 2, row0 = tile * 128 + 32 * (w & 3);
-    const int row = row0 + 16 * wk;                    // the 16 channels this wave finishes
+    const int n0 = (int)blockIdx.y * 16 * TB, wk = w >> 2, row0 = tile * 64 * RB + 16 * RB * (w & 3);
+    const int row = row0 + 16 * HB * wk;               // the 16 HB channels this wave finishes
     const int k0 = slice * a.per, k1 = min(a.nks, k0 + a.per), passes = a.rp >> 5, ug = w % CH;
-    v4f acc[TB][2], u[LP][TB];
+    v4f acc[TB][RB], u[LP][TB];
 #pragma unroll
     for (int t = 0; t < TB; ++t) {
-        acc[t][0] = acc[t][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < RB; ++i) acc[t][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int r = 0; r < LP; ++r) u[r][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
@@ -396,9 +397,9 @@ __global__ __launch_bounds__(512, LP == 1 ? 4 : 2) void k_rows_split(RowsArgs a)
             for (int p = 0; p < P; ++p) lds[((g * P + p) * TB * 16 + n) * 17 + (tid & 15)] = part[p];
         }
     };
-    const Stream<2> weight(a, row0, lane);
-    uint4 c[J][2], l1[4];
-    int e[J][2];
+    const Stream<RB> weight(a, row0, lane);
+    uint4 c[J][RB], l1[4], l2[HB];
+    int e[J][RB];
     auto load_u = [&](int ks, int r) {                 // (places past the slice: its last step again, not used)
         const uint4* p = a.l1p + ((long long)min(ks + ug, k1 - 1) * (a.rp >> 4) + 2 * r + wk) * 256 + lane;
 #pragma unroll
@@ -436,43 +437,49 @@ __global__ __launch_bounds__(512, LP == 1 ? 4 : 2) void k_rows_split(RowsArgs a)
             if (!MORE && ks + g >= k1) break;
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
-                const v8bf w0 = weight8(word(c[j][0], f), pow2f(e[j][0] - 127));
-                const v8bf w1 = weight8(word(c[j][1], f), pow2f(e[j][1] - 127));
+                v8bf wv[RB];
+#pragma unroll
+                for (int i = 0; i < RB; ++i) wv[i] = weight8(word(c[j][i], f), pow2f(e[j][i] - 127));
 #pragma unroll
                 for (int t = 0; t < TB; ++t)
 #pragma unroll
                     for (int p = 0; p < P; ++p) {
                         const uint4 x = lds[((g * P + p) * TB + t) * BLK + rd + f];
-                        acc[t][0] = mfma(w0, x, acc[t][0]);
-                        acc[t][1] = mfma(w1, x, acc[t][1]);
+#pragma unroll
+                        for (int i = 0; i < RB; ++i) acc[t][i] = mfma(wv[i], x, acc[t][i]);
                     }
             }
             if constexpr (MORE) weight.fetch(min(ks + CH + g, k1 - 1), c[j], e[j]);
         }
         __syncthreads();                               // (the operands are read)
     };
+    auto load_l2s = [&](int r) {
+#pragma unroll
+        for (int i = 0; i < HB; ++i) l2[i] = load_l2(a, 32 * r, row + 16 * i, lane);
+    };
     load_x(k0);
-    uint4 l2 = make_uint4(0u, 0u, 0u, 0u);
     if (passes) {
         load_u(k0, 0);
-        l2 = load_l2(a, 0, row, lane);
+        load_l2s(0);
     }
 #pragma unroll
     for (int j = 0; j < J; ++j) weight.fetch(min(k0 + 2 * j + wk, k1 - 1), c[j], e[j]);
     int ks = k0;
     for (; ks + CH < k1; ks += CH) chunk(ks, std::true_type());
     chunk(ks, std::false_type());
-    // each wave finishes 16 of its 32 channels: the other half goes to its
+    // each wave finishes one half of its channels: the other half goes to its
     // partner (w ^ 4) through LDS, and its share of U to every wave
     v4f *part = (v4f*)lds, *us = part + OUT;
 #pragma unroll
-    for (int t = 0; t < TB; ++t) part[(w * TB + t) * 64 + lane] = wk ? acc[t][0] : acc[t][1];
-    v4f y[TB];
+    for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int i = 0; i < HB; ++i) part[((w * TB + t) * HB + i) * 64 + lane] = wk ? acc[t][i] : acc[t][HB + i];
+    v4f y[TB][HB];
 #pragma unroll
     for (int r = 0; r < LP; ++r) {
         if (r && r >= passes) break;
         if (r) {
-            l2 = load_l2(a, 32 * r, row, lane);
+            load_l2s(r);
             __syncthreads();
         }
 #pragma unroll
@@ -480,10 +487,12 @@ __global__ __launch_bounds__(512, LP == 1 ? 4 : 2) void k_rows_split(RowsArgs a)
         __syncthreads();
         if (r == 0) {
 #pragma unroll
-            for (int t = 0; t < TB; ++t) {
-                const v4f other = part[((w ^ 4) * TB + t) * 64 + lane];
-                y[t] = wk ? other + acc[t][1] : acc[t][0] + other;
-            }
+            for (int t = 0; t < TB; ++t)
+#pragma unroll
+                for (int i = 0; i < HB; ++i) {
+                    const v4f other = part[(((w ^ 4) * TB + t) * HB + i) * 64 + lane];
+                    y[t][i] = wk ? other + acc[t][HB + i] : acc[t][i] + other;
+                }
         }
         if (!passes) break;
         // rank block b of 32 lies with the waves 4 b .. 4 b + 3, a share of the steps each
@@ -498,37 +507,42 @@ __global__ __launch_bounds__(512, LP == 1 ? 4 : 2) void k_rows_split(RowsArgs a)
             }
             uint4 up[3];
             split_u(u0, u1, up);
-            y[t] = low_rank(l2, up, y[t]);
+#pragma unroll
+            for (int i = 0; i < HB; ++i) y[t][i] = low_rank(l2[i], up, y[t][i]);
         }
     }
     if (a.slices > 1) {
         const long long unit = (long long)blockIdx.y * a.tiles + tile;
-        const int mine = w * TB * 64 + lane;
+        const int mine = w * TB * HB * 64 + lane;
         const __amdgpu_buffer_rsrc_t sums = shared_sums(a.sums + unit * a.slices * OUT * 4, (size_t)a.slices * OUT * 16);
 #pragma unroll
-        for (int t = 0; t < TB; ++t) hand_over(sums, slice * OUT + mine + t * 64, y[t]);
+        for (int t = 0; t < TB; ++t)
+#pragma unroll
+            for (int i = 0; i < HB; ++i) hand_over(sums, slice * OUT + mine + (t * HB + i) * 64, y[t][i]);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (every wave's sums have arrived before the workgroup says so)
         __syncthreads();
         if (tid == 0) arrived = __hip_atomic_fetch_add(a.arrivals + unit, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         __syncthreads();
         if (arrived != a.slices - 1) return;
         for (int s = 0; s < a.slices; s += 4) {        // (4 slices' loads in flight)
-            v4f v[4][TB];
+            v4f v[4][TB * HB];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (s + i < a.slices)
+            for (int k = 0; k < 4; ++k)
+                if (s + k < a.slices)
 #pragma unroll
-                    for (int t = 0; t < TB; ++t) v[i][t] = take_over(sums, (s + i) * OUT + mine + t * 64);
+                    for (int i = 0; i < TB * HB; ++i) v[k][i] = take_over(sums, (s + k) * OUT + mine + i * 64);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (s + i < a.slices)
+            for (int k = 0; k < 4; ++k)
+                if (s + k < a.slices)
 #pragma unroll
-                    for (int t = 0; t < TB; ++t) y[t] = s + i ? y[t] + v[i][t] : v[i][t];
+                    for (int i = 0; i < TB * HB; ++i) y[i / HB][i % HB] = s + k ? y[i / HB][i % HB] + v[k][i] : v[k][i];
         }
         if (tid == 0) a.arrivals[unit] = 0;            // (for the next launch)
     }
 #pragma unroll
-    for (int t = 0; t < TB; ++t) store_y(a, n0 + 16 * t + (lane & 15), row + 4 * (lane >> 4), y[t]);
+    for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int i = 0; i < HB; ++i) store_y(a, n0 + 16 * t + (lane & 15), row + 16 * i + 4 * (lane >> 4), y[t][i]);
 }
 
 template <int XK, int N16, int LR, int RB, int W, int D>
@@ -537,12 +551,12 @@ void launch_direct(RowsArgs a, hipStream_t st) {
     k_rows_direct<XK, N16, LR, RB, W, D><<<(unsigned)round_up(a.tiles, 8), 64 * W, 0, st>>>(a);
 }
 
-// How the general form splits N rows of a weight: 16 tb rows to a tile, K
-// slices of `per` steps.
+// How the general form splits N rows of a weight: tiles of 64 rb channels and
+// 16 tb rows, K slices of `per` steps.
 struct SplitPlan {
-    int tb, groups, tiles, slices, per;
+    int tb, rb, groups, tiles, slices, per;
     int64_t units() const { return (int64_t)groups * tiles; }
-    int64_t sum_floats() const { return slices > 1 ? units() * slices * 8 * tb * 256 : 0; }
+    int64_t sum_floats() const { return slices > 1 ? units() * slices * 4 * rb * tb * 256 : 0; }
 };
 // `parts` of a row: three for fp32 rows, whose larger operands leave LDS for
 // 16 rows at a time.
@@ -550,7 +564,13 @@ SplitPlan plan_split(int64_t N, int64_t Co, int nks, int parts) {
     SplitPlan p;
     p.tb = N <= 16 || parts > 1 ? 1 : 2;
     p.groups = (int)((N + 16 * p.tb - 1) / (16 * p.tb));
-    p.tiles = (int)((Co + 127) / 128);
+    // 256 channels to a tile halve what is read again of x and L1.  They pay for
+    // several groups of rows where the tiles still fill a third of the chip and K
+    // is long: 64 rows 5120 -> 10240 20.9 -> 15.7 us, -> 13824 21.3 -> 18.4 us; but
+    // 5120 -> 5120 12.1 -> 20.0 us, 1536 -> 10240 9.2 -> 10.4 us, and 20 rows 5120 ->
+    // 10240 13.1 -> 14.2 us
+    p.rb = p.groups > 1 && parts == 1 && (Co + 255) / 256 * p.groups >= 80 && nks >= 24 ? 4 : 2;
+    p.tiles = (int)((Co + 64 * p.rb - 1) / (64 * p.rb));
     const int64_t target = parts > 1 && p.groups > 1 ? 2 * SPLIT_TARGET : SPLIT_TARGET;
     const int64_t most = std::max<int64_t>(1, target / p.units());
     p.per = (int)std::max<int64_t>(std::min(nks, 2), (nks + most - 1) / most);
@@ -558,14 +578,14 @@ SplitPlan plan_split(int64_t N, int64_t Co, int nks, int parts) {
     return p;
 }
 
-template <int XK, int TB>
+template <int XK, int TB, int RB>
 void launch_split(RowsArgs a, const SplitPlan& p, hipStream_t st) {
     a.tiles = p.tiles;
     a.slices = p.slices;
     a.per = p.per;
     const dim3 grid((unsigned)(round_up(p.tiles, 8) * p.slices), (unsigned)p.groups);
-    if (a.rp <= 32) k_rows_split<XK, TB, 1><<<grid, 512, 0, st>>>(a);
-    else k_rows_split<XK, TB, 4><<<grid, 512, 0, st>>>(a);
+    if (a.rp <= 32) k_rows_split<XK, TB, 1, RB><<<grid, 512, 0, st>>>(a);
+    else k_rows_split<XK, TB, 4, RB><<<grid, 512, 0, st>>>(a);
 }
 
 template <int XK>
@@ -587,8 +607,8 @@ hipError_t launch_rows_product(const RowsArgs& a, hipStream_t st) {
         if (a.Co >= 8192) a.rp ? go(some, four) : go(none, four);
         else a.rp ? go(some, two) : go(none, two);
     } else {
-        if (p.tb == 1) launch_split<XK, 1>(a, p, st);
-        else if constexpr (P == 1) launch_split<XK, 2>(a, p, st);
+        if (p.tb == 1) launch_split<XK, 1, 2>(a, p, st);
+        else if constexpr (P == 1) p.rb == 2 ? launch_split<XK, 2, 2>(a, p, st) : launch_split<XK, 2, 4>(a, p, st);
     }
     return hipGetLastError();
 }
