@@ -206,3 +206,16 @@ def test_oracle_product_is_the_dense_one():
     y, main, low = rows.product(x, rc, rs, l1, l2)
     np.testing.assert_allclose(y, x @ dense, rtol=0, atol=1e-12 * float((main + low).max()))
     assert (np.abs(y) <= (main + low) * (1 + 1e-12)).all()
+
+
+def test_binding_names_its_calls():
+    """Every status that the binding checks is checked under one function's name."""
+    import ast
+    import inspect
+    tree = ast.parse(inspect.getsource(dq))
+    calls = [c for c in ast.walk(tree) if isinstance(c, ast.Call) and isinstance(c.func, ast.Name) and c.func.id == "_check"]
+    assert len(calls) > 30
+    for c in calls:
+        assert len(c.args) == 2 and not c.keywords, ast.unparse(c)
+        if isinstance(c.args[1], ast.Constant):
+            assert c.args[1].value in dq.EXPORTS, ast.unparse(c)

@@ -515,8 +515,7 @@ def dq_orbit_linear(o: Orbit, x, a: OrbitAct, y, stream=None):
 def dq_orbit_act_export(a: OrbitAct, stream=None) -> dict:
     out = dict(codes=np.zeros((a.N, a.weights.Ci // 2), np.uint8), scale=np.zeros(a.N, np.float32))
     _check(load().dq_orbit_act_export(a.handle, _ptr(out["codes"]), _ptr(out["scale"]), _stream(stream)),
-           "dq_orbit_act_export", "dq_import_weights", "dq_rows_create", "dq_rows_destroy", "dq_linear_rows",
-           "dq_linear_rows8", "dq_rmsnorm8")
+           "dq_orbit_act_export")
     return out
 
 
