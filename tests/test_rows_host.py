@@ -219,3 +219,16 @@ def test_binding_names_its_calls():
         assert len(c.args) == 2 and not c.keywords, ast.unparse(c)
         if isinstance(c.args[1], ast.Constant):
             assert c.args[1].value in dq.EXPORTS, ast.unparse(c)
+
+
+def test_one_hip_runtime():
+    """The library loaded first, torch after it: both use one HIP runtime (with
+    two, neither knows the other's streams and memory)."""
+    import subprocess
+    import sys
+    prog = ("from w4a4_quantized_linear_cube_amd import dq; dq.load(); import torch; "
+            "print(len({l.split()[-1] for l in open('/proc/self/maps') if 'libamdhip64' in l}))")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", prog], capture_output=True, text=True, cwd=root, timeout=300)
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.split()[-1] == "1", r.stdout

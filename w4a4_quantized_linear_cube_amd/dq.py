@@ -58,6 +58,7 @@ def load():
     path = library_path()
     if not os.path.exists(path):
         raise RuntimeError(f"{path} is not built; run __graft_entry__.build()")
+    import torch  # noqa: F401  (before libdq.so, which then shares the HIP runtime that torch brings)
     lib = ctypes.CDLL(path)
     P, I32, I64, U64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
     PP = ctypes.POINTER(ctypes.c_void_p)
@@ -111,7 +112,6 @@ def load():
         f = getattr(lib, name)
         f.argtypes = args
         f.restype = res
-    import torch  # noqa: F401  (the native part links against its libraries)
     from . import _dqcall
     _CALL = _dqcall
     _LIB = lib
