@@ -31,11 +31,11 @@
  *    faults of enqueued work surface at the caller's next synchronisation.
  *    dq_last_error() gives a message for the last failure on this thread.
  *  - Streams are hipStream_t values passed as void*; NULL is the null stream.
- *  - All allocation happens in dq_prepare_weights* and dq_qact_create; the
- *    hot calls (dq_quantize_act, dq_linear_forward, dq_linear) allocate
- *    nothing.
+ *  - All allocation happens in dq_prepare_weights*, dq_import_weights and the
+ *    handles' dq_*_create; the hot calls (dq_quantize_act, dq_linear_forward,
+ *    dq_linear, dq_linear_rows*, dq_rmsnorm8) allocate nothing.
  *  - A dq_weights is read-only after preparation and may be shared by
- *    streams; a dq_qact must not be used by two streams at once.
+ *    streams; a dq_qact or dq_rows must not be used by two streams at once.
  */
 #ifndef DQ_H
 #define DQ_H
@@ -340,8 +340,8 @@ dq_status dq_import_weights(const uint8_t* rcodes_host, const uint8_t* rscales_h
 /* Workspace for up to max_rows rows (1 <= max_rows <= 4096) of a 4-bit weight
  * with Ci <= 65536, or of any other with the same Ci, Co and rank on its
  * device.  Tuned for up
- * to 64 rows; more are taken 64 at a time, each group reading the weight
- * again.  Must not be used by two streams at once (two captured graphs that
+ * to 64 rows; more than 16 are taken 32 at a time (16 of fp32 rows), each
+ * group reading the weight again.  Must not be used by two streams at once (two captured graphs that
  * share one must not run at once either). */
 typedef struct dq_rows dq_rows;
 dq_status dq_rows_create(const dq_weights* w, int64_t max_rows, dq_rows** out);
@@ -354,7 +354,9 @@ void dq_rows_destroy(dq_rows* a);
  *   y_dev [N][Co] of dtype ydt, rows ldy elements apart (ldy >= Co), every
  *         element of the N rows written, nothing else; must not share memory
  *         with x (DQ_ERR_INVALID_ARG)
- * fp32 x is taken at its full precision.  Asynchronous on `stream`; allocates
+ * fp32 x is taken at its full precision, bits below 2^-133 apart; weights and
+ * MX-FP8 values as bf16 holds them (exact from 2^-133 to 2^128, infinite from
+ * there).  Infinite and NaN values stay in their rows.  Asynchronous on `stream`; allocates
  * nothing and can be captured into a HIP graph. */
 dq_status dq_linear_rows(const dq_weights* w, const void* x_dev, dq_dtype dt, int64_t ldx, int64_t N, dq_rows* a,
                          void* y_dev, dq_dtype ydt, int64_t ldy, void* stream);

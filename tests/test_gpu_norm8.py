@@ -236,3 +236,20 @@ def test_refused_on_device(dqm):
     with pytest.raises(dqm.DQError, match="overlap"):
         buf = torch.zeros(5, 64, device=DEV)
         dqm.dq_rmsnorm8(buf[:4], None, 1e-6, codes, scales, y=buf[1:])
+
+
+def test_more_rows_than_one_launch_takes(dqm):
+    """2^26 rows and a few, of 32 channels: offsets past 32 bits, and more threads than a launch may have."""
+    _say("norm of 2^26 + 700 rows")
+    period, n, c = 1 << 14, (1 << 26) + 700, 32
+    base = torch.randn(period, c, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
+    few = [torch.empty(period, k, dtype=torch.uint8, device=DEV) for k in (c, 1)]
+    dqm.dq_rmsnorm8(base, None, 1e-6, *few)
+    x = base.repeat(n // period + 1, 1)[:n]
+    codes, scales = (torch.full((n + 1, k), 0xA5, dtype=torch.uint8, device=DEV) for k in (c, 1))
+    dqm.dq_rmsnorm8(x, None, 1e-6, codes[:n], scales[:n])
+    for got, want in zip((codes, scales), few):
+        whole = n // period * period
+        assert (got[:whole].view(-1, period, got.shape[1]) == want).all()
+        assert torch.equal(got[whole:n], want[:n - whole])
+        assert (got[n:] == 0xA5).all()

@@ -376,3 +376,113 @@ def test_refused_on_device(dqm):
     f(w, x[:0], a, y[:0])                                     # no rows: nothing happens
     torch.cuda.synchronize()
     assert (y == 2.0).all()
+
+
+@pytest.mark.parametrize("rank", [0, 5, 32, 37, 128])
+@pytest.mark.parametrize("n", [1, 3, 20])
+def test_infinite_channels_with_low_ranks(dqm, n, rank):
+    """Positive weights and factors: a row with an infinite channel is infinite,
+    also where the rank does not fill its padded width; a NaN stays in its row."""
+    ci, co = 288, 140
+    rng = np.random.default_rng(rank)
+    rc = (rng.integers(1, 8, (co, ci // 2)) | rng.integers(1, 8, (co, ci // 2)) << 4).astype(np.uint8)
+    rs = np.full((co, ci // 32), 127, np.uint8)
+    bits = lambda v: mx.f32_to_bf16_bits(v.astype(np.float32))
+    l1, l2 = (bits(rng.integers(1, 4, s)) for s in ((ci, rank), (rank, co)))
+    w = dqm.dq_import_weights(rc, rs, l1 if rank else None, l2 if rank else None)
+    a = dqm.dq_rows_create(w, n)
+    x = torch.ones(n, ci)
+    x[0, 287] = float("-inf")
+    if n > 2:
+        x[2, 3] = float("nan")
+    for t in (torch.float32, torch.bfloat16):
+        y = torch.zeros(n, co, device=DEV)
+        dqm.dq_linear_rows(w, x.to(t).to(DEV), a, y)
+        assert (y[0] == float("-inf")).all()
+        assert n == 1 or torch.isnan(y[2]).all() and torch.isfinite(y[[i for i in range(1, n) if i != 2]]).all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "mx8"])
+@pytest.mark.parametrize("n", [2, 24])
+def test_tiny_values(dqm, n, kind):
+    """Values of multiples of 2^-133 (subnormal parts in bf16) against scales of
+    2^120, one a row.  An fp32 value here has up to 23 bits and a weight 2, so
+    their product has up to 25 and takes one rounding (the first two parts'
+    products have 10 bits each and sum exactly; only the third addition
+    rounds, by 2^-23 of the sum where it truncates); an MX-FP8 product is exact."""
+    ci, co = 96, 50
+    rng = np.random.default_rng(n)
+    rc, rs = rng.integers(0, 256, (co, ci // 2), dtype=np.uint8), np.full((co, ci // 32), 247, np.uint8)
+    w = dqm.dq_import_weights(rc, rs, None, None)
+    a, y = dqm.dq_rows_create(w, n), torch.empty(n, co, device=DEV)
+    at = rng.integers(0, ci, n)
+    if kind == "f32":
+        x = np.zeros((n, ci), np.float32)
+        x[np.arange(n), at] = np.ldexp(rng.integers(2 ** 19, 2 ** 22, n).astype(np.float32) * 2 + 1, -133)
+        args = (torch.from_numpy(x).to(DEV),)
+    else:
+        codes, scales = np.zeros((n, ci), np.uint8), np.full((n, ci // 32), 3, np.uint8)       # 2^-124, least code 2^-9
+        codes[np.arange(n), at] = rng.integers(1, 0x7F, n)
+        args, x = (torch.from_numpy(codes).to(DEV), torch.from_numpy(scales).to(DEV)), mx.mx_dequantize(codes, scales, "fp8")
+    _call(dqm, w, args, a, y)
+    want, _, _ = rows.product(x, rc, rs, None, None)
+    assert (np.abs(y.cpu().numpy() - want) <= (2.0 ** -23 if kind == "f32" else 0.0) * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("n,ci,co,rank", [(1, 8320, 200, 32), (24, 1024, 130, 40), (64, 3104, 10250, 32)])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_shared_tiles_in_graphs(dqm, n, ci, co, rank, kind):
+    """Products whose tiles several workgroups share, captured and replayed on new rows, with eager calls through the same workspace between."""
+    w, *_ = _weight(dqm, ci, co, rank, ci)
+    a = dqm.dq_rows_create(w, n)
+    many = [_x(n, ci, kind, 50 + i)[0][0] for i in range(3)]
+    x, y = torch.empty_like(many[0]), torch.empty(n, co, device=DEV)
+
+    def eager(i):
+        x.copy_(many[i])
+        dqm.dq_linear_rows(w, x, a, y)
+        return y.clone()
+
+    want = [eager(i) for i in range(3)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dqm.dq_linear_rows(w, x, a, y)
+        dqm.dq_linear_rows(w, x, a, y)                        # (one after the other: the workspace is ready for the next)
+    for i in (1, 0, 2, 1):
+        x.copy_(many[i])
+        y.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[i]), i
+        assert torch.equal(eager(2), want[2])
+
+
+def test_host_threads(dqm):
+    """Calls from several threads on one weight, each with its own workspace and stream (given as its raw value)."""
+    import threading
+    n, ci, co = 20, 1536, 300
+    w, rc, rs, l1, l2 = _weight(dqm, ci, co, 32, 3)
+    args, x64 = _x(n, ci, "mx8", 4)
+    jobs = [(dqm.dq_rows_create(w, n), torch.full((n, co), float("nan"), device=DEV), torch.cuda.Stream()) for _ in range(4)]
+    torch.cuda.synchronize()
+    errors = []
+
+    def run(a, y, stream):
+        try:
+            for _ in range(50):
+                dqm.dq_linear_rows8(w, *args, a, y, stream.cuda_stream)
+            with pytest.raises(dqm.DQError, match="max_rows"):
+                dqm.dq_linear_rows8(w, *(torch.cat((t, t)) for t in args), a, torch.cat((y, y)))
+        except BaseException as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for _, y, _ in jobs:
+        _check(y, x64, rc, rs, l1, l2, 1, "f32")

@@ -83,6 +83,12 @@ bool output(PyObject* o, int64_t n, const Pair& p, Matrix* y, dq_dtype* d) {
     return matrix(o, 1, y) && y->n == n && y->c == p.Co && y->device == p.device && dtype_of(y->type, d);
 }
 
+// Other Python threads run while a call enqueues (it may wait for room in the queue).
+struct Released {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Released() { PyEval_RestoreThread(state); }
+};
+
 // Runs `body`; None where it finds the arguments unfit or torch objects to them.
 template <class Body>
 PyObject* guarded(Body body) {
@@ -108,6 +114,7 @@ PyObject* linear_rows(PyObject*, PyObject* const* v, Py_ssize_t n) {
         if (n != 4 || !pair_of(v[0], &p) || !matrix(v[1], 16, &x) || x.c != p.Ci || x.device != p.device || !dtype_of(x.type, &dx) ||
             !output(v[2], x.n, p, &y, &dy) || !stream_of(v[3], p.device, &stream))
             return false;
+        Released released;
         *status = dq_linear_rows(p.w, x.p, dx, x.ld, x.n, p.a, y.p, dy, y.ld, stream);
         return true;
     });
@@ -123,6 +130,7 @@ PyObject* linear_rows8(PyObject*, PyObject* const* v, Py_ssize_t n) {
         if (n != 5 || !pair_of(v[0], &p) || !mx8(v[1], v[2], p.device, &c, &s) || c.c != p.Ci || !output(v[3], c.n, p, &y, &dy) ||
             !stream_of(v[4], p.device, &stream))
             return false;
+        Released released;
         *status = dq_linear_rows8(p.w, (const uint8_t*)c.p, (const uint8_t*)s.p, c.n, p.a, y.p, dy, y.ld, stream);
         return true;
     });
@@ -153,6 +161,7 @@ PyObject* rmsnorm8(PyObject*, PyObject* const* v, Py_ssize_t n) {
             }
         const long group = PyLong_AsLong(v[8]);
         if ((group != 32 && group != 64) || !stream_of(v[9], x.device, &stream)) return false;
+        Released released;
         *status = dq_rmsnorm8(x.p, x.ld, more[0].p, more[0].ld, dx, gain, dg, PyFloat_AS_DOUBLE(v[2]), x.n, x.c, (int32_t)group,
                               more[1].p, more[1].ld, (uint8_t*)c.p, (uint8_t*)s.p, more[2].p, more[2].ld, x.device, stream);
         return true;

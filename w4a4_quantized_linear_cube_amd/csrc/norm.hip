@@ -11,6 +11,7 @@
 // to the border of two codes goes by the last bit of f).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -32,7 +33,7 @@ struct NormArgs {
     void* y;            // v in the stream's type, or null
     uint8_t* codes;     // or null
     uint8_t* scales;
-    long long N, ldx, ldr, ldh, ldy;
+    long long first, N, ldx, ldr, ldh, ldy;   // first: row of the launch's first block
     int C, wide;        // wide: one scale for 64 channels
     int g_bf16;
     double eps;
@@ -110,7 +111,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm8(NormArgs a) 
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
     constexpr int WPR = TPR / 64;
     const int t = threadIdx.x % TPR;
-    const long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
+    const long long row = a.first + (long long)blockIdx.x * RPB + threadIdx.x / TPR;
     const bool live = row < a.N;
     const int nch = a.C >> 3;
     float h[CH][8];
@@ -209,16 +210,20 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm8(NormArgs a) 
     }
 }
 
-// C / 8 chunks over TPR threads: MIN to 4 each.
+// C / 8 chunks over TPR threads: MIN to 4 each.  A launch takes fewer than 2^32
+// threads, so more rows than that are several launches.
 template <class T, int TPR, int MIN, bool NT>
-void launch_norm(const NormArgs& a, hipStream_t st) {
-    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
-    const unsigned grid = (unsigned)((a.N + RPB - 1) / RPB);
-    const int threads = TPR < 256 ? 256 : TPR, ch = (a.C / 8 + TPR - 1) / TPR;
-    if constexpr (MIN <= 1) if (ch == 1) return k_rmsnorm8<T, TPR, 1, NT><<<grid, threads, 0, st>>>(a);
-    if constexpr (MIN <= 2) if (ch == 2) return k_rmsnorm8<T, TPR, 2, NT><<<grid, threads, 0, st>>>(a);
-    if constexpr (MIN <= 3) if (ch == 3) return k_rmsnorm8<T, TPR, 3, NT><<<grid, threads, 0, st>>>(a);
-    k_rmsnorm8<T, TPR, 4, NT><<<grid, threads, 0, st>>>(a);
+void launch_norm(NormArgs a, hipStream_t st) {
+    constexpr int RPB = TPR < 256 ? 256 / TPR : 1, THREADS = TPR < 256 ? 256 : TPR;
+    constexpr long long MOST = (1ll << 31) / THREADS;
+    const int ch = (a.C / 8 + TPR - 1) / TPR;
+    const auto go = [&](unsigned grid) {
+        if constexpr (MIN <= 1) if (ch == 1) return k_rmsnorm8<T, TPR, 1, NT><<<grid, THREADS, 0, st>>>(a);
+        if constexpr (MIN <= 2) if (ch == 2) return k_rmsnorm8<T, TPR, 2, NT><<<grid, THREADS, 0, st>>>(a);
+        if constexpr (MIN <= 3) if (ch == 3) return k_rmsnorm8<T, TPR, 3, NT><<<grid, THREADS, 0, st>>>(a);
+        k_rmsnorm8<T, TPR, 4, NT><<<grid, THREADS, 0, st>>>(a);
+    };
+    for (; a.first < a.N; a.first += MOST * RPB) go((unsigned)std::min(MOST, (a.N - a.first + RPB - 1) / RPB));
 }
 
 // Few rows are bound by their own latency, so a row gets as many threads as it
@@ -313,7 +318,7 @@ extern "C" dq_status dq_rmsnorm8(const void* x_dev, int64_t ldx, const void* res
     if (st != DQ_OK) return st;
     DeviceGuard dg(device);
     if (!dg.ok) return fail(DQ_ERR_DEVICE, "hipSetDevice failed");
-    const NormArgs a{x_dev, res_dev, gain_dev, h_dev, y_dev, codes_dev, scales_dev, (long long)N, (long long)ldx,
+    const NormArgs a{x_dev, res_dev, gain_dev, h_dev, y_dev, codes_dev, scales_dev, 0, (long long)N, (long long)ldx,
                      (long long)ldr, (long long)ldh, (long long)ldy, (int)C, group == 64, gain_dt == DQ_BF16, eps};
     const hipError_t e = dt == DQ_BF16 ? launch_norm<uint16_t>(a, (hipStream_t)stream) : launch_norm<float>(a, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "norm launch");

@@ -11,6 +11,7 @@
 // not need the decoding, but keeps only about 13 bits of its products' sum.)
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstring>
 #include <memory>
 #include <new>
@@ -39,7 +40,7 @@ struct RowsArgs {
     const void* x;                        // rows (bf16, fp32) or E4M3 codes
     const uint8_t* xs;                    // E8M0 codes of MX-FP8 rows
     long long ldx;
-    int N, Ci, nks, Co, rp, y_bf16, y_wide, tiles, slices, per;
+    int N, Ci, nks, Co, rank, rp, y_bf16, y_wide, tiles, slices, per;
     const uint8_t *rq, *rs;
     const uint4* l1p;
     const uint16_t* l2t;
@@ -144,12 +145,19 @@ __device__ __forceinline__ v4f mfma(v8bf w, uint4 x, v4f acc) {
 // matrix instruction with ranks 4 g .. + 3 of row n in lane 16 g + n; as an
 // operand, lane l needs ranks 8 (l / 16) .. + 7 of row l % 16, which two lanes
 // 16 apart hold, the first of them in place u_place(l) of two blocks' 128.
+// Ranks past the last are zeros whatever x holds (an infinite channel makes
+// its product with a padding column NaN); `left` ranks remain from the lane's first.
 __device__ __forceinline__ int u_place(int lane) {
     const int q = lane >> 4;
     return (q >> 1) * 64 + 32 * (q & 1) + (lane & 15);
 }
-__device__ __forceinline__ void split_u(v4f u0, v4f u1, uint4* part) {
-    const float f[8] = {u0[0], u0[1], u0[2], u0[3], u1[0], u1[1], u1[2], u1[3]};
+__device__ __forceinline__ void split_u(v4f u0, v4f u1, int left, uint4* part) {
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[j] = j < left ? u0[j] : 0.0f;
+        f[4 + j] = 4 + j < left ? u1[j] : 0.0f;
+    }
     split3(f, part);
 }
 
@@ -325,7 +333,7 @@ __global__ __launch_bounds__(64 * W) void k_rows_direct(RowsArgs a) {
             u1 += ((const v4f*)lds[i])[from + 16];
         }
         uint4 part[3];
-        split_u(u0, u1, part);
+        split_u(u0, u1, a.rank - 8 * (lane >> 4), part);
         y = low_rank(l2, part, y);
     }
     if ((lane & 15) < N16) store_y(a, lane & 15, row + 4 * (lane >> 4), y);
@@ -506,7 +514,7 @@ __global__ __launch_bounds__(512, LP == 1 && RB == 2 ? 4 : 2) void k_rows_split(
                 u1 += us[base + (i * TB + t) * 64 + 16];
             }
             uint4 up[3];
-            split_u(u0, u1, up);
+            split_u(u0, u1, a.rank - 32 * r - 8 * (lane >> 4), up);
 #pragma unroll
             for (int i = 0; i < HB; ++i) y[t][i] = low_rank(l2[i], up, y[t][i]);
         }
@@ -616,12 +624,12 @@ hipError_t launch_rows_product(const RowsArgs& a, hipStream_t st) {
 // Canonical codes [Co][Ci / 2] and scale codes [Co][Ci / 32] to the step-major layout.
 __global__ __launch_bounds__(256) void k_import(const uint8_t* codes, const uint8_t* scales, long long Co, int groups,
                                                 int nks, uint8_t* rq, uint8_t* rs) {
-    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (id >= Co * groups) return;
-    const long long j = id / groups;
-    const int G = (int)(id % groups);
-    *(uint4*)(rq + off_fp4(j, G, nks)) = ((const uint4*)codes)[id];
-    rs[off_scale(j, G, nks)] = scales[id];
+    for (long long id = (long long)blockIdx.x * 256 + threadIdx.x; id < Co * groups; id += (long long)gridDim.x * 256) {
+        const long long j = id / groups;
+        const int G = (int)(id % groups);
+        *(uint4*)(rq + off_fp4(j, G, nks)) = ((const uint4*)codes)[id];
+        rs[off_scale(j, G, nks)] = scales[id];
+    }
 }
 
 template <class T>
@@ -666,6 +674,7 @@ RowsArgs rows_args(const dq_weights* w, dq_rows* a, int64_t N, void* y, dq_dtype
     r.Ci = (int)w->Ci;
     r.nks = (int)(w->Kp / 128);
     r.Co = (int)w->Co;
+    r.rank = (int)w->rank;
     r.rp = w->rp;
     r.rq = w->rq;
     r.rs = w->rs;
@@ -731,8 +740,8 @@ dq_status dq_import_weights(const uint8_t* rcodes_host, const uint8_t* rscales_h
     if ((e = hipMemcpy(cd.p, rcodes_host, (size_t)(Co * Ci / 2), hipMemcpyHostToDevice)) != hipSuccess ||
         (e = hipMemcpy(sd.p, rscales_host, (size_t)(Co * groups), hipMemcpyHostToDevice)) != hipSuccess)
         return hip_fail(e, "copy weight");
-    k_import<<<(unsigned)((Co * groups + 255) / 256), 256, 0, nullptr>>>(cd.p, sd.p, (long long)Co, (int)groups,
-                                                                        (int)(w->Kp / 128), w->rq, w->rs);
+    k_import<<<(unsigned)std::min<int64_t>((Co * groups + 255) / 256, 1 << 16), 256, 0, nullptr>>>(
+        cd.p, sd.p, (long long)Co, (int)groups, (int)(w->Kp / 128), w->rq, w->rs);
     if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "import kernel");
     if ((st = upload_factors(w, l1_host, l2_host)) != DQ_OK) return st;
     if ((e = hipDeviceSynchronize()) != hipSuccess) return hip_fail(e, "weight import");
