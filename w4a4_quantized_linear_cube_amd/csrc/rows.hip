@@ -21,6 +21,57 @@
 #include "dq_device.h"
 #include "dq_internal.h"
 
+namespace dq {
+
+constexpr int CUS = 256, MAX_ROWS = 4096;
+
+// How the general form splits N rows of a weight: tiles of 64 rb channels and
+// 16 tb rows, K slices of `per` steps.
+struct SplitPlan {
+    int tb, rb, groups, tiles, slices, per;
+    int64_t units() const { return (int64_t)groups * tiles; }
+    int64_t sum_floats() const { return slices > 1 ? units() * slices * 4 * rb * tb * 256 : 0; }
+};
+
+// `parts` of a row: three for fp32 rows, whose larger operands leave LDS for
+// 16 rows at a time.  Figures below are us of bf16 rows, rank 32.
+//  - rb: 256 channels to a tile (rb 4) halve what is read again of x and L1, which
+//    pays for several groups of rows where the tiles fill a quarter of the chip.
+//    128 / 256: 64 rows 5120 -> 10240 18.2 / 16.3, 13824 -> 8192 27.0 / 24.4, 5120 ->
+//    13824 19.3 / 19.4; but 5120 -> 5120 12.1 / 13.6 and, with few K steps,
+//    1536 -> 10240 8.7 / 10.9.
+//  - slices: a CU's time goes by the K steps of its slice, three more to every
+//    chunk of four begun, and each slice costs the workgroup that joins them the
+//    time of 1.6 steps (1.0 where a step is longer: three parts, more low ranks).
+//    Slices of 4 / 8 / 12 / 20 steps: 16 rows 8960 -> 1536 10.5 / 9.1 / 9.3 / 10.8,
+//    24 rows 5120 -> 5120 14.2 / 10.4 / 10.6 / 12.6, 64 rows 1536 -> 1536
+//    7.2 of 4 and 8.0 of 12.  Not more workgroups than CUs, or than two to a CU
+//    where two fit, in fp32 (64 rows 5120 -> 5120: 480 of 14 steps 21.2, 160 of 40
+//    25.3; in bf16 64 rows 1536 -> 8960: 420 of 4 steps 14.4, 140 of 12 9.0).
+// Over 59 shapes the choice is within 0.6 % of the best slice length on average.
+SplitPlan plan_split(int64_t N, int64_t Co, int nks, int rp, int parts) {
+    SplitPlan p;
+    p.tb = N <= 16 || parts > 1 ? 1 : 2;
+    p.groups = (int)((N + 16 * p.tb - 1) / (16 * p.tb));
+    p.rb = p.groups > 1 && parts == 1 && (Co + 255) / 256 * p.groups >= 64 && nks >= 24 ? 4 : 2;
+    p.tiles = (int)((Co + 64 * p.rb - 1) / (64 * p.rb));
+    const int most = parts == 3 && rp <= 32 ? 2 * CUS : CUS;
+    double least = 0.0;
+    for (int s = 1; s == 1 || (s <= nks / 2 && p.units() * s <= most); ++s) {
+        const int per = (nks + s - 1) / s, slices = (nks + per - 1) / per;
+        const int64_t rounds = (p.units() * slices + CUS - 1) / CUS;
+        const double cost = (double)rounds * (per + 3 * ((per + 3) / 4)) + (parts == 1 && rp <= 32 ? 1.6 : 1.0) * slices;
+        if (s == 1 || cost < least) {
+            least = cost;
+            p.per = per;
+            p.slices = slices;
+        }
+    }
+    return p;
+}
+
+}  // namespace dq
+
 // Workspace of the few-row products: where workgroups that share a tile meet.
 struct dq_rows {
     int device = 0;
@@ -28,12 +79,12 @@ struct dq_rows {
     int rp = 0;
     float* sums = nullptr;     // the K slices' sums of every tile
     int* arrivals = nullptr;   // slices of a tile that have ended (0 between launches)
+    dq::SplitPlan plans[2][dq::MAX_ROWS / 16];   // of 1 .. 16, 17 .. 32, .. rows, for one part a row and for three
 };
 
 namespace dq {
 namespace {
 
-constexpr int SPLIT_TARGET = 256;         // workgroups the general form aims at (one for each CU)
 constexpr int X_BF16 = 0, X_F32 = 1, X_MX8 = 2;
 
 struct RowsArgs {
@@ -83,20 +134,26 @@ __device__ __forceinline__ Piece<XK> load_piece(const RowsArgs& a, int n, int ch
 }
 
 // fp32 values as the sum of three bf16 values: the leading 8 bits, then those
-// of what is left.  The differences are exact, so the parts sum to the value;
-// a NaN or an infinity is its first part alone.
+// of what is left, twice.  The differences are exact, so the parts sum to the
+// value (bits below 2^-133 apart).  What is left of an infinity is made zero; of
+// a NaN it is NaN.
 __device__ __forceinline__ void split3(const float* v, uint4* out) {
     uint32_t w[3][4];
+    const auto upper = [](uint32_t hi, uint32_t lo) { return __builtin_amdgcn_perm(hi, lo, 0x07060302u); };   // two leading halves
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        float left = v[j];
+    for (int j = 0; j < 4; ++j) {
+        uint32_t b[3][2];
 #pragma unroll
-        for (int p = 0; p < 3; ++p) {
-            uint32_t b = __float_as_uint(left) >> 16;
-            if (p == 0 && (__float_as_uint(left) & 0x7fffffffu) > 0x7f800000u) b = 0x7fc0u;
-            left = p == 0 && (b & 0x7f80u) == 0x7f80u ? 0.0f : left - __uint_as_float(b << 16);
-            w[p][j >> 1] = j & 1 ? w[p][j >> 1] | (b << 16) : b;
+        for (int k = 0; k < 2; ++k) {
+            const float f = v[2 * j + k];
+            b[0][k] = __float_as_uint(f);
+            float left = f - __uint_as_float(b[0][k] & 0xffff0000u);
+            left = __builtin_fabsf(f) == __builtin_inff() ? 0.0f : left;
+            b[1][k] = __float_as_uint(left);
+            b[2][k] = __float_as_uint(left - __uint_as_float(b[1][k] & 0xffff0000u));
         }
+#pragma unroll
+        for (int p = 0; p < 3; ++p) w[p][j] = upper(b[p][1], b[p][0]);
     }
 #pragma unroll
     for (int p = 0; p < 3; ++p) out[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
@@ -363,18 +420,23 @@ __device__ __forceinline__ v4f take_over(__amdgpu_buffer_rsrc_t r, int at) {
 // L1 is read once a tile and step.  The slices' sums meet in the workspace:
 // whichever workgroup of a tile ends last adds them up in slice order, so
 // nothing waits and a result does not depend on the order of arrival.
+// The operands of the next chunk are laid out in LDS while one is used, so a
+// chunk has one barrier (0.39 -> 0.29 us a K step of 24 rows; where that leaves
+// no room for a second workgroup or its registers, in fp32 and with 256 channels,
+// it costs more than it gives and there is one place).
 // LP: groups of 32 low ranks (1, also for rank 0, or 4).
 template <int XK, int TB, int LP, int RB>
-__global__ __launch_bounds__(512, LP == 1 && RB == 2 ? 4 : 2) void k_rows_split(RowsArgs a) {
+__global__ __launch_bounds__(512, XK == X_F32 && LP == 1 ? 4 : 2) void k_rows_split(RowsArgs a) {
     constexpr int P = XK == X_F32 ? 3 : 1, CH = 4, J = CH / 2, NP = CH * TB / 2, BLK = 16 * 17;
     constexpr int HB = RB / 2, OUT = 8 * TB * HB * 64; // blocks of channels a wave finishes; 16-byte places of the tile's sums
     constexpr int ALL = OUT + 8 * TB * 64;             // ... with U's shares, where the operands were
-    __shared__ uint4 lds[CH * P * TB * BLK > ALL ? CH * P * TB * BLK : ALL];
+    constexpr bool TWO = P == 1 && RB == 2;                       // the next chunk's operands are laid out beside the one in use
+    constexpr int X = CH * P * TB * BLK, ROOM = TWO ? 2 * X : X;
+    __shared__ uint4 lds[ROOM > ALL ? ROOM : ALL];
     __shared__ int arrived;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    // the slices of a tile go to one XCD (workgroups go to the 8 XCDs in turn)
-    const int turn = (int)(blockIdx.x >> 3), tile = (int)(blockIdx.x & 7) + 8 * (turn / a.slices), slice = turn % a.slices;
-    if (tile >= a.tiles) return;
+    const int tile = (int)blockIdx.x % a.tiles, slice = (int)blockIdx.x / a.tiles;
+    if (slice >= a.slices) return;
     const int n0 = (int)blockIdx.y * 16 * TB, wk = w >> 2, row0 = tile * 64 * RB + 16 * RB * (w & 3);
     const int row = row0 + 16 * HB * wk;               // the 16 HB channels this wave finishes
     const int k0 = slice * a.per, k1 = min(a.nks, k0 + a.per), passes = a.rp >> 5, ug = w % CH;
@@ -395,14 +457,14 @@ __global__ __launch_bounds__(512, LP == 1 && RB == 2 ? 4 : 2) void k_rows_split(
             px[i] = load_piece<XK>(a, n0 + R % (16 * TB), 128 * (ks + R / (16 * TB)) + 8 * (tid & 15));
         }
     };
-    auto stage_x = [&]() {
+    auto stage_x = [&](int to) {
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int R = 32 * i + (tid >> 4), g = R / (16 * TB), n = R % (16 * TB);
             uint4 part[P];
             operand<XK>(px[i], part);
 #pragma unroll
-            for (int p = 0; p < P; ++p) lds[((g * P + p) * TB * 16 + n) * 17 + (tid & 15)] = part[p];
+            for (int p = 0; p < P; ++p) lds[to + ((g * P + p) * TB * 16 + n) * 17 + (tid & 15)] = part[p];
         }
     };
     const Stream<RB> weight(a, row0, lane);
@@ -413,12 +475,16 @@ __global__ __launch_bounds__(512, LP == 1 && RB == 2 ? 4 : 2) void k_rows_split(
 #pragma unroll
         for (int f = 0; f < 4; ++f) l1[f] = p[f * 64];
     };
-    const int rd = (lane & 15) * 17 + 4 * (lane >> 4);
-    auto chunk = [&](int ks, auto more) {
-        constexpr bool MORE = decltype(more)::value;   // another chunk follows
-        stage_x();
-        __syncthreads();
-        if constexpr (MORE) load_x(ks + CH);
+    const int own = (lane & 15) * 17 + 4 * (lane >> 4);
+    int at = 0;                                        // place of the chunk in use
+    auto chunk = [&](int ks, auto next, auto after) {
+        constexpr bool MORE = decltype(next)::value, AFTER = decltype(after)::value;   // another chunk follows, another two
+        const int rd = at + own;
+        if constexpr (!TWO) {
+            stage_x(0);
+            __syncthreads();
+            if constexpr (MORE) load_x(ks + CH);
+        }
         auto form_u = [&](int r) {
 #pragma unroll
             for (int f = 0; f < 4; ++f)
@@ -458,8 +524,14 @@ __global__ __launch_bounds__(512, LP == 1 && RB == 2 ? 4 : 2) void k_rows_split(
                     }
             }
             if constexpr (MORE) weight.fetch(min(ks + CH + g, k1 - 1), c[j], e[j]);
+            if constexpr (TWO && MORE)
+                if (j == 0) {
+                    stage_x(X - at);
+                    if constexpr (AFTER) load_x(ks + 2 * CH);
+                }
         }
-        __syncthreads();                               // (the operands are read)
+        __syncthreads();                               // (the operands are read, the next ones laid out)
+        if constexpr (TWO) at = X - at;
     };
     auto load_l2s = [&](int r) {
 #pragma unroll
@@ -472,9 +544,20 @@ __global__ __launch_bounds__(512, LP == 1 && RB == 2 ? 4 : 2) void k_rows_split(
     }
 #pragma unroll
     for (int j = 0; j < J; ++j) weight.fetch(min(k0 + 2 * j + wk, k1 - 1), c[j], e[j]);
+    if constexpr (TWO) {
+        stage_x(0);
+        if (k0 + CH < k1) load_x(k0 + CH);
+        __syncthreads();
+    }
+    const std::true_type yes;
+    const std::false_type no;
     int ks = k0;
-    for (; ks + CH < k1; ks += CH) chunk(ks, std::true_type());
-    chunk(ks, std::false_type());
+    for (; ks + 2 * CH < k1; ks += CH) chunk(ks, yes, yes);
+    if (ks + CH < k1) {
+        chunk(ks, yes, no);
+        ks += CH;
+    }
+    chunk(ks, no, no);
     // each wave finishes one half of its channels: the other half goes to its
     // partner (w ^ 4) through LDS, and its share of U to every wave
     v4f *part = (v4f*)lds, *us = part + OUT;
@@ -559,54 +642,41 @@ void launch_direct(RowsArgs a, hipStream_t st) {
     k_rows_direct<XK, N16, LR, RB, W, D><<<(unsigned)round_up(a.tiles, 8), 64 * W, 0, st>>>(a);
 }
 
-// How the general form splits N rows of a weight: tiles of 64 rb channels and
-// 16 tb rows, K slices of `per` steps.
-struct SplitPlan {
-    int tb, rb, groups, tiles, slices, per;
-    int64_t units() const { return (int64_t)groups * tiles; }
-    int64_t sum_floats() const { return slices > 1 ? units() * slices * 4 * rb * tb * 256 : 0; }
-};
-// `parts` of a row: three for fp32 rows, whose larger operands leave LDS for
-// 16 rows at a time.
-SplitPlan plan_split(int64_t N, int64_t Co, int nks, int parts) {
-    SplitPlan p;
-    p.tb = N <= 16 || parts > 1 ? 1 : 2;
-    p.groups = (int)((N + 16 * p.tb - 1) / (16 * p.tb));
-    // 256 channels to a tile halve what is read again of x and L1.  They pay for
-    // several groups of rows where the tiles still fill a third of the chip and K
-    // is long: 64 rows 5120 -> 10240 20.9 -> 15.7 us, -> 13824 21.3 -> 18.4 us; but
-    // 5120 -> 5120 12.1 -> 20.0 us, 1536 -> 10240 9.2 -> 10.4 us, and 20 rows 5120 ->
-    // 10240 13.1 -> 14.2 us
-    p.rb = p.groups > 1 && parts == 1 && (Co + 255) / 256 * p.groups >= 80 && nks >= 24 ? 4 : 2;
-    p.tiles = (int)((Co + 64 * p.rb - 1) / (64 * p.rb));
-    const int64_t target = parts > 1 && p.groups > 1 ? 2 * SPLIT_TARGET : SPLIT_TARGET;
-    const int64_t most = std::max<int64_t>(1, target / p.units());
-    p.per = (int)std::max<int64_t>(std::min(nks, 2), (nks + most - 1) / most);
-    p.slices = (nks + p.per - 1) / p.per;
-    return p;
-}
-
 template <int XK, int TB, int RB>
 void launch_split(RowsArgs a, const SplitPlan& p, hipStream_t st) {
     a.tiles = p.tiles;
     a.slices = p.slices;
     a.per = p.per;
-    const dim3 grid((unsigned)(round_up(p.tiles, 8) * p.slices), (unsigned)p.groups);
+    const dim3 grid((unsigned)round_up(p.tiles * p.slices, 8), (unsigned)p.groups);
     if (a.rp <= 32) k_rows_split<XK, TB, 1, RB><<<grid, 512, 0, st>>>(a);
     else k_rows_split<XK, TB, 4, RB><<<grid, 512, 0, st>>>(a);
 }
 
+// Measured at bf16 rows, rank 32 unless said otherwise (us, a captured run of calls):
+//  - Direct or split.  The direct form needs no meeting of workgroups, but each
+//    of its workgroups reads all of L1 and x, so it pays up to a number of K
+//    steps that depends on what it reads.  Direct / split: one row 1536 -> 1536
+//    4.1 / 5.6, 5120 -> 5120 8.2 / 8.4, 5120 -> 13824 10.0 / 11.8, 8960 -> 5120
+//    11.5 / 11.0; 8 rows 2080 -> 4999 5.9 / 7.1, 5120 -> 5120 9.1 / 8.7.  Without
+//    low ranks: 16 rows 5120 -> 5120 6.8 / 8.2, 13824 -> 5120 13.4 / 12.4; 4 rows
+//    13824 -> 5120 10.8 / 11.6.  fp32 has three parts a row, so four rows at most.
+//  - 64 output channels to a workgroup halve the readings of L1 and x, but leave
+//    CUs idle for few channels.  32 / 64 channels: one row 5120 -> 5120 8.2 / 9.0,
+//    1536 -> 8960 6.3 / 5.4, 5120 -> 13824 13.2 / 10.0.
+//  - Two K steps in flight help where U and more rows do not need the registers.
+//    One / two: rank 0 5120 -> 5120 4 rows 6.4 / 5.8, but 5120 -> 13824 16 rows
+//    9.3 / 9.8; with U one row 5120 -> 13824 10.0 / 11.3.
 template <int XK>
-hipError_t launch_rows_product(const RowsArgs& a, hipStream_t st) {
+hipError_t launch_rows_product(const RowsArgs& a, const SplitPlan& p, hipStream_t st) {
     constexpr int P = XK == X_F32 ? 3 : 1;
-    const SplitPlan p = plan_split(a.N, a.Co, a.nks, P);
-    const bool direct = a.N <= (P == 1 ? 16 : 4) && (a.rp == 0 || (a.rp == 32 && a.nks <= 60)) && !(P == 1 && p.slices == 1);
+    const int most = a.rp ? (a.N == 1 ? 48 : 24) : a.N <= 4 && P == 1 ? 120 : 60;
+    const bool direct = a.N <= (P == 1 ? 16 : 4) && a.rp <= 32 && a.nks <= most;
     if (direct) {
         const auto go = [&](auto lr, auto rb) {
             constexpr int LR = decltype(lr)::value, RB = decltype(rb)::value, D = LR || P == 3 ? 1 : 2;
             if (a.N == 1) launch_direct<XK, 1, LR, RB, 8, D>(a, st);
             else if (a.N <= 4) launch_direct<XK, 4, LR, RB, 8, D>(a, st);
-            else if constexpr (P == 1) launch_direct<XK, 16, LR, RB, 8, D>(a, st);
+            else if constexpr (P == 1) launch_direct<XK, 16, LR, RB, 8, 1>(a, st);
         };
         const std::integral_constant<int, 0> none;
         const std::integral_constant<int, 1> some;
@@ -755,7 +825,7 @@ dq_status dq_rows_create(const dq_weights* w, int64_t max_rows, dq_rows** out) {
     *out = nullptr;
     if (!w) return fail(DQ_ERR_INVALID_ARG, "weights handle is NULL");
     if (w->wfmt != 4) return fail(DQ_ERR_INVALID_ARG, "a 6-bit weight takes the 6-bit entry points");
-    if (max_rows < 1 || max_rows > 4096) return fail(DQ_ERR_SHAPE, "max_rows must be in [1, 4096]");
+    if (max_rows < 1 || max_rows > MAX_ROWS) return fail(DQ_ERR_SHAPE, "max_rows must be in [1, 4096]");
     if (w->Ci > 65536) return fail(DQ_ERR_SHAPE, "Ci must be <= 65536 for few-row products");
     DeviceGuard dg(w->device);
     if (!dg.ok) return fail(DQ_ERR_DEVICE, "hipSetDevice failed");
@@ -772,9 +842,10 @@ dq_status dq_rows_create(const dq_weights* w, int64_t max_rows, dq_rows** out) {
     int64_t floats = 0, units = 0;                      // the largest need of any row count up to max_rows
     for (int64_t n = 16; n < max_rows + 16; n += 16)
         for (const int parts : {1, 3}) {
-            const SplitPlan p = plan_split(std::min(n, max_rows), w->Co, (int)(w->Kp / 128), parts);
+            const SplitPlan p = plan_split(n, w->Co, (int)(w->Kp / 128), w->rp, parts);
             floats = std::max(floats, p.sum_floats());
             units = std::max(units, p.units());
+            a->plans[parts > 1][n / 16 - 1] = p;
         }
     hipError_t e;
     if ((e = zalloc(&a->sums, (size_t)floats, &bytes)) != hipSuccess ||
@@ -805,8 +876,9 @@ dq_status dq_linear_rows(const dq_weights* w, const void* x_dev, dq_dtype dt, in
     RowsArgs r = rows_args(w, a, N, y_dev, ydt, ldy);
     r.x = x_dev;
     r.ldx = ldx;
-    const hipError_t e = dt == DQ_BF16 ? launch_rows_product<X_BF16>(r, (hipStream_t)stream)
-                                       : launch_rows_product<X_F32>(r, (hipStream_t)stream);
+    const SplitPlan& p = a->plans[dt == DQ_F32][(N - 1) / 16];
+    const hipError_t e = dt == DQ_BF16 ? launch_rows_product<X_BF16>(r, p, (hipStream_t)stream)
+                                       : launch_rows_product<X_F32>(r, p, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "product launch");
     return DQ_OK;
 }
@@ -828,7 +900,7 @@ dq_status dq_linear_rows8(const dq_weights* w, const uint8_t* codes_dev, const u
     RowsArgs r = rows_args(w, a, N, y_dev, ydt, ldy);
     r.x = codes_dev;
     r.xs = scales_dev;
-    const hipError_t e = launch_rows_product<X_MX8>(r, (hipStream_t)stream);
+    const hipError_t e = launch_rows_product<X_MX8>(r, a->plans[0][(N - 1) / 16], (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "product launch");
     return DQ_OK;
 }
