@@ -75,7 +75,11 @@ SHAPES = [  # n, ci, co, rank
     # every form by rows, rank and output channels: 1, up to 4, up to 16 rows; rank none or up to 32; below 8192 outputs and above
     (1, 992, 300, 0), (4, 992, 301, 0), (16, 992, 302, 0), (1, 640, 8200, 0), (4, 640, 8201, 0), (12, 640, 8202, 0),
     (1, 640, 8199, 32), (2, 640, 8200, 17), (16, 640, 8201, 32), (5, 1600, 17000, 32), (64, 3104, 10300, 32), (33, 3104, 10241, 100),
-    (50, 3104, 10250, 0), (1, 20480, 96, 0), (3, 20480, 50, 32), (20, 7712, 33, 5)]
+    (50, 3104, 10250, 0), (1, 20480, 96, 0), (3, 20480, 50, 32), (20, 7712, 33, 5),
+    # long K without low ranks: up to 8 and up to 16 rows by 16 waves, and shared out
+    (1, 16384, 70, 0), (4, 12000, 65, 0), (8, 13824, 300, 0), (16, 10240, 100, 0), (16, 13824, 96, 0), (4, 7712, 8300, 0),
+    # one row with low ranks up to 48 steps, and past them; the largest rank
+    (1, 6144, 40, 8), (1, 6176, 40, 8), (2, 2976, 129, 32), (2, 3136, 129, 32), (1, 640, 200, 128), (40, 9000 // 32 * 32, 513, 128)]
 
 
 @pytest.mark.parametrize("n,ci,co,rank", SHAPES)
@@ -272,12 +276,12 @@ def test_twice_the_same_on_streams_and_in_graphs(dqm):
     norm and two products replayed on new inputs with eager work between."""
     n, c = 4, 1536
     wq, *_ = _weight(dqm, c, c, 32, 91)
-    wk, *_ = _weight(dqm, c, 2 * c, 32, 92)
+    wk, *_ = _weight(dqm, c, 2 * c - 40, 32, 92)
     aq, ak = dqm.dq_rows_create(wq, n), dqm.dq_rows_create(wk, n)
     x, r = (torch.empty(n, c, dtype=torch.bfloat16, device=DEV) for _ in range(2))
     codes, scales = torch.empty(n, c, dtype=torch.uint8, device=DEV), torch.empty(n, c // 32, dtype=torch.uint8, device=DEV)
     h = torch.empty_like(x)
-    out = [torch.empty(n, k * c, dtype=torch.bfloat16, device=DEV) for k in (1, 2)]
+    out = [torch.empty(n, co, dtype=torch.bfloat16, device=DEV) for co in (c, 2 * c - 40)]
 
     def step(stream=None):
         dqm.dq_rmsnorm8(x, None, 1e-6, codes, scales, residual=r, h=h, stream=stream)

@@ -282,6 +282,11 @@ __device__ __forceinline__ void store_y(const RowsArgs& a, int n, int j, v4f y) 
 // their partial sums are added in wave order.  With LR (32 low ranks) every
 // workgroup forms U as well: L1 is read again by each, from L2.
 // D steps are in flight.
+// Bound by the weight's bytes for many channels (2 fp32 rows 5120 -> 30720, rank
+// 0: 83.8 MB in 16.1 us, 5.2 TB/s; one MX-FP8 row 5120 -> 13824, rank 32: 38.9 MB
+// in 9.5 us, 4.1 TB/s, of which U takes 1.6), and for few by the launch and one
+// chain of loads, products and a sum (1 row 1536 -> 1536 4.1 us, 3.2 without U).
+// Forming U in a launch of its own instead costs 2.8 to 3.1 us.
 template <int XK, int N16, int LR, int RB, int W, int D>
 __global__ __launch_bounds__(64 * W) void k_rows_direct(RowsArgs a) {
     constexpr int P = XK == X_F32 ? 3 : 1, G = 16 / (N16 * P), NI = (G * N16 + 3) / 4, SUMS = RB + (LR ? 2 : 0);
@@ -424,6 +429,13 @@ __device__ __forceinline__ v4f take_over(__amdgpu_buffer_rsrc_t r, int at) {
 // chunk has one barrier (0.39 -> 0.29 us a K step of 24 rows; where that leaves
 // no room for a second workgroup or its registers, in fp32 and with 256 channels,
 // it costs more than it gives and there is one place).
+// A K step of 128 x 32 operands takes a CU 0.29 us, whether 12 workgroups run
+// or 240.  In timing copies of the form with one place (0.39 us) it was 0.15 less
+// without laying out x, 0.10 without reading the operands from LDS, 0.07 without
+// loading L1, 0.05 without loading x.  Before and after the loop come the launch and the first loads,
+// 2.2 us, and the chain of low-rank product, hand-over, arrival and joining, 3 us:
+// 64 MX-FP8 rows 5120 -> 5120 11.8 us, 16 bf16 rows 13824 -> 5120 12.8 us (39.4 MB,
+// 3.1 TB/s), 37 rows 2080 -> 4999 9.2 us.
 // LP: groups of 32 low ranks (1, also for rank 0, or 4).
 template <int XK, int TB, int LP, int RB>
 __global__ __launch_bounds__(512, XK == X_F32 && LP == 1 ? 4 : 2) void k_rows_split(RowsArgs a) {
@@ -435,6 +447,8 @@ __global__ __launch_bounds__(512, XK == X_F32 && LP == 1 ? 4 : 2) void k_rows_sp
     __shared__ uint4 lds[ROOM > ALL ? ROOM : ALL];
     __shared__ int arrived;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // (a row of workgroups is a multiple of 8, so the groups of rows that read the
+    // same weight are on the same XCD and its L2: 64 rows 5120 -> 13824 21.2 -> 19.3 us)
     const int tile = (int)blockIdx.x % a.tiles, slice = (int)blockIdx.x / a.tiles;
     if (slice >= a.slices) return;
     const int n0 = (int)blockIdx.y * 16 * TB, wk = w >> 2, row0 = tile * 64 * RB + 16 * RB * (w & 3);
@@ -658,25 +672,30 @@ void launch_split(RowsArgs a, const SplitPlan& p, hipStream_t st) {
 //    steps that depends on what it reads.  Direct / split: one row 1536 -> 1536
 //    4.1 / 5.6, 5120 -> 5120 8.2 / 8.4, 5120 -> 13824 10.0 / 11.8, 8960 -> 5120
 //    11.5 / 11.0; 8 rows 2080 -> 4999 5.9 / 7.1, 5120 -> 5120 9.1 / 8.7.  Without
-//    low ranks: 16 rows 5120 -> 5120 6.8 / 8.2, 13824 -> 5120 13.4 / 12.4; 4 rows
-//    13824 -> 5120 10.8 / 11.6.  fp32 has three parts a row, so four rows at most.
+//    low ranks: 16 rows 5120 -> 5120 6.8 / 8.2, 10240 -> 5120 10.0 / 10.9, 13824 ->
+//    5120 12.3 / 12.0; 8 rows 16384 -> 5120 10.8 / 12.7; 4 rows 5120 -> 10240 8.0 /
+//    9.4, 13824 -> 10240 16.5 / 15.8.  fp32 has three parts a row, so four rows at most.
 //  - 64 output channels to a workgroup halve the readings of L1 and x, but leave
 //    CUs idle for few channels.  32 / 64 channels: one row 5120 -> 5120 8.2 / 9.0,
 //    1536 -> 8960 6.3 / 5.4, 5120 -> 13824 13.2 / 10.0.
 //  - Two K steps in flight help where U and more rows do not need the registers.
 //    One / two: rank 0 5120 -> 5120 4 rows 6.4 / 5.8, but 5120 -> 13824 16 rows
 //    9.3 / 9.8; with U one row 5120 -> 13824 10.0 / 11.3.
+//  - 16 waves to a workgroup instead of 8 help where neither U nor 64 channels
+//    take the registers and LDS of two: rank 0 8 rows 8960 -> 5120 9.4 / 7.5, one row
+//    5120 -> 5120 5.2 / 5.4; but 8 rows 5120 -> 13824 8.9 / 9.2, and with U one
+//    row 1536 -> 1536 4.1 / 4.6, 5120 -> 5120 8.3 / 8.7.
 template <int XK>
 hipError_t launch_rows_product(const RowsArgs& a, const SplitPlan& p, hipStream_t st) {
     constexpr int P = XK == X_F32 ? 3 : 1;
-    const int most = a.rp ? (a.N == 1 ? 48 : 24) : a.N <= 4 && P == 1 ? 120 : 60;
+    const int most = a.rp ? (a.N == 1 ? 48 : 24) : a.Co >= 8192 ? 60 : a.N <= 8 ? 128 : 100;
     const bool direct = a.N <= (P == 1 ? 16 : 4) && a.rp <= 32 && a.nks <= most;
     if (direct) {
         const auto go = [&](auto lr, auto rb) {
-            constexpr int LR = decltype(lr)::value, RB = decltype(rb)::value, D = LR || P == 3 ? 1 : 2;
-            if (a.N == 1) launch_direct<XK, 1, LR, RB, 8, D>(a, st);
-            else if (a.N <= 4) launch_direct<XK, 4, LR, RB, 8, D>(a, st);
-            else if constexpr (P == 1) launch_direct<XK, 16, LR, RB, 8, 1>(a, st);
+            constexpr int LR = decltype(lr)::value, RB = decltype(rb)::value, D = LR || P == 3 ? 1 : 2, W = LR || RB == 4 ? 8 : 16;
+            if (a.N == 1) launch_direct<XK, 1, LR, RB, W, D>(a, st);
+            else if (a.N <= 4) launch_direct<XK, 4, LR, RB, W, D>(a, st);
+            else if constexpr (P == 1) launch_direct<XK, 16, LR, RB, W, 1>(a, st);
         };
         const std::integral_constant<int, 0> none;
         const std::integral_constant<int, 1> some;
