@@ -253,3 +253,33 @@ def test_more_rows_than_one_launch_takes(dqm):
         assert (got[:whole].view(-1, period, got.shape[1]) == want).all()
         assert torch.equal(got[whole:n], want[:n - whole])
         assert (got[n:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("n", [1, 7, 33, 1030])
+@pytest.mark.parametrize("c,group", [(32, 32), (64, 32), (64, 64), (96, 32), (128, 64), (160, 32), (192, 64), (256, 32), (288, 32), (512, 64), (544, 32)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_short_rows(dqm, n, c, group, dtype):
+    """Several rows to a wave: each with its own sum and scales, none past the last touched."""
+    x, r = _stream_rows(n, c, dtype, c + n), _stream_rows(n, c, dtype, c + n + 1)
+    x[n // 2] = 0.0 if n > 1 else x[0]
+    codes, scales, h, y = _outputs(n + 3, c, dtype)
+    before = [t[n:].clone() for t in (codes, scales, h, y)]
+    dqm.dq_rmsnorm8(x.to(DEV), None, 1e-5, codes[:n], scales[:n], residual=r.to(DEV), h=h[:n], y=y[:n], group=group)
+    want = rows.rms_norm8(_f32(x), _f32(r), None, 1e-5, dtype, group)
+    _compare(want, codes[:n], scales[:n], h[:n], y[:n], dtype)
+    for t, b in zip((codes, scales, h, y), before):
+        assert torch.equal(t[n:].view(torch.uint8), b.view(torch.uint8))
+
+
+def test_many_short_rows(dqm):
+    """Enough rows that the outputs bypass the caches, by a period of rows whose own codes are known."""
+    for c, dtype in ((64, "bf16"), (128, "f32"), (448, "bf16")):
+        period, n = 1000, (4 << 20) // c + 77
+        base = _stream_rows(period, c, dtype, c)
+        want = rows.rms_norm8(_f32(base), None, None, 1e-6, dtype)
+        x = base.repeat(n // period + 1, 1)[:n].to(DEV)
+        codes, scales, _, _ = _outputs(n, c, dtype)
+        dqm.dq_rmsnorm8(x, None, 1e-6, codes, scales)
+        for got, part in ((codes, want["codes"]), (scales, want["scales"])):
+            full = torch.from_numpy(part).repeat(n // period + 1, 1)[:n]
+            assert torch.equal(got.view(torch.uint8).cpu(), full)

@@ -113,7 +113,7 @@ __device__ __forceinline__ void load_gain(const NormArgs& a, int c, float* g) {
 template <class T, int TPR, int CH, bool NT>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm8(NormArgs a) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
-    constexpr int WPR = TPR / 64;
+    constexpr int WPR = TPR / 64;                   // waves to a row (0: several rows to a wave)
     const int t = threadIdx.x % TPR;
     const long long row = a.first + (long long)blockIdx.x * RPB + threadIdx.x / TPR;
     const bool live = row < a.N;
@@ -151,7 +151,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm8(NormArgs a) 
             for (int j = 0; j < 8; ++j) s = __builtin_fma((double)h[i][j], (double)h[i][j], s);
     }
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m, 64);
+    for (int m = 1; m < (TPR < 64 ? TPR : 64); m <<= 1) s += __shfl_xor(s, m, 64);
     if constexpr (WPR > 1) {
         __shared__ double part[RPB * WPR];
         const int w = threadIdx.x >> 6;
@@ -214,23 +214,35 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm8(NormArgs a) 
     }
 }
 
-// C / 8 chunks over TPR threads: MIN to 4 each.  A launch takes fewer than 2^32
-// threads, so more rows than that are several launches.
-template <class T, int TPR, int MIN, bool NT>
+// C / 8 chunks over TPR threads: MIN to MAX each.  A launch takes fewer than
+// 2^32 threads, so more rows than that are several launches.
+template <class T, int TPR, int MIN, int MAX, bool NT>
 void launch_norm(NormArgs a, hipStream_t st) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1, THREADS = TPR < 256 ? 256 : TPR;
     constexpr long long MOST = (1ll << 31) / THREADS;
     const int ch = (a.C / 8 + TPR - 1) / TPR;
     const auto go = [&](unsigned grid) {
-        if constexpr (MIN <= 1) if (ch == 1) return k_rmsnorm8<T, TPR, 1, NT><<<grid, THREADS, 0, st>>>(a);
-        if constexpr (MIN <= 2) if (ch == 2) return k_rmsnorm8<T, TPR, 2, NT><<<grid, THREADS, 0, st>>>(a);
-        if constexpr (MIN <= 3) if (ch == 3) return k_rmsnorm8<T, TPR, 3, NT><<<grid, THREADS, 0, st>>>(a);
-        k_rmsnorm8<T, TPR, 4, NT><<<grid, THREADS, 0, st>>>(a);
+        if constexpr (MIN <= 1 && MAX > 1) if (ch == 1) return k_rmsnorm8<T, TPR, 1, NT><<<grid, THREADS, 0, st>>>(a);
+        if constexpr (MIN <= 2 && MAX > 2) if (ch == 2) return k_rmsnorm8<T, TPR, 2, NT><<<grid, THREADS, 0, st>>>(a);
+        if constexpr (MIN <= 3 && MAX > 3) if (ch == 3) return k_rmsnorm8<T, TPR, 3, NT><<<grid, THREADS, 0, st>>>(a);
+        k_rmsnorm8<T, TPR, MAX, NT><<<grid, THREADS, 0, st>>>(a);
     };
     for (; a.first < a.N; a.first += MOST * RPB) go((unsigned)std::min(MOST, (a.N - a.first + RPB - 1) / RPB));
 }
 
-// Few rows are bound by their own latency, so a row gets as many threads as it
+// Rows of up to 64 chunks: one to a wave, or several, with as many lanes to a
+// row as it has chunks.  In bf16 with a residual, by 256 threads a row for few
+// rows and 64 for many / by these: 4096 x 128 6.1 / 3.1 us, 16384 x 64 16.4 / 3.6,
+// 524288 x 128 204 / 77, 1024 x 512 3.5 / 3.3; 65536 x 512 38.3 / 38.3.
+template <class T, bool NT>
+void launch_short(const NormArgs& a, hipStream_t st) {
+    if (a.C <= 64) launch_norm<T, 8, 1, 1, NT>(a, st);
+    else if (a.C <= 128) launch_norm<T, 16, 1, 1, NT>(a, st);
+    else if (a.C <= 256) launch_norm<T, 32, 1, 1, NT>(a, st);
+    else launch_norm<T, 64, 1, 1, NT>(a, st);
+}
+
+// Few longer rows are bound by their own latency, so a row gets as many threads as it
 // has chunks; many by HBM, so a thread holds up to four chunks, and the
 // outputs bypass the caches.  Measured in bf16 with a residual, few / many form:
 //   1 x 5120 3.2 / 4.2 us; 64 x 1536 2.8 / 4.5 us; 256 x 5120 with plain values
@@ -241,17 +253,20 @@ void launch_norm(NormArgs a, hipStream_t st) {
 // Threads to a long row: 20000 x 13824 takes 358 us with 512, 368 us with 256.
 template <class T>
 hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
-    if (a.N * a.C <= (3ll << 20)) {
-        if (a.C <= 2048) launch_norm<T, 256, 1, false>(a, st);
-        else launch_norm<T, 1024, 1, false>(a, st);
+    const bool few = a.N * a.C <= (3ll << 20);
+    if (a.C <= 512) {
+        few ? launch_short<T, false>(a, st) : launch_short<T, true>(a, st);
+    } else if (few) {
+        if (a.C <= 2048) launch_norm<T, 256, 1, 1, false>(a, st);
+        else launch_norm<T, 1024, 1, 4, false>(a, st);
     } else if (a.C <= 2048) {
-        launch_norm<T, 64, 1, true>(a, st);
+        launch_norm<T, 64, 2, 4, true>(a, st);
     } else if (a.C <= 8192) {
-        launch_norm<T, 256, 2, true>(a, st);
+        launch_norm<T, 256, 2, 4, true>(a, st);
     } else if (a.C <= 16384) {
-        launch_norm<T, 512, 3, true>(a, st);
+        launch_norm<T, 512, 3, 4, true>(a, st);
     } else {
-        launch_norm<T, 1024, 3, true>(a, st);
+        launch_norm<T, 1024, 3, 4, true>(a, st);
     }
     return hipGetLastError();
 }
