@@ -79,7 +79,9 @@ SHAPES = [  # n, ci, co, rank
     # long K without low ranks: up to 8 and up to 16 rows by 16 waves, and shared out
     (1, 16384, 70, 0), (4, 12000, 65, 0), (8, 13824, 300, 0), (16, 10240, 100, 0), (16, 13824, 96, 0), (4, 7712, 8300, 0),
     # one row with low ranks up to 48 steps, and past them; the largest rank
-    (1, 6144, 40, 8), (1, 6176, 40, 8), (2, 2976, 129, 32), (2, 3136, 129, 32), (1, 640, 200, 128), (40, 9000 // 32 * 32, 513, 128)]
+    (1, 6144, 40, 8), (1, 6176, 40, 8), (2, 2976, 129, 32), (2, 3136, 129, 32), (1, 640, 200, 128), (40, 9000 // 32 * 32, 513, 128),
+    # 33 to 64 ranks in the form of few rows, up to 14 steps and past them, and 65
+    (1, 96, 40, 33), (3, 1792, 300, 64), (16, 1056, 8200, 64), (1, 1824, 77, 48), (4, 640, 129, 64), (2, 640, 129, 65)]
 
 
 @pytest.mark.parametrize("n,ci,co,rank", SHAPES)
@@ -382,7 +384,7 @@ def test_refused_on_device(dqm):
     assert (y == 2.0).all()
 
 
-@pytest.mark.parametrize("rank", [0, 5, 32, 37, 128])
+@pytest.mark.parametrize("rank", [0, 5, 32, 37, 64, 128])
 @pytest.mark.parametrize("n", [1, 3, 20])
 def test_infinite_channels_with_low_ranks(dqm, n, rank):
     """Positive weights and factors: a row with an infinite channel is infinite,

@@ -279,8 +279,8 @@ __device__ __forceinline__ void store_y(const RowsArgs& a, int n, int j, v4f y) 
 // time, and lays them out as operands in its own LDS rows (17 pieces apart, so
 // that neither the writes by row nor the reads by piece meet in a bank).  The
 // W waves of a workgroup share out the K steps of 16 RB output channels and
-// their partial sums are added in wave order.  With LR (32 low ranks) every
-// workgroup forms U as well: L1 is read again by each, from L2.
+// their partial sums are added in wave order.  With LR (groups of 32 low
+// ranks, 1 or 2) every workgroup forms U as well: L1 is read again by each, from L2.
 // D steps are in flight.
 // Bound by the weight's bytes for many channels (2 fp32 rows 5120 -> 30720, rank
 // 0: 83.8 MB in 16.1 us, 5.2 TB/s; one MX-FP8 row 5120 -> 13824, rank 32: 38.9 MB
@@ -289,7 +289,7 @@ __device__ __forceinline__ void store_y(const RowsArgs& a, int n, int j, v4f y) 
 // Forming U in a launch of its own instead costs 2.8 to 3.1 us.
 template <int XK, int N16, int LR, int RB, int W, int D>
 __global__ __launch_bounds__(64 * W) void k_rows_direct(RowsArgs a) {
-    constexpr int P = XK == X_F32 ? 3 : 1, G = 16 / (N16 * P), NI = (G * N16 + 3) / 4, SUMS = RB + (LR ? 2 : 0);
+    constexpr int P = XK == X_F32 ? 3 : 1, G = 16 / (N16 * P), NI = (G * N16 + 3) / 4, SUMS = RB + 2 * LR;
     constexpr int SLOTS = 16 * 17 > 64 * SUMS ? 16 * 17 : 64 * SUMS;
     __shared__ uint4 lds[W][SLOTS];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -328,21 +328,22 @@ __global__ __launch_bounds__(64 * W) void k_rows_direct(RowsArgs a) {
         __builtin_amdgcn_wave_barrier();
     };
     const Stream<RB> weight(a, row0, lane);
-    uint4 c[D][RB], l1[D][LR ? 8 : 1];
+    uint4 c[D][RB], l1[D][LR ? 8 * LR : 1];
     int e[D][RB];
     auto fetch = [&](int d, int ks) {
         weight.fetch(ks, c[d], e[d]);
         if constexpr (LR) {
 #pragma unroll
-            for (int f = 0; f < 8; ++f) l1[d][f] = a.l1p[((long long)ks * 8 + f) * 64 + lane];
+            for (int f = 0; f < 8 * LR; ++f) l1[d][f] = a.l1p[((long long)ks * (8 * LR) + f) * 64 + lane];
         }
     };
     if (k0 < k1) load_x(k0);
 #pragma unroll
     for (int d = 0; d < D; ++d)
         if (k0 + d < k1) fetch(d, k0 + d);
-    uint4 l2;
-    if constexpr (LR) l2 = load_l2(a, 0, row0 + 16 * (w % RB), lane);
+    uint4 l2[LR ? LR : 1];
+#pragma unroll
+    for (int r = 0; r < LR; ++r) l2[r] = load_l2(a, 32 * r, row0 + 16 * (w % RB), lane);
     const int rd = (lane & (N16 - 1)) * 17 + 4 * (lane >> 4);
     int staged = G;                                    // steps used of the staged ones
     for (int ks = k0; ks < k1; ks += D) {
@@ -368,7 +369,7 @@ __global__ __launch_bounds__(64 * W) void k_rows_direct(RowsArgs a) {
                 }
                 if constexpr (LR) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                    for (int i = 0; i < 2 * LR; ++i)
 #pragma unroll
                         for (int p = 0; p < P; ++p) acc[RB + i] = mfma(__builtin_bit_cast(v8bf, l1[d][4 * i + f]), x[p], acc[RB + i]);
                 }
@@ -386,8 +387,9 @@ __global__ __launch_bounds__(64 * W) void k_rows_direct(RowsArgs a) {
     v4f y = ((const v4f*)lds[0])[w * 64 + lane];
 #pragma unroll
     for (int i = 1; i < W; ++i) y += ((const v4f*)lds[i])[w * 64 + lane];
-    if constexpr (LR) {
-        const int from = RB * 64 + u_place(lane);
+#pragma unroll
+    for (int r = 0; r < LR; ++r) {
+        const int from = (RB + 2 * r) * 64 + u_place(lane);
         v4f u0 = {0.0f, 0.0f, 0.0f, 0.0f}, u1 = u0;
 #pragma unroll
         for (int i = 0; i < W; ++i) {
@@ -395,8 +397,8 @@ __global__ __launch_bounds__(64 * W) void k_rows_direct(RowsArgs a) {
             u1 += ((const v4f*)lds[i])[from + 16];
         }
         uint4 part[3];
-        split_u(u0, u1, a.rank - 8 * (lane >> 4), part);
-        y = low_rank(l2, part, y);
+        split_u(u0, u1, a.rank - 32 * r - 8 * (lane >> 4), part);
+        y = low_rank(l2[r], part, y);
     }
     if ((lane & 15) < N16) store_y(a, lane & 15, row + 4 * (lane >> 4), y);
 }
@@ -436,12 +438,13 @@ __device__ __forceinline__ v4f take_over(__amdgpu_buffer_rsrc_t r, int at) {
 // 2.2 us, and the chain of low-rank product, hand-over, arrival and joining, 3 us:
 // 64 MX-FP8 rows 5120 -> 5120 11.8 us, 16 bf16 rows 13824 -> 5120 12.8 us (39.4 MB,
 // 3.1 TB/s), 37 rows 2080 -> 4999 9.2 us.
-// LP: groups of 32 low ranks (1, also for rank 0, or 4).
+// LP: groups of 32 low ranks (1, also for rank 0, or 4, whose next group's L1
+// loads while one is used: 64 rows 5120 -> 5120 rank 128 21.6 -> 18.6 us).
 template <int XK, int TB, int LP, int RB>
 __global__ __launch_bounds__(512, XK == X_F32 && LP == 1 ? 4 : 2) void k_rows_split(RowsArgs a) {
     constexpr int P = XK == X_F32 ? 3 : 1, CH = 4, J = CH / 2, NP = CH * TB / 2, BLK = 16 * 17;
     constexpr int HB = RB / 2, OUT = 8 * TB * HB * 64; // blocks of channels a wave finishes; 16-byte places of the tile's sums
-    constexpr int ALL = OUT + 8 * TB * 64;             // ... with U's shares, where the operands were
+    constexpr int ALL = OUT + LP * 8 * TB * 64;        // ... with U's shares, where the operands were
     constexpr bool TWO = P == 1 && RB == 2;                       // the next chunk's operands are laid out beside the one in use
     constexpr int X = CH * P * TB * BLK, ROOM = TWO ? 2 * X : X;
     __shared__ uint4 lds[ROOM > ALL ? ROOM : ALL];
@@ -482,12 +485,12 @@ __global__ __launch_bounds__(512, XK == X_F32 && LP == 1 ? 4 : 2) void k_rows_sp
         }
     };
     const Stream<RB> weight(a, row0, lane);
-    uint4 c[J][RB], l1[4], l2[HB];
+    uint4 c[J][RB], l1[LP > 1 ? 2 : 1][4], l2[LP][HB];  // (of one group of 32 low ranks in use, and the next)
     int e[J][RB];
     auto load_u = [&](int ks, int r) {                 // (places past the slice: its last step again, not used)
         const uint4* p = a.l1p + ((long long)min(ks + ug, k1 - 1) * (a.rp >> 4) + 2 * r + wk) * 256 + lane;
 #pragma unroll
-        for (int f = 0; f < 4; ++f) l1[f] = p[f * 64];
+        for (int f = 0; f < 4; ++f) l1[r & 1][f] = p[f * 64];
     };
     const int own = (lane & 15) * 17 + 4 * (lane >> 4);
     int at = 0;                                        // place of the chunk in use
@@ -506,16 +509,15 @@ __global__ __launch_bounds__(512, XK == X_F32 && LP == 1 ? 4 : 2) void k_rows_sp
                 for (int t = 0; t < TB; ++t)
 #pragma unroll
                     for (int p = 0; p < P; ++p)
-                        u[r][t] = mfma(__builtin_bit_cast(v8bf, l1[f]), lds[((ug * P + p) * TB + t) * BLK + rd + f], u[r][t]);
+                        u[r][t] = mfma(__builtin_bit_cast(v8bf, l1[r & 1][f]), lds[((ug * P + p) * TB + t) * BLK + rd + f], u[r][t]);
         };
         if (passes && (MORE || ks + ug < k1)) {
-            form_u(0);
 #pragma unroll
-            for (int r = 1; r < LP; ++r)
-                if (r < passes) {
-                    load_u(ks, r);
-                    form_u(r);
-                }
+            for (int r = 0; r < LP; ++r) {
+                if (r && r >= passes) break;
+                if (r + 1 < LP && r + 1 < passes) load_u(ks, r + 1);
+                form_u(r);
+            }
         }
         if constexpr (MORE)
             if (passes) load_u(ks + CH, 0);
@@ -549,7 +551,7 @@ __global__ __launch_bounds__(512, XK == X_F32 && LP == 1 ? 4 : 2) void k_rows_sp
     };
     auto load_l2s = [&](int r) {
 #pragma unroll
-        for (int i = 0; i < HB; ++i) l2[i] = load_l2(a, 32 * r, row + 16 * i, lane);
+        for (int i = 0; i < HB; ++i) l2[r][i] = load_l2(a, 32 * r, row + 16 * i, lane);
     };
     load_x(k0);
     if (passes) {
@@ -579,41 +581,39 @@ __global__ __launch_bounds__(512, XK == X_F32 && LP == 1 ? 4 : 2) void k_rows_sp
     for (int t = 0; t < TB; ++t)
 #pragma unroll
         for (int i = 0; i < HB; ++i) part[((w * TB + t) * HB + i) * 64 + lane] = wk ? acc[t][i] : acc[t][HB + i];
-    v4f y[TB][HB];
 #pragma unroll
     for (int r = 0; r < LP; ++r) {
         if (r && r >= passes) break;
-        if (r) {
-            load_l2s(r);
-            __syncthreads();
+        if (r) load_l2s(r);
+#pragma unroll
+        for (int t = 0; t < TB; ++t) us[((r * 8 + w) * TB + t) * 64 + lane] = u[r][t];
+    }
+    __syncthreads();
+    v4f y[TB][HB];
+#pragma unroll
+    for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int i = 0; i < HB; ++i) {
+            const v4f other = part[(((w ^ 4) * TB + t) * HB + i) * 64 + lane];
+            y[t][i] = wk ? other + acc[t][HB + i] : acc[t][i] + other;
         }
+    // rank block b of 32 lies with the waves 4 b .. 4 b + 3, a share of the steps each
+    const int from = u_place(lane), base = 4 * (from >> 6) * TB * 64 + (from & 63);
 #pragma unroll
-        for (int t = 0; t < TB; ++t) us[(w * TB + t) * 64 + lane] = u[r][t];
-        __syncthreads();
-        if (r == 0) {
-#pragma unroll
-            for (int t = 0; t < TB; ++t)
-#pragma unroll
-                for (int i = 0; i < HB; ++i) {
-                    const v4f other = part[(((w ^ 4) * TB + t) * HB + i) * 64 + lane];
-                    y[t][i] = wk ? other + acc[t][HB + i] : acc[t][i] + other;
-                }
-        }
-        if (!passes) break;
-        // rank block b of 32 lies with the waves 4 b .. 4 b + 3, a share of the steps each
-        const int from = u_place(lane), base = 4 * (from >> 6) * TB * 64 + (from & 63);
+    for (int r = 0; r < LP; ++r) {
+        if (r ? r >= passes : !passes) break;
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
             v4f u0 = {0.0f, 0.0f, 0.0f, 0.0f}, u1 = u0;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
-                u0 += us[base + (i * TB + t) * 64];
-                u1 += us[base + (i * TB + t) * 64 + 16];
+                u0 += us[base + ((r * 8 + i) * TB + t) * 64];
+                u1 += us[base + ((r * 8 + i) * TB + t) * 64 + 16];
             }
             uint4 up[3];
             split_u(u0, u1, a.rank - 32 * r - 8 * (lane >> 4), up);
 #pragma unroll
-            for (int i = 0; i < HB; ++i) y[t][i] = low_rank(l2[i], up, y[t][i]);
+            for (int i = 0; i < HB; ++i) y[t][i] = low_rank(l2[r][i], up, y[t][i]);
         }
     }
     if (a.slices > 1) {
@@ -674,7 +674,10 @@ void launch_split(RowsArgs a, const SplitPlan& p, hipStream_t st) {
 //    11.5 / 11.0; 8 rows 2080 -> 4999 5.9 / 7.1, 5120 -> 5120 9.1 / 8.7.  Without
 //    low ranks: 16 rows 5120 -> 5120 6.8 / 8.2, 10240 -> 5120 10.0 / 10.9, 13824 ->
 //    5120 12.3 / 12.0; 8 rows 16384 -> 5120 10.8 / 12.7; 4 rows 5120 -> 10240 8.0 /
-//    9.4, 13824 -> 10240 16.5 / 15.8.  fp32 has three parts a row, so four rows at most.
+//    9.4, 13824 -> 10240 16.5 / 15.8.  Rank
+//    64: one row 928 -> 3265 5.3 / 6.3, 16 rows 1536 -> 1536 6.3 / 6.6, 2080 -> 4999
+//    8.5 / 8.5, one row 2976 -> 1536 7.4 / 7.2; rank 128: 1536 -> 1536 8.3 / 7.5.
+//    fp32 has three parts a row, so four rows at most.
 //  - 64 output channels to a workgroup halve the readings of L1 and x, but leave
 //    CUs idle for few channels.  32 / 64 channels: one row 5120 -> 5120 8.2 / 9.0,
 //    1536 -> 8960 6.3 / 5.4, 5120 -> 13824 13.2 / 10.0.
@@ -688,8 +691,8 @@ void launch_split(RowsArgs a, const SplitPlan& p, hipStream_t st) {
 template <int XK>
 hipError_t launch_rows_product(const RowsArgs& a, const SplitPlan& p, hipStream_t st) {
     constexpr int P = XK == X_F32 ? 3 : 1;
-    const int most = a.rp ? (a.N == 1 ? 48 : 24) : a.Co >= 8192 ? 60 : a.N <= 8 ? 128 : 100;
-    const bool direct = a.N <= (P == 1 ? 16 : 4) && a.rp <= 32 && a.nks <= most;
+    const int most = a.rp > 32 ? 14 : a.rp ? (a.N == 1 ? 48 : 24) : a.Co >= 8192 ? 60 : a.N <= 8 ? 128 : 100;
+    const bool direct = a.N <= (P == 1 ? 16 : 4) && a.rp <= 64 && a.nks <= most;
     if (direct) {
         const auto go = [&](auto lr, auto rb) {
             constexpr int LR = decltype(lr)::value, RB = decltype(rb)::value, D = LR || P == 3 ? 1 : 2, W = LR || RB == 4 ? 8 : 16;
@@ -698,11 +701,11 @@ hipError_t launch_rows_product(const RowsArgs& a, const SplitPlan& p, hipStream_
             else if constexpr (P == 1) launch_direct<XK, 16, LR, RB, W, 1>(a, st);
         };
         const std::integral_constant<int, 0> none;
-        const std::integral_constant<int, 1> some;
+        const std::integral_constant<int, 1> one;
         const std::integral_constant<int, 2> two;
         const std::integral_constant<int, 4> four;
-        if (a.Co >= 8192) a.rp ? go(some, four) : go(none, four);
-        else a.rp ? go(some, two) : go(none, two);
+        if (a.Co >= 8192) a.rp > 32 ? go(two, four) : a.rp ? go(one, four) : go(none, four);
+        else a.rp > 32 ? go(two, two) : a.rp ? go(one, two) : go(none, two);
     } else {
         if (p.tb == 1) launch_split<XK, 1, 2>(a, p, st);
         else if constexpr (P == 1) p.rb == 2 ? launch_split<XK, 2, 2>(a, p, st) : launch_split<XK, 2, 4>(a, p, st);
