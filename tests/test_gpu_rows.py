@@ -81,7 +81,8 @@ SHAPES = [  # n, ci, co, rank
     # one row with low ranks up to 48 steps, and past them; the largest rank
     (1, 6144, 40, 8), (1, 6176, 40, 8), (2, 2976, 129, 32), (2, 3136, 129, 32), (1, 640, 200, 128), (40, 9000 // 32 * 32, 513, 128),
     # 33 to 64 ranks in the form of few rows, up to 14 steps and past them, and 65
-    (1, 96, 40, 33), (3, 1792, 300, 64), (16, 1056, 8200, 64), (1, 1824, 77, 48), (4, 640, 129, 64), (2, 640, 129, 65)]
+    (1, 96, 40, 33), (3, 1792, 300, 64), (16, 1056, 8200, 64), (1, 1824, 77, 48), (4, 640, 129, 64), (2, 640, 129, 65),
+    (16, 992, 8200, 64), (9, 992, 100, 50), (5, 1024, 70, 8), (7, 1056, 70, 8), (16, 2176, 100, 0), (6, 2208, 8192, 0)]
 
 
 @pytest.mark.parametrize("n,ci,co,rank", SHAPES)

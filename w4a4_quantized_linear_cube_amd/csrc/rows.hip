@@ -289,8 +289,8 @@ __device__ __forceinline__ void store_y(const RowsArgs& a, int n, int j, v4f y) 
 // Forming U in a launch of its own instead costs 2.8 to 3.1 us.
 template <int XK, int N16, int LR, int RB, int W, int D>
 __global__ __launch_bounds__(64 * W) void k_rows_direct(RowsArgs a) {
-    constexpr int P = XK == X_F32 ? 3 : 1, G = 16 / (N16 * P), NI = (G * N16 + 3) / 4, SUMS = RB + 2 * LR;
-    constexpr int SLOTS = 16 * 17 > 64 * SUMS ? 16 * 17 : 64 * SUMS;
+    constexpr int P = XK == X_F32 ? 3 : 1, G = N16 * P > 16 ? 1 : 16 / (N16 * P), NI = (G * N16 + 3) / 4, SUMS = RB + 2 * LR;
+    constexpr int STAGED = G * P * N16 * 17, SLOTS = STAGED > 64 * SUMS ? STAGED : 64 * SUMS;
     __shared__ uint4 lds[W][SLOTS];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     // workgroups go to the 8 XCDs in turn; an XCD takes neighbouring tiles,
@@ -671,13 +671,15 @@ void launch_split(RowsArgs a, const SplitPlan& p, hipStream_t st) {
 //    of its workgroups reads all of L1 and x, so it pays up to a number of K
 //    steps that depends on what it reads.  Direct / split: one row 1536 -> 1536
 //    4.1 / 5.6, 5120 -> 5120 8.2 / 8.4, 5120 -> 13824 10.0 / 11.8, 8960 -> 5120
-//    11.5 / 11.0; 8 rows 2080 -> 4999 5.9 / 7.1, 5120 -> 5120 9.1 / 8.7.  Without
+//    11.5 / 9.8; 8 rows 2080 -> 4999 5.9 / 7.1, 5120 -> 5120 9.1 / 8.7.  Without
 //    low ranks: 16 rows 5120 -> 5120 6.8 / 8.2, 10240 -> 5120 10.0 / 10.9, 13824 ->
 //    5120 12.3 / 12.0; 8 rows 16384 -> 5120 10.8 / 12.7; 4 rows 5120 -> 10240 8.0 /
 //    9.4, 13824 -> 10240 16.5 / 15.8.  Rank
 //    64: one row 928 -> 3265 5.3 / 6.3, 16 rows 1536 -> 1536 6.3 / 6.6, 2080 -> 4999
 //    8.5 / 8.5, one row 2976 -> 1536 7.4 / 7.2; rank 128: 1536 -> 1536 8.3 / 7.5.
-//    fp32 has three parts a row, so four rows at most.
+//    fp32 rows have three parts, and 5 to 16 of them: 16 rows 928 -> 3265 5.6 / 7.5,
+//    1536 -> 1536 7.2 / 7.2; without low ranks 2080 -> 4999 7.6 / 8.0, 2976 -> 1536
+//    7.4 / 7.2.
 //  - 64 output channels to a workgroup halve the readings of L1 and x, but leave
 //    CUs idle for few channels.  32 / 64 channels: one row 5120 -> 5120 8.2 / 9.0,
 //    1536 -> 8960 6.3 / 5.4, 5120 -> 13824 13.2 / 10.0.
@@ -691,14 +693,17 @@ void launch_split(RowsArgs a, const SplitPlan& p, hipStream_t st) {
 template <int XK>
 hipError_t launch_rows_product(const RowsArgs& a, const SplitPlan& p, hipStream_t st) {
     constexpr int P = XK == X_F32 ? 3 : 1;
-    const int most = a.rp > 32 ? 14 : a.rp ? (a.N == 1 ? 48 : 24) : a.Co >= 8192 ? 60 : a.N <= 8 ? 128 : 100;
-    const bool direct = a.N <= (P == 1 ? 16 : 4) && a.rp <= 64 && a.nks <= most;
+    int most;                                              // K steps the direct form takes
+    if (P > 1 && a.N > 4) most = a.rp ? 8 : 17;
+    else if (a.rp) most = a.rp > 32 ? 14 : a.N == 1 ? 48 : 24;
+    else most = a.Co >= 8192 ? 60 : a.N <= 8 ? 128 : 100;
+    const bool direct = a.N <= 16 && a.rp <= 64 && a.nks <= most;
     if (direct) {
         const auto go = [&](auto lr, auto rb) {
             constexpr int LR = decltype(lr)::value, RB = decltype(rb)::value, D = LR || P == 3 ? 1 : 2, W = LR || RB == 4 ? 8 : 16;
             if (a.N == 1) launch_direct<XK, 1, LR, RB, W, D>(a, st);
             else if (a.N <= 4) launch_direct<XK, 4, LR, RB, W, D>(a, st);
-            else if constexpr (P == 1) launch_direct<XK, 16, LR, RB, W, 1>(a, st);
+            else launch_direct<XK, 16, LR, RB, P == 1 ? W : 8, 1>(a, st);
         };
         const std::integral_constant<int, 0> none;
         const std::integral_constant<int, 1> one;
