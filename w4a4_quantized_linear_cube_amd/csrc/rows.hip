@@ -49,7 +49,7 @@ struct SplitPlan {
 //    where two fit, in fp32 (64 rows 5120 -> 5120: 480 of 14 steps 21.2, 160 of 40
 //    25.3; in bf16 64 rows 1536 -> 8960: 420 of 4 steps 14.4, 140 of 12 9.0).
 // Over 59 shapes the choice is within 0.6 % of the best slice length on average.
-SplitPlan plan_split(int64_t N, int64_t Co, int nks, int rp, int parts) {
+static SplitPlan plan_split(int64_t N, int64_t Co, int nks, int rp, int parts) {
     SplitPlan p;
     p.tb = N <= 16 || parts > 1 ? 1 : 2;
     p.groups = (int)((N + 16 * p.tb - 1) / (16 * p.tb));
