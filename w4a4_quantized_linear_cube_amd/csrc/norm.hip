@@ -217,17 +217,19 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm8(NormArgs a) 
 // C / 8 chunks over TPR threads: MIN to MAX each.  A launch takes fewer than
 // 2^32 threads, so more rows than that are several launches.
 template <class T, int TPR, int MIN, int MAX, bool NT>
-void launch_norm(NormArgs a, hipStream_t st) {
+hipError_t launch_norm(NormArgs a, hipStream_t st) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1, THREADS = TPR < 256 ? 256 : TPR;
     constexpr long long MOST = (1ll << 31) / THREADS;
     const int ch = (a.C / 8 + TPR - 1) / TPR;
     const auto go = [&](unsigned grid) {
-        if constexpr (MIN <= 1 && MAX > 1) if (ch == 1) return k_rmsnorm8<T, TPR, 1, NT><<<grid, THREADS, 0, st>>>(a);
-        if constexpr (MIN <= 2 && MAX > 2) if (ch == 2) return k_rmsnorm8<T, TPR, 2, NT><<<grid, THREADS, 0, st>>>(a);
-        if constexpr (MIN <= 3 && MAX > 3) if (ch == 3) return k_rmsnorm8<T, TPR, 3, NT><<<grid, THREADS, 0, st>>>(a);
-        k_rmsnorm8<T, TPR, MAX, NT><<<grid, THREADS, 0, st>>>(a);
+        if constexpr (MIN <= 1 && MAX > 1) if (ch == 1) return launch(k_rmsnorm8<T, TPR, 1, NT>, grid, THREADS, st, a);
+        if constexpr (MIN <= 2 && MAX > 2) if (ch == 2) return launch(k_rmsnorm8<T, TPR, 2, NT>, grid, THREADS, st, a);
+        if constexpr (MIN <= 3 && MAX > 3) if (ch == 3) return launch(k_rmsnorm8<T, TPR, 3, NT>, grid, THREADS, st, a);
+        return launch(k_rmsnorm8<T, TPR, MAX, NT>, grid, THREADS, st, a);
     };
-    for (; a.first < a.N; a.first += MOST * RPB) go((unsigned)std::min(MOST, (a.N - a.first + RPB - 1) / RPB));
+    hipError_t e = hipSuccess;
+    for (; a.first < a.N && e == hipSuccess; a.first += MOST * RPB) e = go((unsigned)std::min(MOST, (a.N - a.first + RPB - 1) / RPB));
+    return e;
 }
 
 // Rows of up to 64 chunks: one to a wave, or several, with as many lanes to a
@@ -235,11 +237,11 @@ void launch_norm(NormArgs a, hipStream_t st) {
 // rows and 64 for many / by these: 4096 x 128 6.1 / 3.1 us, 16384 x 64 16.4 / 3.6,
 // 524288 x 128 204 / 77, 1024 x 512 3.5 / 3.3; 65536 x 512 38.3 / 38.3.
 template <class T, bool NT>
-void launch_short(const NormArgs& a, hipStream_t st) {
-    if (a.C <= 64) launch_norm<T, 8, 1, 1, NT>(a, st);
-    else if (a.C <= 128) launch_norm<T, 16, 1, 1, NT>(a, st);
-    else if (a.C <= 256) launch_norm<T, 32, 1, 1, NT>(a, st);
-    else launch_norm<T, 64, 1, 1, NT>(a, st);
+hipError_t launch_short(const NormArgs& a, hipStream_t st) {
+    if (a.C <= 64) return launch_norm<T, 8, 1, 1, NT>(a, st);
+    if (a.C <= 128) return launch_norm<T, 16, 1, 1, NT>(a, st);
+    if (a.C <= 256) return launch_norm<T, 32, 1, 1, NT>(a, st);
+    return launch_norm<T, 64, 1, 1, NT>(a, st);
 }
 
 // Few longer rows are bound by their own latency, so a row gets as many threads as it
@@ -254,21 +256,12 @@ void launch_short(const NormArgs& a, hipStream_t st) {
 template <class T>
 hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
     const bool few = a.N * a.C <= (3ll << 20);
-    if (a.C <= 512) {
-        few ? launch_short<T, false>(a, st) : launch_short<T, true>(a, st);
-    } else if (few) {
-        if (a.C <= 2048) launch_norm<T, 256, 1, 1, false>(a, st);
-        else launch_norm<T, 1024, 1, 4, false>(a, st);
-    } else if (a.C <= 2048) {
-        launch_norm<T, 64, 2, 4, true>(a, st);
-    } else if (a.C <= 8192) {
-        launch_norm<T, 256, 2, 4, true>(a, st);
-    } else if (a.C <= 16384) {
-        launch_norm<T, 512, 3, 4, true>(a, st);
-    } else {
-        launch_norm<T, 1024, 3, 4, true>(a, st);
-    }
-    return hipGetLastError();
+    if (a.C <= 512) return few ? launch_short<T, false>(a, st) : launch_short<T, true>(a, st);
+    if (few) return a.C <= 2048 ? launch_norm<T, 256, 1, 1, false>(a, st) : launch_norm<T, 1024, 1, 4, false>(a, st);
+    if (a.C <= 2048) return launch_norm<T, 64, 2, 4, true>(a, st);
+    if (a.C <= 8192) return launch_norm<T, 256, 2, 4, true>(a, st);
+    if (a.C <= 16384) return launch_norm<T, 512, 3, 4, true>(a, st);
+    return launch_norm<T, 1024, 3, 4, true>(a, st);
 }
 
 }  // namespace

@@ -651,19 +651,18 @@ __global__ __launch_bounds__(512, XK == X_F32 && LP == 1 ? 4 : 2) void k_rows_sp
 }
 
 template <int XK, int N16, int LR, int RB, int W, int D>
-void launch_direct(RowsArgs a, hipStream_t st) {
+hipError_t launch_direct(RowsArgs a, hipStream_t st) {
     a.tiles = (a.Co + 16 * RB - 1) / (16 * RB);
-    k_rows_direct<XK, N16, LR, RB, W, D><<<(unsigned)round_up(a.tiles, 8), 64 * W, 0, st>>>(a);
+    return launch(k_rows_direct<XK, N16, LR, RB, W, D>, dim3((unsigned)round_up(a.tiles, 8)), 64 * W, st, a);
 }
 
 template <int XK, int TB, int RB>
-void launch_split(RowsArgs a, const SplitPlan& p, hipStream_t st) {
+hipError_t launch_split(RowsArgs a, const SplitPlan& p, hipStream_t st) {
     a.tiles = p.tiles;
     a.slices = p.slices;
     a.per = p.per;
     const dim3 grid((unsigned)round_up(p.tiles * p.slices, 8), (unsigned)p.groups);
-    if (a.rp <= 32) k_rows_split<XK, TB, 1, RB><<<grid, 512, 0, st>>>(a);
-    else k_rows_split<XK, TB, 4, RB><<<grid, 512, 0, st>>>(a);
+    return launch(a.rp <= 32 ? k_rows_split<XK, TB, 1, RB> : k_rows_split<XK, TB, 4, RB>, grid, 512, st, a);
 }
 
 // Measured at bf16 rows, rank 32 unless said otherwise (us, a captured run of calls):
@@ -701,21 +700,21 @@ hipError_t launch_rows_product(const RowsArgs& a, const SplitPlan& p, hipStream_
     if (direct) {
         const auto go = [&](auto lr, auto rb) {
             constexpr int LR = decltype(lr)::value, RB = decltype(rb)::value, D = LR || P == 3 ? 1 : 2, W = LR || RB == 4 ? 8 : 16;
-            if (a.N == 1) launch_direct<XK, 1, LR, RB, W, D>(a, st);
-            else if (a.N <= 4) launch_direct<XK, 4, LR, RB, W, D>(a, st);
-            else launch_direct<XK, 16, LR, RB, P == 1 ? W : 8, 1>(a, st);
+            if (a.N == 1) return launch_direct<XK, 1, LR, RB, W, D>(a, st);
+            if (a.N <= 4) return launch_direct<XK, 4, LR, RB, W, D>(a, st);
+            return launch_direct<XK, 16, LR, RB, P == 1 ? W : 8, 1>(a, st);
         };
         const std::integral_constant<int, 0> none;
         const std::integral_constant<int, 1> one;
         const std::integral_constant<int, 2> two;
         const std::integral_constant<int, 4> four;
-        if (a.Co >= 8192) a.rp > 32 ? go(two, four) : a.rp ? go(one, four) : go(none, four);
-        else a.rp > 32 ? go(two, two) : a.rp ? go(one, two) : go(none, two);
-    } else {
-        if (p.tb == 1) launch_split<XK, 1, 2>(a, p, st);
-        else if constexpr (P == 1) p.rb == 2 ? launch_split<XK, 2, 2>(a, p, st) : launch_split<XK, 2, 4>(a, p, st);
+        if (a.Co >= 8192) return a.rp > 32 ? go(two, four) : a.rp ? go(one, four) : go(none, four);
+        return a.rp > 32 ? go(two, two) : a.rp ? go(one, two) : go(none, two);
     }
-    return hipGetLastError();
+    if constexpr (P == 1) {
+        if (p.tb == 2) return p.rb == 2 ? launch_split<XK, 2, 2>(a, p, st) : launch_split<XK, 2, 4>(a, p, st);
+    }
+    return launch_split<XK, 1, 2>(a, p, st);
 }
 
 // Canonical codes [Co][Ci / 2] and scale codes [Co][Ci / 32] to the step-major layout.
