@@ -236,6 +236,15 @@ dq_status upload_factors(dq_weights* w, const uint16_t* l1_host, const uint16_t*
 // DQ_OK for the index of a gfx950 device (asked of the runtime once per device; norm.hip).
 dq_status known_device(int device);
 
+// A launch of one argument by the runtime's own call: 2.15 us of the host,
+// against 2.3 by <<< >>>, which stacks and unstacks the launch's shape (a kernel
+// with any argument costs 1.6 us more than one without, whatever its size).
+template <class A>
+hipError_t launch(void (*kernel)(A), dim3 grid, unsigned threads, hipStream_t st, A a) {
+    void* p[] = {&a};
+    return hipLaunchKernel((const void*)kernel, grid, dim3(threads), p, 0, st);
+}
+
 // A caller's array: n rows of `bytes` bytes, `pitch` bytes apart (none where p is null).
 struct Span {
     const void* p;
@@ -252,15 +261,6 @@ inline bool overlap(const Span& a, const Span& b) {
     const uint64_t pitch = (uint64_t)a.pitch, d = (uint64_t)(pb - pa) % pitch;   // where b's columns begin in a's rows
     const uint64_t e = pb >= pa ? d : (pitch - (uint64_t)(pa - pb) % pitch) % pitch;
     return e < (uint64_t)a.bytes || e + (uint64_t)b.bytes > pitch;
-}
-
-// A launch of one argument by the runtime's own call: 2.15 us of the host,
-// against 2.3 by <<< >>>, which stacks and unstacks the launch's shape (a kernel
-// with any argument costs 1.6 us more than one without, whatever its size).
-template <class A>
-hipError_t launch(void (*kernel)(A), dim3 grid, unsigned threads, hipStream_t st, A a) {
-    void* p[] = {&a};
-    return hipLaunchKernel((const void*)kernel, grid, dim3(threads), p, 0, st);
 }
 
 // Makes a handle's device current for the scope and restores the caller's.
