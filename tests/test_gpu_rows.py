@@ -493,3 +493,22 @@ def test_host_threads(dqm):
     assert not errors, errors
     for _, y, _ in jobs:
         _check(y, x64, rc, rs, l1, l2, 1, "f32")
+
+
+@pytest.mark.parametrize("n,ci,co,rank", [(4096, 160, 130, 32), (4095, 96, 70, 0), (2, 65536, 40, 32), (16, 65536, 33, 0), (33, 65536, 20, 5)])
+@pytest.mark.parametrize("kind", ["bf16", "f32", "mx8"])
+def test_largest_sizes(dqm, n, ci, co, rank, kind):
+    """The most rows a workspace takes, and the longest K."""
+    _say(f"largest {n} {ci}->{co} rank {rank} {kind}")
+    w, rc, rs, l1, l2 = _weight(dqm, ci, co, rank, 5)
+    args, x64 = _x(n, ci, kind, 6)
+    y = torch.full((n + 1, co), float("nan"), device=DEV)
+    _call(dqm, w, args, dqm.dq_rows_create(w, n), y[:n])
+    _check(y[:n], x64, rc, rs, l1, l2, 3 if kind == "f32" else 1, "f32")
+    assert torch.isnan(y[n]).all()
+
+
+def test_longer_rows_are_refused(dqm):
+    w, *_ = _weight(dqm, 65568, 20, 0, 5)
+    with pytest.raises(dqm.DQError, match="65536"):
+        dqm.dq_rows_create(w, 1)
