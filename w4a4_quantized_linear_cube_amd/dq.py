@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 from types import SimpleNamespace
 from typing import Optional, Sequence, Tuple
 
@@ -51,14 +52,19 @@ def library_path() -> str:
 
 
 def load():
-    """Load libdq.so and the binding's native part (raises if they have not been built)."""
+    """Load libdq.so (raises if it has not been built), and the native
+    marshalling of the small calls where torch and _dqcall.so are there; without
+    it those calls take a few us more of the host."""
     global _LIB, _CALL
     if _LIB is not None:
         return _LIB
     path = library_path()
     if not os.path.exists(path):
         raise RuntimeError(f"{path} is not built; run __graft_entry__.build()")
-    import torch  # noqa: F401  (before libdq.so, which then shares the HIP runtime that torch brings)
+    try:
+        import torch                # (before libdq.so, which then shares the HIP runtime that torch brings)
+    except ImportError:
+        torch = None                # (the entry points themselves do not need it)
     lib = ctypes.CDLL(path)
     P, I32, I64, U64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
     PP = ctypes.POINTER(ctypes.c_void_p)
@@ -112,8 +118,13 @@ def load():
         f = getattr(lib, name)
         f.argtypes = args
         f.restype = res
-    from . import _dqcall
-    _CALL = _dqcall
+    if torch is not None:
+        try:
+            from . import _dqcall
+            _CALL = _dqcall
+        except ImportError as e:
+            warnings.warn(f"the small calls' native marshalling (_dqcall.so) is not there, they take a few us more: {e}; "
+                          "run __graft_entry__.build()", RuntimeWarning, stacklevel=2)
     _LIB = lib
     return lib
 
@@ -651,8 +662,9 @@ def dq_rmsnorm8(x, gain, eps: float, codes=None, scales=None, residual=None, h=N
     plain values y, or both; h receives x + residual (it, or y, may be x or
     residual itself).  gain [C] in bf16 or fp32, or None."""
     f = "dq_rmsnorm8"
-    status = (_CALL or _native()).rmsnorm8(x, gain, eps, codes, scales, residual, h, y, group,
-                                           None if stream is None else getattr(stream, "cuda_stream", stream))
+    call = _CALL or _native()
+    status = None if call is None else call.rmsnorm8(x, gain, eps, codes, scales, residual, h, y, group,
+                                                     None if stream is None else getattr(stream, "cuda_stream", stream))
     if status is not None:
         return _check(status, f) if status else None
     import torch
