@@ -3,10 +3,14 @@ part of the Python binding, with g++ against torch's headers.
 
 Each source compiles to its own object in `_build/` (in parallel), then one
 link each makes the shared libraries next to this file.  Every call rebuilds.
+_dqcall.so is left out, with a notice, where what it needs is not there
+(libdq.so does not need it, and dq.py goes without).
 """
 from __future__ import annotations
 
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -32,9 +36,23 @@ FLAGS = [
 ]
 
 
-def _torch_dir() -> str:
-    import importlib.util
-    return os.path.dirname(importlib.util.find_spec("torch").origin)
+def _torch_dir():
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec else None
+
+
+def _call_lacks():
+    """What _dqcall.so needs and this machine has not, or None."""
+    t = _torch_dir()
+    if shutil.which("g++") is None:
+        return "g++"
+    if t is None:
+        return "torch"
+    for name, path in (("torch's HIP headers", os.path.join(t, "include", "c10", "hip", "HIPStream.h")),
+                       ("Python's headers", os.path.join(sysconfig.get_paths()["include"], "Python.h"))):
+        if not os.path.isfile(path):
+            return name
+    return None
 
 
 def _call_flags():
@@ -44,21 +62,24 @@ def _call_flags():
             "-I", os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include")]
 
 
+def _start(cmd, verbose):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     procs = []
+    lacks = _call_lacks()
     call_obj = os.path.join(BUILD, "binding.o")
-    procs.append(("binding.cpp", subprocess.Popen(["g++", *_call_flags(), "-c", os.path.join(CSRC, "binding.cpp"), "-o", call_obj],
-                                                  stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    call = None if lacks else _start(["g++", *_call_flags(), "-c", os.path.join(CSRC, "binding.cpp"), "-o", call_obj], verbose)
     objs = []
     for src in SOURCES:
         obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
         objs.append(obj)
         lang = ["-x", "hip"] if src.endswith(".hip") else []
-        cmd = [HIPCC, *FLAGS, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+        procs.append((src, _start([HIPCC, *FLAGS, *lang, "-c", os.path.join(CSRC, src), "-o", obj], verbose)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -68,6 +89,7 @@ def build(verbose: bool = False) -> str:
             print(out, file=sys.stderr, flush=True)
         if p.returncode:
             failed.append(src)
+    call_out = call.communicate()[0] if call else ""
     if failed:
         raise RuntimeError(f"hipcc failed for {failed}")
     tmp = LIB + ".tmp"
@@ -76,10 +98,20 @@ def build(verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    # (one of an older build would call the new library by the old arguments)
+    if os.path.exists(CALL_LIB):
+        os.remove(CALL_LIB)
+    if lacks:
+        print(f"_dqcall.so is left out: {lacks} not found", file=sys.stderr, flush=True)
+        return LIB
     tmp = CALL_LIB + ".tmp"
-    lib = os.path.join(_torch_dir(), "lib")
-    subprocess.run(["g++", "-shared", call_obj, "-o", tmp, "-L", HERE, "-ldq", "-Wl,-rpath,$ORIGIN", "-L", lib, "-lc10", "-lc10_hip",
-                    "-ltorch_cpu", "-ltorch_python"], check=True)
+    if call.returncode == 0:
+        call = _start(["g++", "-shared", call_obj, "-o", tmp, "-L", HERE, "-ldq", "-Wl,-rpath,$ORIGIN", "-L",
+                       os.path.join(_torch_dir(), "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"], verbose)
+        call_out = call.communicate()[0]
+    if call.returncode:
+        print(call_out, file=sys.stderr, flush=True)
+        raise RuntimeError("g++ failed for _dqcall.so (libdq.so is built)")
     os.replace(tmp, CALL_LIB)
     return LIB
 
