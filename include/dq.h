@@ -375,7 +375,10 @@ dq_status dq_linear_rows8(const dq_weights* w, const uint8_t* codes_dev, const u
  *   each 32 channels, or 64 (group = 64: stored at both 32-channel places);
  *   codes v 2^-e in E4M3, nearest, ties to even
  * Infinite and NaN elements of v get the E4M3 NaN code and do not enter the
- * scale.  Reproducible bit for bit (the one sum is kept in fp64).
+ * scale.  Repeated calls agree bit for bit, and a row's results do not depend
+ * on N or on the other rows: the one sum is kept in fp64, in an order that goes
+ * by C alone.  (Another implementation's order can move f by one unit in its
+ * last place, in about one row of 10^9.)
  *   x_dev, res_dev (or NULL), h_dev (or NULL), y_dev (or NULL; v rounded to dt):
  *         [N][C] of dtype dt, rows ld elements apart (ld >= C), 16-byte
  *         aligned rows; h_dev and y_dev may be x_dev or res_dev themselves

@@ -5,10 +5,13 @@
 //   f = fl32(1 / sqrt(s / C + eps)), formed in fp64 and rounded once
 //   v_c = fl32(fl32(h_c f) g_c);  MX-FP8 of v per 32 (or 64) channels
 //
-// The sum of squares is kept in fp64 so that f does not depend on the order
-// of the sum: every later step is one fp32 rounding per element, so codes and
-// scales are reproducible bit for bit by any implementation (an element next
-// to the border of two codes goes by the last bit of f).
+// The sum of squares is kept in fp64, in an order that goes by C alone: 8
+// channels one by one, and such chunks pairwise by the bits of their place,
+// lowest first.  So a row's results do not depend on the rows beside it,
+// whichever form they take.  Every later step is one fp32 rounding per element.
+// Another order moves the sum by some 2^-54 of it, and f by one unit in its
+// last place where it lies that near to a border of two fp32 values: about one
+// row in 10^9.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -103,6 +106,62 @@ __device__ __forceinline__ void load_gain(const NormArgs& a, int c, float* g) {
     }
 }
 
+// Sums over lanes, pairwise by the bits of a lane's place, lowest first.
+template <int CTRL>
+__device__ __forceinline__ double moved(double v) {
+    const v2w w = __builtin_bit_cast(v2w, v);
+    return __builtin_bit_cast(double, v2w{(uint32_t)__builtin_amdgcn_mov_dpp((int)w[0], CTRL, 0xF, 0xF, true),
+                                          (uint32_t)__builtin_amdgcn_mov_dpp((int)w[1], CTRL, 0xF, 0xF, true)});
+}
+// ... of the lane 16 (32) places on, for the lower of two rows (halves); both get the sum
+__device__ __forceinline__ double add_row(double v) {
+    const v2w w = __builtin_bit_cast(v2w, v);
+    const v2w lo = __builtin_amdgcn_permlane16_swap(w[0], w[0], false, false), hi = __builtin_amdgcn_permlane16_swap(w[1], w[1], false, false);
+    return __builtin_bit_cast(double, v2w{lo[0], hi[0]}) + __builtin_bit_cast(double, v2w{lo[1], hi[1]});
+}
+__device__ __forceinline__ double add_half(double v) {
+    const v2w w = __builtin_bit_cast(v2w, v);
+    const v2w lo = __builtin_amdgcn_permlane32_swap(w[0], w[0], false, false), hi = __builtin_amdgcn_permlane32_swap(w[1], w[1], false, false);
+    return __builtin_bit_cast(double, v2w{lo[0], hi[0]}) + __builtin_bit_cast(double, v2w{lo[1], hi[1]});
+}
+__device__ __forceinline__ double first_lane(double v) {
+    const v2w w = __builtin_bit_cast(v2w, v);
+    return __builtin_bit_cast(double, v2w{(uint32_t)__builtin_amdgcn_readfirstlane((int)w[0]), (uint32_t)__builtin_amdgcn_readfirstlane((int)w[1])});
+}
+// The sum of each N neighbouring lanes, in all of them.  (The lanes of a group
+// of 4 hold one sum already, so a mirrored half row serves for the lane 4
+// places on, and a mirrored row for that 8 places on.)
+template <int N>
+__device__ __forceinline__ double sum_lanes(double v) {
+    if constexpr (N > 1) v += moved<0xB1>(v);          // lane ^ 1
+    if constexpr (N > 2) v += moved<0x4E>(v);          // lane ^ 2
+    if constexpr (N > 4) v += moved<0x141>(v);
+    if constexpr (N > 8) v += moved<0x140>(v);
+    if constexpr (N > 16) v = add_row(v);
+    if constexpr (N > 32) v = add_half(v);
+    return v;
+}
+// The wave's sums of CH values, value i in lane i: from the first two steps on
+// a lane carries on with one value (its place's lowest bits), which takes half
+// the additions that each value by itself would (1024 x 5120 with plain values
+// 9.4 -> 9.2 us).  Lanes from 4 on hold sums in other orders.
+template <int CH>
+__device__ __forceinline__ double sum_wave(const double* q, int t) {
+    if constexpr (CH == 1) return sum_lanes<64>(q[0]);
+    const bool odd = t & 1, upper = t & 2;
+    double v = (odd ? q[1 % CH] : q[0]) + moved<0xB1>(odd ? q[0] : q[1 % CH]);
+    if constexpr (CH > 2) {
+        const double q3 = CH > 3 ? q[3 % CH] : 0.0;
+        const double u = (odd ? q3 : q[2 % CH]) + moved<0xB1>(odd ? q[2 % CH] : q3);
+        v = (upper ? u : v) + moved<0x4E>(upper ? v : u);
+    } else {
+        v += moved<0x4E>(v);
+    }
+    v += moved<0x12C>(v);                              // row rotated: the lane 4 places on
+    v += moved<0x128>(v);                              // ... 8 places on
+    return add_half(add_row(v));
+}
+
 // A row is held in registers by TPR threads, CH chunks of 8 channels each
 // (chunk i of thread t: channels 8 (i TPR + t) ..), so it is read once; a
 // group of 32 channels is 4 neighbouring lanes' chunk.
@@ -119,7 +178,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm8(NormArgs a) 
     const bool live = row < a.N;
     const int nch = a.C >> 3;
     float h[CH][8];
-    double s = 0.0;
+    double q[CH];                                   // sums of squares of the chunks
+#pragma unroll
+    for (int i = 0; i < CH; ++i) q[i] = 0.0;
     if (live) {
         const T* xp = (const T*)a.x + row * a.ldx;
 #pragma unroll
@@ -148,18 +209,22 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm8(NormArgs a) 
 #pragma unroll
         for (int i = 0; i < CH; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s = __builtin_fma((double)h[i][j], (double)h[i][j], s);
+            for (int j = 0; j < 8; ++j) q[i] = __builtin_fma((double)h[i][j], (double)h[i][j], q[i]);
     }
-#pragma unroll
-    for (int m = 1; m < (TPR < 64 ? TPR : 64); m <<= 1) s += __shfl_xor(s, m, 64);
-    if constexpr (WPR > 1) {
-        __shared__ double part[RPB * WPR];
-        const int w = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0) part[w] = s;
+    double s;
+    if constexpr (WPR > 1) {                        // (block of 64 chunks i WPR + w)
+        static_assert(RPB == 1 && CH * WPR <= 64);
+        __shared__ double part[CH * WPR];
+        s = sum_wave<CH>(q, t);
+        if ((t & 63) < CH) part[(t & 63) * WPR + (t >> 6)] = s;
         __syncthreads();
-        s = 0.0;
-#pragma unroll
-        for (int i = 0; i < WPR; ++i) s += part[(w / WPR) * WPR + i];
+        s = (t & 63) < CH * WPR ? part[t & 63] : 0.0;
+        s = first_lane(sum_lanes<(CH * WPR > 32 ? 64 : CH * WPR > 16 ? 32 : CH * WPR > 8 ? 16 : 8)>(s));
+    } else if constexpr (CH > 1) {
+        s = sum_wave<CH>(q, t);
+        s = first_lane(sum_lanes<4>((t & 3) < CH ? s : 0.0));
+    } else {
+        s = sum_lanes<(TPR < 64 ? TPR : 64)>(q[0]);
     }
     if (!live) return;
     const float f = (float)(1.0 / sqrt(s / (double)a.C + a.eps));
@@ -234,8 +299,8 @@ hipError_t launch_norm(NormArgs a, hipStream_t st) {
 
 // Rows of up to 64 chunks: one to a wave, or several, with as many lanes to a
 // row as it has chunks.  In bf16 with a residual, by 256 threads a row for few
-// rows and 64 for many / by these: 4096 x 128 6.1 / 3.1 us, 16384 x 64 16.4 / 3.6,
-// 524288 x 128 204 / 77, 1024 x 512 3.5 / 3.3; 65536 x 512 38.3 / 38.3.
+// rows and 64 for many / by these: 4096 x 128 5.6 / 3.0 us, 16384 x 64 14.9 / 3.3,
+// 524288 x 128 221 / 81, 1024 x 512 3.3 / 3.0; 65536 x 512 43.9 / 43.0.
 template <class T, bool NT>
 hipError_t launch_short(const NormArgs& a, hipStream_t st) {
     if (a.C <= 64) return launch_norm<T, 8, 1, 1, NT>(a, st);
@@ -247,8 +312,8 @@ hipError_t launch_short(const NormArgs& a, hipStream_t st) {
 // Few longer rows are bound by their own latency, so a row gets as many threads as it
 // has chunks; many by HBM, so a thread holds up to four chunks, and the
 // outputs bypass the caches.  Measured in bf16 with a residual, few / many form:
-//   1 x 5120 3.2 / 4.2 us; 64 x 1536 2.8 / 4.5 us; 256 x 5120 with plain values
-//   4.6 / 5.3 us; 1024 x 5120 the same 11.2 / 8.8 us; 4096 x 1536 10.2 / 10.0 us.
+//   1 x 5120 3.1 / 4.4 us; 64 x 1536 2.9 / 4.7 us; 256 x 5120 with plain values
+//   4.5 / 5.3 us; 1024 x 5120 the same 11.1 / 9.2 us; 4096 x 1536 10.6 / 9.3 us.
 // Bypassing stores on 75600 x 5120: 480 -> 466 us (5.8 TB/s); bypassing loads
 // as well gain another 2 % there, but lose 12 % where the rows are still in the
 // memory-side cache (32760 x 1536 fp32: 44 -> 49 us), so they stay plain.
