@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -35,9 +36,10 @@ dq_status hip_fail(hipError_t e, const char* what) {
     return fail(DQ_ERR_DEVICE, std::string(what) + ": " + hipGetErrorString(e));
 }
 
-namespace {
-
-dq_status check_device(int device) {
+// gfx950 check of a device index, asked of the runtime once per device.
+dq_status known_device(int device) {
+    static std::atomic<uint64_t> known{0};
+    if (device >= 0 && device < 64 && (known.load(std::memory_order_relaxed) >> device & 1)) return DQ_OK;
     int n = 0;
     if (hipGetDeviceCount(&n) != hipSuccess || n <= 0) return fail(DQ_ERR_DEVICE, "no HIP device available");
     if (device < 0 || device >= n) return fail(DQ_ERR_INVALID_ARG, "device index out of range");
@@ -45,8 +47,11 @@ dq_status check_device(int device) {
     if (hipGetDeviceProperties(&prop, device) != hipSuccess) return fail(DQ_ERR_DEVICE, "hipGetDeviceProperties failed");
     if (std::strncmp(prop.gcnArchName, "gfx950", 6) != 0)
         return fail(DQ_ERR_UNSUPPORTED, std::string("device is ") + prop.gcnArchName + ", gfx950 required");
+    if (device < 64) known.fetch_or(uint64_t(1) << device, std::memory_order_relaxed);
     return DQ_OK;
 }
+
+namespace {
 
 // Zero-filled device allocation.
 template <class T>
@@ -262,7 +267,7 @@ static dq_status prepare_weights(const void* w_host, dq_dtype dt, int64_t Ci, in
     if (rank < 0 || rank > std::min(Ci, Co)) return fail(DQ_ERR_INVALID_ARG, "rank must be in [0, min(Ci, Co)]");
     if (rank > 128) return fail(DQ_ERR_INVALID_ARG, "rank must be <= 128");
     if (rank > 0 && (!l1_host || !l2_host)) return fail(DQ_ERR_INVALID_ARG, "factors are NULL");
-    dq_status st = check_device(device);
+    dq_status st = known_device(device);
     if (st != DQ_OK) return st;
     DeviceGuard dg(device);
     if (!dg.ok) return fail(DQ_ERR_DEVICE, "hipSetDevice failed");

@@ -233,7 +233,7 @@ dq_status plan_qact(const dq_weights* w, const dq_geom& geom, int core_group, in
 
 // Stores a weight's bf16 factors (host copies and padded device transposes).
 dq_status upload_factors(dq_weights* w, const uint16_t* l1_host, const uint16_t* l2_host);
-// DQ_OK for the index of a gfx950 device (asked of the runtime once per device; norm.hip).
+// DQ_OK for the index of a gfx950 device (asked of the runtime once per device).
 dq_status known_device(int device);
 
 // A launch of one argument by the runtime's own call: 2.15 us of the host,

@@ -15,9 +15,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
-#include <cstring>
 
 #include "dq.h"
 #include "dq_device.h"
@@ -330,21 +328,6 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
 }
 
 }  // namespace
-
-// gfx950 check of a device index, asked of the runtime once per device.
-dq_status known_device(int device) {
-    static std::atomic<uint64_t> known{0};
-    if (device >= 0 && device < 64 && (known.load(std::memory_order_relaxed) >> device & 1)) return DQ_OK;
-    int n = 0;
-    if (hipGetDeviceCount(&n) != hipSuccess || n <= 0) return fail(DQ_ERR_DEVICE, "no HIP device available");
-    if (device < 0 || device >= n) return fail(DQ_ERR_INVALID_ARG, "device index out of range");
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, device) != hipSuccess) return fail(DQ_ERR_DEVICE, "hipGetDeviceProperties failed");
-    if (std::strncmp(prop.gcnArchName, "gfx950", 6) != 0)
-        return fail(DQ_ERR_UNSUPPORTED, std::string("device is ") + prop.gcnArchName + ", gfx950 required");
-    if (device < 64) known.fetch_or(uint64_t(1) << device, std::memory_order_relaxed);
-    return DQ_OK;
-}
 
 }  // namespace dq
 

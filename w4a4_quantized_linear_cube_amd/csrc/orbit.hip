@@ -352,12 +352,8 @@ dq_status dq_orbit_prepare(const void* w_host, dq_dtype dt, int64_t Ci, int64_t 
             seen[(size_t)v] = 1;
         }
     }
-    int n = 0;
-    if (hipGetDeviceCount(&n) != hipSuccess || n <= 0) return fail(DQ_ERR_DEVICE, "no HIP device available");
-    if (device < 0 || device >= n) return fail(DQ_ERR_INVALID_ARG, "device index out of range");
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, device) != hipSuccess) return fail(DQ_ERR_DEVICE, "hipGetDeviceProperties failed");
-    if (std::strncmp(prop.gcnArchName, "gfx950", 6) != 0) return fail(DQ_ERR_UNSUPPORTED, "gfx950 required");
+    const dq_status st = known_device(device);
+    if (st != DQ_OK) return st;
     DeviceGuard dg(device);
     if (!dg.ok) return fail(DQ_ERR_DEVICE, "hipSetDevice failed");
     auto* o = new (std::nothrow) dq_orbit();
