@@ -151,6 +151,8 @@ struct dq_weights {
     uint16_t* l2t = nullptr;   // [Cop][rp]     L2^T bf16 (device)
     uint16_t* l1p = nullptr;   // L1^T in the order of 16x16x32 matrix operands (4-bit weights, device):
                                // [Kp/128][rp/16][f][lane][8], lane l: rank l % 16, channels 32 (l / 16) + 8 f .. + 7
+                               // (for few rows, which any 4-bit weight may meet: rank 32 adds 64 bytes a channel,
+                               // 1 % of the codes of 13824 outputs)
     std::vector<uint16_t> l1, l2;   // host copies [Ci][rank], [rank][Co]
     size_t bytes = 0;
 };
