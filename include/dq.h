@@ -323,8 +323,8 @@ dq_status dq_orbit_act_export(const dq_orbit_act* a, uint8_t* codes_host, float*
  *     y_n = x_n Q4(R) + (x_n L1) L2
  * to rows as they are (bf16 or fp32), or to rows in MX-FP8, as dq_rmsnorm8
  * writes them.  Products are exact, sums (U = x L1 included, which is not
- * rounded to bf16 here) are fp32 in a fixed order, and one rounding to y's
- * type ends them: repeated calls agree bit for bit. */
+ * rounded to bf16 here) are fp32 in an order that goes by N and the layer's sizes,
+ * and one rounding to y's type ends them: repeated calls agree bit for bit. */
 
 /* A weight that is already coded, in the layout dq_weights_export writes:
  *   rcodes_host  [Co][Ci/2] FP4 codes;  rscales_host [Co][Ci/32] scale codes
@@ -339,10 +339,11 @@ dq_status dq_import_weights(const uint8_t* rcodes_host, const uint8_t* rscales_h
 
 /* Workspace for up to max_rows rows (1 <= max_rows <= 4096) of a 4-bit weight
  * with Ci <= 65536, or of any other with the same Ci, Co and rank on its
- * device.  Tuned for up
- * to 64 rows; more than 16 are taken 32 at a time (16 of fp32 rows), each
- * group reading the weight again.  Must not be used by two streams at once (two captured graphs that
- * share one must not run at once either). */
+ * device.  Tuned for up to 64 rows; more than 16 are taken 32 at a time (16 of
+ * fp32 rows), each group reading the weight again: 256 bf16 rows 5120 -> 5120
+ * take 29 us, 1024 82 us, where dq_linear, which quantizes them, takes 70.
+ * Must not be used by two streams at once (two captured graphs that share one
+ * must not run at once either). */
 typedef struct dq_rows dq_rows;
 dq_status dq_rows_create(const dq_weights* w, int64_t max_rows, dq_rows** out);
 void dq_rows_destroy(dq_rows* a);

@@ -163,10 +163,10 @@ __device__ __forceinline__ double sum_wave(const double* q, int t) {
 // A row is held in registers by TPR threads, CH chunks of 8 channels each
 // (chunk i of thread t: channels 8 (i TPR + t) ..), so it is read once; a
 // group of 32 channels is 4 neighbouring lanes' chunk.
-// Many rows are bound by HBM: 75600 x 5120 bf16 moves 2.72 GB in 466 us, 5.8
+// Many rows are bound by HBM: 75600 x 5120 bf16 moves 2.72 GB in 464 us, 5.9
 // TB/s (a copy of 1 GiB reaches 4.8), 32760 x 1536 fp32 44 us, 5.7 TB/s.  One
 // row is bound by its chain of two loads, the sum across 16 waves and the
-// stores: 1 x 5120 3.0 us, where an empty kernel takes 2.3.
+// stores: 1 x 5120 2.7 us, where an empty kernel takes 2.3.
 template <class T, int TPR, int CH, bool NT>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm8(NormArgs a) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
