@@ -331,8 +331,8 @@ dq_status dq_orbit_act_export(const dq_orbit_act* a, uint8_t* codes_host, float*
  *   l1_host [Ci][rank], l2_host [rank][Co] bf16 bits (may be NULL when rank == 0)
  * for any entry point that takes a 4-bit weight.  R is what the codes stand
  * for (dq_weights_export then decodes it).  Requirements on Ci, Co and rank
- * as dq_prepare_weights_lowrank; DQ_ERR_INVALID_ARG for a scale code of 255.
- * The arrays' sizes cannot be checked here.  Synchronous. */
+ * as dq_prepare_weights_lowrank; DQ_ERR_INVALID_ARG for a scale code of 255 and
+ * for a weight of 2^128 or more (no fp32 or bf16 value).  The arrays' sizes cannot be checked here.  Synchronous. */
 dq_status dq_import_weights(const uint8_t* rcodes_host, const uint8_t* rscales_host, int64_t Ci, int64_t Co,
                             int32_t rank, const uint16_t* l1_host, const uint16_t* l2_host, int32_t device,
                             dq_weights** out);
@@ -355,10 +355,12 @@ void dq_rows_destroy(dq_rows* a);
  *   y_dev [N][Co] of dtype ydt, rows ldy elements apart (ldy >= Co), every
  *         element of the N rows written, nothing else; must not share memory
  *         with x (DQ_ERR_INVALID_ARG)
- * fp32 x is taken at its full precision, bits below 2^-133 apart; weights and
- * MX-FP8 values as bf16 holds them (exact from 2^-133 to 2^128, infinite from
- * there).  Infinite and NaN values stay in their rows.  Asynchronous on `stream`; allocates
- * nothing and can be captured into a HIP graph. */
+ * fp32 x is taken at its full precision, bits below 2^-133 apart; weights are
+ * exact (a prepared one whose residual rounds up to 2^128 is infinite, and in
+ * fp32 rows NaN); MX-FP8 values are as bf16 holds them, exact from 2^-133 to
+ * 2^128 and infinite from there.  Infinite and NaN values stay in their rows.
+ * Asynchronous on `stream`; allocates nothing and can be captured into a HIP
+ * graph. */
 dq_status dq_linear_rows(const dq_weights* w, const void* x_dev, dq_dtype dt, int64_t ldx, int64_t N, dq_rows* a,
                          void* y_dev, dq_dtype ydt, int64_t ldy, void* stream);
 /* The same for rows in MX-FP8: codes_dev [N][Ci] E4M3, 8-byte aligned;

@@ -12,9 +12,9 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <cstring>
 #include <memory>
 #include <new>
+#include <string>
 #include <type_traits>
 
 #include "dq.h"
@@ -807,8 +807,15 @@ dq_status dq_import_weights(const uint8_t* rcodes_host, const uint8_t* rscales_h
         return fail(DQ_ERR_INVALID_ARG, "rank must be in [0, min(Ci, Co, 128)]");
     if (rank > 0 && (!l1_host || !l2_host)) return fail(DQ_ERR_INVALID_ARG, "factors are NULL");
     const int64_t groups = Ci / 32;
-    if (std::memchr(rscales_host, 255, (size_t)(Co * groups)))
-        return fail(DQ_ERR_INVALID_ARG, "a scale code is 255 (not a number)");
+    uint8_t top = 0;
+    for (int64_t i = 0; i < Co * groups; ++i) top = std::max(top, rscales_host[i]);
+    if (top == 255) return fail(DQ_ERR_INVALID_ARG, "a scale code is 255 (not a number)");
+    if (top >= 253)                                // (4 2^126 and 2 2^127 are the first that bf16 cannot hold: codes 6 and 4)
+        for (int64_t i = 0; i < Co * groups; ++i)
+            for (int k = 0; rscales_host[i] >= 253 && k < 32; ++k)
+                if ((rcodes_host[i * 16 + k / 2] >> (k % 2 * 4) & 7) >= (rscales_host[i] == 253 ? 6 : 4))
+                    return fail(DQ_ERR_INVALID_ARG, "a weight reaches 2^128: output " + std::to_string(i / groups) + ", channel " +
+                                                        std::to_string(i % groups * 32 + k));
     dq_status st = known_device(device);
     if (st != DQ_OK) return st;
     DeviceGuard dg(device);
