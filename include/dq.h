@@ -332,7 +332,8 @@ dq_status dq_orbit_act_export(const dq_orbit_act* a, uint8_t* codes_host, float*
  * for any entry point that takes a 4-bit weight.  R is what the codes stand
  * for (dq_weights_export then decodes it).  Requirements on Ci, Co and rank
  * as dq_prepare_weights_lowrank; DQ_ERR_INVALID_ARG for a scale code of 255 and
- * for a weight of 2^128 or more (no fp32 or bf16 value).  The arrays' sizes cannot be checked here.  Synchronous. */
+ * for a weight of 2^128 or more (no fp32 or bf16 value).  The arrays' sizes
+ * cannot be checked here.  Synchronous. */
 dq_status dq_import_weights(const uint8_t* rcodes_host, const uint8_t* rscales_host, int64_t Ci, int64_t Co,
                             int32_t rank, const uint16_t* l1_host, const uint16_t* l2_host, int32_t device,
                             dq_weights** out);

@@ -118,6 +118,7 @@ def load():
         f = getattr(lib, name)
         f.argtypes = args
         f.restype = res
+    _LIB = lib
     if torch is not None:
         try:
             from . import _dqcall
@@ -125,7 +126,6 @@ def load():
         except ImportError as e:
             warnings.warn(f"the small calls' native marshalling (_dqcall.so) is not there, they take a few us more: {e}; "
                           "run __graft_entry__.build()", RuntimeWarning, stacklevel=2)
-    _LIB = lib
     return lib
 
 
