@@ -33,9 +33,11 @@
  *  - Streams are hipStream_t values passed as void*; NULL is the null stream.
  *  - All allocation happens in dq_prepare_weights*, dq_import_weights and the
  *    handles' dq_*_create; the hot calls (dq_quantize_act, dq_linear_forward,
- *    dq_linear, dq_linear_rows*, dq_rmsnorm8) allocate nothing.
+ *    dq_linear, dq_linear_rows*, dq_rmsnorm8, dq_norm_rope, dq_kv_*,
+ *    dq_attn_rows) allocate nothing.
  *  - A dq_weights is read-only after preparation and may be shared by
- *    streams; a dq_qact or dq_rows must not be used by two streams at once.
+ *    streams; a dq_qact, dq_rows or dq_attn must not be used by two streams at
+ *    once.
  */
 #ifndef DQ_H
 #define DQ_H
@@ -397,6 +399,152 @@ dq_status dq_linear_rows8(const dq_weights* w, const uint8_t* codes_dev, const u
 dq_status dq_rmsnorm8(const void* x_dev, int64_t ldx, const void* res_dev, int64_t ldr, dq_dtype dt, const void* gain_dev,
                       dq_dtype gain_dt, double eps, int64_t N, int64_t C, int32_t group, void* h_dev, int64_t ldh,
                       uint8_t* codes_dev, uint8_t* scales_dev, void* y_dev, int64_t ldy, int32_t device, void* stream);
+
+/* ---- heads: from the query, key and value projections to attention ----------
+ * Rows of heads [N][heads][head_dim] (head_dim 32, 64, 128 or 256) as a
+ * projection leaves them: the norm of each head or of the whole row, the
+ * rotation of its channels by the row's position, and keys and values kept as
+ * MX-FP8 or MX-FP4 codes in the pages of a cache, which dq_kv_read decodes and
+ * dq_attn_rows attends to.  All buffers are the caller's.  Nothing here
+ * allocates, apart from dq_attn_create; every call but that one is asynchronous
+ * on its stream and can be captured into a HIP graph. */
+
+/* DQ_NORM_HEAD: f = fl32(1 / sqrt(sum_c x_c^2 / head_dim + eps)) of each head,
+ * gain [head_dim]; DQ_NORM_ROW: of the whole row, over heads * head_dim
+ * channels, gain [heads * head_dim] (f as dq_rmsnorm8 forms it, bit for bit).
+ * v_c = fl32(fl32(x_c f) gain_c).  The sum of squares is kept in fp64 in an
+ * order that goes by the channels' count alone. */
+typedef enum { DQ_NORM_NONE = 0, DQ_NORM_HEAD = 1, DQ_NORM_ROW = 2 } dq_norm;
+
+/* Rotation by 1 to 3 position axes (text: one; video: frames, rows, columns).
+ * Axis i owns the next pairs[i] pairs of channels; with P pairs in all, pair j
+ * is channels (2 j, 2 j + 1) when interleaved, else (j, j + P), P then a
+ * multiple of 8; channels from 2 P on (2 P <= head_dim) are not rotated.  With
+ * (c, s) the pair's cos and sin at the row's position on its axis,
+ *     a' = fl32(fl32(a c) - fl32(b s)),  b' = fl32(fl32(a s) + fl32(b c)).
+ * table_dev[i] [positions[i]][pairs[i]][2] fp32 holds (c, s), 8-byte aligned.
+ * A position outside [0, positions[i]) turns the pairs of its axis to NaN. */
+typedef struct {
+    int32_t axes, interleaved;
+    int32_t pairs[3];
+    int64_t positions[3];          /* 1 .. 2^31 - 1 */
+    const float* table_dev[3];
+} dq_rope;
+
+/* Fills one axis' table: (cos, sin) of fl64(p freq_j), each rounded to fp32,
+ * for positions 0 .. positions - 1 and 1 to 128 pairs (freq_host [pairs],
+ * radians per position, finite).  Asynchronous on `stream`. */
+dq_status dq_rope_table(const double* freq_host, int32_t pairs, int64_t positions, float* table_dev, int32_t device,
+                        void* stream);
+
+/* What is done to the heads of queries and keys. */
+typedef struct {
+    dq_norm norm;
+    dq_dtype gain_dt;
+    double eps;                    /* [1e-60, inf); unused without a norm */
+    const dq_rope* rope;           /* NULL: no rotation */
+    const int32_t* pos_dev;        /* [N][axes]; NULL (one axis only): the row's number n, or, in a cache, its place in the sequence */
+} dq_head_ops;
+
+/* y = the heads of x, normed and rotated, with one rounding to ydt.
+ *   x_dev [N][heads * head_dim] of dtype dt, y_dev of dtype ydt: rows ldx, ldy
+ *         elements apart, 16-byte aligned rows; y_dev may be x_dev itself (same
+ *         dtype and stride), otherwise they must not share memory
+ *   gain_dev [head_dim] or [heads * head_dim], 16-byte aligned, or NULL for ones
+ * Requires heads * head_dim <= 32768, 0 <= N <= 2^31 - 256.  A row's results do not depend on
+ * N or on the other rows.  Infinite and NaN values stay in their heads (in
+ * their rows, with DQ_NORM_ROW). */
+dq_status dq_norm_rope(const void* x_dev, int64_t ldx, dq_dtype dt, int64_t N, int32_t heads, int32_t head_dim,
+                       const void* gain_dev, const dq_head_ops* ops, void* y_dev, int64_t ldy, dq_dtype ydt, int32_t device,
+                       void* stream);
+
+/* A cache of keys and values: codes [pages][heads][page_tokens][head_dim] E4M3
+ * (bits 8) or [..][head_dim / 2] E2M1, two to a byte (bits 4), 16-byte aligned;
+ * scales [pages][heads][page_tokens][head_dim / 32] E8M0, 4-byte aligned (a code
+ * of 255: the group's values are NaN).  page_tokens is a power of two in [16, 65536]; 1 <= pages <= 2^31 - 1. */
+typedef struct {
+    uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+    int64_t pages;
+    int32_t page_tokens, heads, head_dim, bits;
+} dq_kv;
+
+/* A ragged batch of `seqs` sequences (1 .. 2^20), all arrays on the device: rows
+ * first_dev[b] .. first_dev[b + 1] - 1 (first_dev [seqs + 1], ascending) belong to
+ * sequence b and are its last ones, its cache holds length_dev[b] tokens (those
+ * rows' included), and token t is at place t % page_tokens of page
+ * pages_dev[b * pages_ld + t / page_tokens].  Row n's place in its sequence is
+ * t = length - rows + (n - first).  Rows of no sequence (before the first, behind
+ * the last) are left as they were.  The arrays are read when the work runs;
+ * entries that lie outside of their range never lead outside of the buffers: a
+ * row at a place below 0, past pages_ld pages, or in a page that is none of
+ * [0, pages) has no token in the cache. */
+typedef struct {
+    int64_t seqs;
+    const int32_t *first_dev, *length_dev, *pages_dev;
+    int64_t pages_ld;
+} dq_seqs;
+
+/* Codes the keys (normed and rotated) and values of N rows into the cache, and
+ * (q_dev not NULL) norms and rotates their queries: one launch for a decoding step.
+ *   k_dev, v_dev [N][kv heads * head_dim], q_dev [N][q_heads * head_dim] of
+ *         dtype dt, rows ld elements apart, 16-byte aligned (slices of one stacked
+ *         projection do); gain_k_dev, gain_q_dev, y_dev (q's output, [N][q_heads *
+ *         head_dim] of dtype ydt; may be q_dev itself, same dtype and stride) as in dq_norm_rope
+ * Scales as everywhere here: the smallest 2^e, e >= -127, with max|v| <= q_max 2^e
+ * over 32 channels (448, or 6 for E2M1), codes to nearest, ties to even.  Infinite and NaN elements do
+ * not enter the scale and get the E4M3 NaN code; E2M1 has none, so they turn
+ * their group's scale code to 255.  Rows without a token in the cache are not coded
+ * (their queries are still rotated).  Where two rows of a call share a place its codes are
+ * undefined.  Cache, q, k, v and y must not share memory otherwise. */
+dq_status dq_kv_write(const dq_kv* kv, const dq_seqs* seqs, int64_t N, dq_dtype dt, const void* k_dev, int64_t ldk,
+                      const void* v_dev, int64_t ldv, const void* gain_k_dev, const void* q_dev, int64_t ldq, int32_t q_heads,
+                      const void* gain_q_dev, void* y_dev, int64_t ldy, dq_dtype ydt, const dq_head_ops* ops, int32_t device,
+                      void* stream);
+
+/* The values of the N rows' tokens, k_dev and v_dev [N][heads * head_dim] of dtype
+ * dt (either may be NULL, not both), rows ld elements apart, 16-byte aligned:
+ * exact where the type holds them (E4M3 and E2M1 values from 2^-126 to 2^127 in
+ * either; beyond, infinite).  A row without a token in the cache is zero.  To read whole sequences give
+ * first_dev as the sums of the lengths. */
+dq_status dq_kv_read(const dq_kv* kv, const dq_seqs* seqs, int64_t N, void* k_dev, int64_t ldk, void* v_dev, int64_t ldv,
+                     dq_dtype dt, int32_t device, void* stream);
+
+/* Workspace of dq_attn_rows on one device: sums of the parts that a long cache
+ * is split into (72 MiB).  Must not be used by two streams at once (two captured
+ * graphs that share one must not run at once either). */
+typedef struct dq_attn dq_attn;
+dq_status dq_attn_create(int32_t device, dq_attn** out);
+void dq_attn_destroy(dq_attn* a);
+
+/* Which tokens a row sees, and its scores.  With t the row's place, L its
+ * sequence's length and block > 0, e = (floor(t / block) + 1) block: tokens
+ * [max(0, e - window), min(e, L)) (window 0: from 0 on) and [0, min(prefix[b], L));
+ * block 0: all L (window must then be 0, prefix has no effect).  block 1 is the causal mask; with
+ * block the tokens of a frame, a row sees its own frame and those before it. */
+typedef struct {
+    double scale;                  /* (0, 2^64]; head_dim ** -0.5 as a rule */
+    double cap;                    /* scores cap tanh(s / cap); 0: as they are; else [2^-64, 2^64] */
+    int64_t block, window;         /* [0, 2^31) */
+    const int32_t* prefix_dev;     /* [seqs], or NULL */
+} dq_attn_ops;
+
+/* Attention of N query rows over a cache: y = sum_t softmax_t(scale q k_t) v_t
+ * for each of q_heads heads, query head h with the cache's head
+ * h / (q_heads / heads); the statistics are fp32.
+ *   q_dev, y_dev [N][q_heads * head_dim] of dtype dt, rows ldq, ldy elements
+ *         apart, 16-byte aligned; y must not share memory with anything read
+ * head_dim 64 or 128; q_heads a multiple of the cache's heads, q_heads *
+ * head_dim <= 32768; 0 <= N <= 2^24, N * q_heads / heads <= 2^27.  The rows' own
+ * tokens are read from the cache, so write them first.  A row that sees no token is zero; a token in a page
+ * that is none of the cache's is not seen.  What masked tokens hold (NaN included) has no effect.
+ * bf16: weights are rounded to bf16 for their product with v and summed as
+ * rounded; fp32: q is taken at its full precision, weights to 16 bits.
+ * Tuned for few rows: those of a sequence that share a key head are taken up to
+ * 64 (rows times heads) at a time, each such group reading the cache again.
+ * Repeated calls agree bit for bit. */
+dq_status dq_attn_rows(const dq_kv* kv, const dq_seqs* seqs, int64_t N, const void* q_dev, int64_t ldq, dq_dtype dt,
+                       int32_t q_heads, const dq_attn_ops* ops, dq_attn* a, void* y_dev, int64_t ldy, int32_t device,
+                       void* stream);
 
 /* For callers that cannot allocate device memory (code under HIP graph
  * capture, tight serving loops, harnesses that forbid hipMalloc): dq_linear

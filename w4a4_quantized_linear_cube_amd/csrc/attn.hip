@@ -1,0 +1,688 @@
+// dq_attn_rows: attention of a few query rows over a cache of MX-FP8 or MX-FP4
+// keys and values.
+//
+//   s_t = scale (q k_t), capped where asked;  y = sum_t e^(s_t - m) v_t / sum_t e^(s_t - m)
+//
+// One pass over the cache with the running maximum m, the weights' sum and the
+// weighted sum of the values, all fp32, rescaled when m grows.
+//
+// The rows of a sequence that share a key head (its query heads, times its rows)
+// are the 16 columns of a matrix instruction, RB such blocks to a workgroup, so
+// each key and value is read and decoded once for all of them.  A wave takes 32
+// tokens at a time:
+//   S^T [tokens][rows] = K Q^T: a lane decodes a run of its token's channels
+//     straight from global memory into the instruction's operand (channels may
+//     take any order that both operands share);
+//   O^T [channels][rows] += V^T P^T: S^T's accumulators are P^T's operand as they
+//     lie (the order of tokens is again free); V goes through the wave's own part
+//     of LDS as bf16 and comes back transposed.
+// The four waves of a workgroup take blocks of tokens in turn, without a
+// barrier, and join at the end; a long cache is split over workgroups, whose sums
+// meet in the workspace: whichever ends last joins them in order.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <memory>
+#include <new>
+
+#include "dq.h"
+#include "dq_heads.h"
+
+struct dq_attn {
+    int device = 0;
+    float* sums = nullptr;     // [unit][row block][16][D] sums, then [unit][row block][16][4] statistics
+    int* arrivals = nullptr;   // parts that have ended, of each tile and head (0 between launches)
+};
+
+namespace dq {
+namespace {
+
+// Units (tiles x key heads x parts) that may meet in the workspace, and blocks of 16 rows to one.
+constexpr int MAX_UNITS = 2048, MAX_RB = 4;
+constexpr size_t SUM_FLOATS = size_t(MAX_UNITS) * MAX_RB * 16 * 128, STAT_FLOATS = size_t(MAX_UNITS) * MAX_RB * 16 * 4;
+constexpr float LOG2E = 1.44269504088896340736f;
+
+struct AttnArgs {
+    const void* q;
+    void* y;
+    long long ldq, ldy;
+    const uint8_t* codes[2];
+    const uint8_t* scales[2];
+    Pages pages;
+    const int* prefix;
+    int N, G;               // query rows; query heads to a key head
+    int parts;              // workgroups that may share a tile's tokens
+    long long block, window;
+    float scale, cap, cap_inv;   // scale: of the scores in base 2, or (with a cap) of the scores
+    float* sums;
+    float* stats;
+    int* arrivals;
+};
+
+typedef unsigned v4u __attribute__((ext_vector_type(4)));
+typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+
+// Sums that workgroups hand to each other pass the caches of one XCD by (the
+// agent scope's cache bit), so none needs writing back or invalidating.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t shared_floats(float* p, size_t floats) {
+    return __builtin_amdgcn_make_buffer_rsrc(p, (short)0, (int)(floats * 4), 0x00020000);
+}
+__device__ __forceinline__ void hand_over(__amdgpu_buffer_rsrc_t r, size_t at, v4f v) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, v), r, (int)(at * 4), 0, 16);
+}
+__device__ __forceinline__ v4f take_over(__amdgpu_buffer_rsrc_t r, size_t at) {
+    return __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(at * 4), 0, 16));
+}
+
+// Maximum and sum over the four lanes that hold one row.
+__device__ __forceinline__ float max_rows(float v) {
+    const uint32_t w = __float_as_uint(v);
+    const v2w a = __builtin_bit_cast(v2w, __builtin_amdgcn_permlane16_swap(w, w, false, false));
+    const float m = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const uint32_t x = __float_as_uint(m);
+    const v2w b = __builtin_bit_cast(v2w, __builtin_amdgcn_permlane32_swap(x, x, false, false));
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float sum_rows(float v) {
+    const uint32_t w = __float_as_uint(v);
+    const v2w a = __builtin_bit_cast(v2w, __builtin_amdgcn_permlane16_swap(w, w, false, false));
+    const uint32_t x = __float_as_uint(__uint_as_float(a[0]) + __uint_as_float(a[1]));
+    const v2w b = __builtin_bit_cast(v2w, __builtin_amdgcn_permlane32_swap(x, x, false, false));
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+__device__ __forceinline__ float power(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// tanh: (1 - t) / (1 + t) with t = e^-2|x|, and its series where that cancels.
+__device__ __forceinline__ float tanh_of(float x) {
+    const float a = fabsf(x), t = power(-2.0f * LOG2E * a), x2 = x * x;
+    const float far = copysignf((1.0f - t) * __builtin_amdgcn_rcpf(1.0f + t), x);
+    const float near = x * (1.0f + x2 * (-0.33333333f + x2 * (0.13333333f + x2 * (-0.053968254f + x2 * 0.021869489f))));
+    return a < 0.3f ? near : far;
+}
+
+// 8 codes (two words of E4M3, one of E2M1) as bf16, exactly.
+template <int BITS>
+__device__ __forceinline__ v8bf decode8(const uint32_t* w, float scale) {
+    v2b p[4];
+    if constexpr (BITS == 8) {
+        p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[0], scale, false);
+        p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[0], scale, true);
+        p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[1], scale, false);
+        p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[1], scale, true);
+    } else {
+        p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0], scale, 0);
+        p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0], scale, 1);
+        p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0], scale, 2);
+        p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0], scale, 3);
+    }
+    return v8bf{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
+    if constexpr (N >= 4) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const v4w v = *(const v4w*)(p + 4 * i);
+            w[i] = v[0], w[i + 1] = v[1], w[i + 2] = v[2], w[i + 3] = v[3];
+        }
+    } else {
+        const v2w v = *(const v2w*)p;
+        w[0] = v[0], w[1] = v[1];
+    }
+}
+
+// One wave's 32 tokens, as they are held in the cache.
+template <int BITS, int D>
+struct Tokens {
+    static constexpr int KW = D / 4 * BITS / 32;    // words of codes a lane holds of a key (D / 4 channels)
+    static constexpr int VP = D / 32;               // 16-channel pieces of values a lane holds
+    static constexpr int VW = 16 * BITS / 32;
+    uint32_t k[2][KW], v[VP][VW];
+    uint32_t ks[2], vs[VP];
+};
+
+template <class T, int BITS, int D, int RB>
+__global__ __launch_bounds__(256) void k_attn(AttnArgs a) {
+    constexpr bool F32 = sizeof(T) == 4;
+    constexpr int QP = F32 ? 3 : 1, PP = F32 ? 2 : 1;      // bf16 parts of q and of the weights
+    constexpr int TR = 16 * RB, CB = D / 16, NJ = D / 32;  // rows of a tile; blocks of 16 channels; steps of 32 channels
+    constexpr int LPR = D / 16;                            // lanes to a token's values, 16 channels each
+    using Tok = Tokens<BITS, D>;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[4][64 * D];   // a wave's V [32][D] bf16, then its sums [16][D] fp32
+    __shared__ float stat[4][3][TR];
+    __shared__ int arrived;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r16 = lane & 15, g = lane >> 4;
+    const int part = (int)blockIdx.x % a.parts, tile = (int)blockIdx.x / a.parts, head = blockIdx.y;
+
+    // ---- the tile's sequence and rows.  Sequence b's tiles are numbered from
+    // floor(first[b] G / TR) + b on, which leaves each as many as it needs.
+    int b;
+    {
+        const int* first = a.pages.first;
+        const int B = a.pages.seqs, step = (B + 63) >> 6;
+        const auto base = [&](int i) { return ((long long)first[i] * a.G) / TR + i; };
+        b = __popcll(__ballot(lane * step < B && base(min(lane * step, B - 1)) <= tile)) - 1;
+        if (b < 0) return;
+        int lo = b * step, n = min(step, B - lo);
+        while (n > 1) {
+            const int h = n >> 1;
+            if (base(lo + h) <= tile) lo += h, n -= h;
+            else n = h;
+        }
+        b = __builtin_amdgcn_readfirstlane(lo);
+    }
+    const int f0 = min(max(a.pages.first[b], 0), a.N), f1 = min(max(a.pages.first[b + 1], f0), a.N);
+    const int length = max(a.pages.length[b], 0);
+    const int L = (int)min((long long)length, min((long long)a.pages.ld << a.pages.shift, (1ll << 31) - 64));   // tokens that may have a page
+    const long long rows = (long long)(f1 - f0) * a.G, r0 = ((long long)tile - (((long long)a.pages.first[b] * a.G) / TR + b)) * TR;
+    if (r0 < 0 || r0 >= rows) return;
+    const int pf = a.block && a.prefix ? min(max(a.prefix[b], 0), L) : 0;
+
+    // ---- what each row sees: [lo, hi) and [0, pf)
+    const long long t0 = (long long)length - (f1 - f0);    // the first row's place
+    const auto end_of = [&](long long t) {
+        const long long q = t >= 0 ? t / a.block : -((-t + a.block - 1) / a.block);
+        return (q + 1) * a.block;
+    };
+    const auto sees = [&](long long r, int* lo, int* hi) {  // r: packed row
+        if (!a.block) {
+            *lo = 0, *hi = L;
+            return;
+        }
+        const long long e = end_of(t0 + r / a.G);
+        *hi = (int)min(max(e, 0ll), (long long)L);
+        *lo = a.window ? (int)min(max(e - a.window, 0ll), (long long)L) : 0;
+    };
+    int lo[RB], hi[RB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+        lo[i] = hi[i] = 0;
+        if (r0 + 16 * i + r16 < rows) sees(r0 + 16 * i + r16, &lo[i], &hi[i]);
+    }
+    int lo0, hi0, lo1, hi1;                                // of the tile's first and last row
+    sees(r0, &lo0, &hi0);
+    sees(min(rows, r0 + TR) - 1, &lo1, &hi1);
+    // blocks of 32 tokens that some row sees: [0, na) and [b0, b0 + nb)
+    int na = (pf + 31) >> 5, b0 = lo0 >> 5, nb = max(((hi1 + 31) >> 5) - b0, 0);
+    if (hi1 <= lo0) nb = 0;
+    if (na >= b0) nb = max(max(b0 + nb, na), 0), b0 = 0, na = 0;
+    const int blocks = na + nb;
+    int per = (blocks + a.parts - 1) / a.parts;
+    per = (per + 3) & ~3;                                  // (whole rounds of the four waves)
+    const int used = blocks ? (blocks + per - 1) / per : 1;
+    if (part >= used) return;
+    const int c_end = min(blocks, (part + 1) * per);
+
+    // ---- q as the second operand: lane (row, g), channels (D / 4) g + 8 j ..
+    v8bf q[RB][QP][NJ];
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+        const long long r = min(r0 + 16 * i + r16, rows - 1);
+        const T* p = (const T*)a.q + (f0 + r / a.G) * a.ldq + ((long long)head * a.G + r % a.G) * D + (D / 4) * g;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            if constexpr (F32) {
+                float v[8];
+                Stream<float>::load(p + 8 * j, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const __bf16 h = (__bf16)v[e];
+                    const float rest = v[e] - (float)h;
+                    const __bf16 m = (__bf16)rest;
+                    q[i][0][j][e] = h;
+                    q[i][1][j][e] = m;
+                    q[i][2][j][e] = (__bf16)(rest - (float)m);
+                }
+                // (an infinite value has no rest)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if ((__float_as_uint(v[e]) & 0x7f800000u) == 0x7f800000u || fabsf((float)q[i][0][j][e]) > 3.4e38f) {
+                        q[i][1][j][e] = (__bf16)0.0f;
+                        q[i][2][j][e] = (__bf16)0.0f;
+                    }
+            } else {
+                q[i][0][j] = __builtin_bit_cast(v8bf, get16(p + 8 * j));
+            }
+        }
+    }
+
+    // ---- the cache
+    const auto token0 = [&](int c) { return (c < na ? c : c - na + b0) << 5; };
+    struct Two {
+        int p[2];
+    };
+    const auto pages_at = [&](int c) {                     // pages of a block's two halves
+        Two r;
+        const int t = token0(min(c, blocks - 1)), i0 = t >> a.pages.shift, i1 = (t + 16) >> a.pages.shift;
+        r.p[0] = blocks && t < L ? page_of(a.pages, b, i0) : -1;
+        r.p[1] = i1 == i0 ? r.p[0] : blocks && t + 16 < L ? page_of(a.pages, b, i1) : -1;
+        r.p[0] = __builtin_amdgcn_readfirstlane(r.p[0]);
+        r.p[1] = __builtin_amdgcn_readfirstlane(r.p[1]);
+        return r;
+    };
+    const int mask = (1 << a.pages.shift) - 1;
+    const auto load = [&](int c, Two pg) {
+        Tok x;
+        const int t = token0(min(c, blocks - 1));
+        long long base[2];                                 // the cache's row of each half's first token (page 0 where there is none)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            base[h] = (((long long)max(pg.p[h], 0) * a.pages.heads + head) << a.pages.shift) + ((t + 16 * h) & mask);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const long long row = base[h] + r16;
+            load_words<Tok::KW>(a.codes[0] + row * (D * BITS / 8) + g * (Tok::KW * 4), x.k[h]);
+            x.ks[h] = a.scales[0][row * (D / 32) + (D / 4 * g) / 32];
+        }
+#pragma unroll
+        for (int i = 0; i < Tok::VP; ++i) {                // piece i: token (64 / LPR) i + lane / LPR
+            const int tok = (64 / LPR) * i + lane / LPR, c16 = lane % LPR;
+            const long long row = ((64 / LPR) * i < 16 ? base[0] : base[1]) + (tok & 15);
+            load_words<Tok::VW>(a.codes[1] + row * (D * BITS / 8) + c16 * (Tok::VW * 4), x.v[i]);
+            x.vs[i] = a.scales[1][row * (D / 32) + c16 / 2];
+        }
+        return x;
+    };
+
+    v4f acc[RB][CB];
+    float m[RB], l[RB];
+    uint32_t seen = 0;                                     // row blocks whose row (of this lane) saw a token
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+        m[i] = -INFINITY, l[i] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < CB; ++c) acc[i][c] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    // V [32][D] bf16: 32 bytes (16 channels) of a token at slot c16 ^ its own, so
+    // that the transposing reads' 8 rows of 32 bytes meet 64 banks
+    uint8_t* const mine = lds[w];
+    const auto place_v = [&](int tok, int c16) {
+        const int s = D == 128 ? tok & 7 : (tok >> 1) & 3;
+        return tok * (2 * D) + ((c16 ^ s) << 5);
+    };
+    const auto read_v = [&](int cb) {                      // V^T: channels 16 cb + lane % 16, tokens 4 g .. and 16 + 4 g ..
+        const int tok = 4 * g + (r16 >> 2), in = (r16 & 3) * 8;
+        const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(mine + place_v(tok, cb) + in));
+        const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(mine + place_v(tok + 16, cb) + in));
+        typedef short v8s __attribute__((ext_vector_type(8)));
+        return __builtin_bit_cast(v8bf, v8s{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+    };
+
+    const int c_first = part * per + w;
+    Two pg = pages_at(c_first);
+    Tok cur{};
+    if (c_first < c_end) cur = load(c_first, pg);
+    Two pg_next = pages_at(c_first + 4);
+    for (int c = c_first; c < c_end; c += 4) {
+        const Two here = pg;
+        const Tok x = cur;
+        if (c + 4 < c_end) {
+            cur = load(c + 4, pg_next);
+            pg = pg_next;
+            pg_next = pages_at(c + 8);
+        }
+        const int t = token0(c);
+        // ---- scores
+        v4f s[RB][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float scale = scale_of(x.ks[h]);
+#pragma unroll
+            for (int i = 0; i < RB; ++i) s[i][h] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const v8bf k = decode8<BITS>(x.k[h] + j * (BITS / 4), scale);
+#pragma unroll
+                for (int i = 0; i < RB; ++i)
+#pragma unroll
+                    for (int p = QP - 1; p >= 0; --p) s[i][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[i][p][j], s[i][h], 0, 0, 0);
+            }
+        }
+        // ---- values into LDS
+        const bool all = here.p[0] >= 0 && here.p[1] >= 0 && ((t >= lo1 && t + 32 <= hi0) || t + 32 <= pf);   // every row sees every token
+        bool odd = false;                                  // values that are not finite, where some row must not see them
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int i = 0; i < Tok::VP; ++i) {
+            const int tok = (64 / LPR) * i + lane / LPR, c16 = lane % LPR;
+            const float scale = scale_of(x.vs[i]);
+            uint4* to = (uint4*)(mine + place_v(tok, c16));
+            v8bf v0 = decode8<BITS>(x.v[i], scale), v1 = decode8<BITS>(x.v[i] + BITS / 4, scale);
+            if (!all) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    // (times 0: NaN for what is not finite)
+                    const float z0 = (float)v0[e] * 0.0f, z1 = (float)v1[e] * 0.0f;
+                    if (z0 != z0) odd = true, v0[e] = (__bf16)0.0f;
+                    if (z1 != z1) odd = true, v1[e] = (__bf16)0.0f;
+                }
+            }
+            to[0] = __builtin_bit_cast(uint4, v0);
+            to[1] = __builtin_bit_cast(uint4, v1);
+        }
+        // ---- weights
+        v8bf pw[RB][PP];
+        uint32_t vis[RB];
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+            float e[8];
+            vis[i] = 0xff;
+            if (!all) {
+                vis[i] = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int tok = t + 16 * (j >> 2) + 4 * g + (j & 3);
+                    const bool on = ((tok >= lo[i] && tok < hi[i]) || tok < pf) && here.p[j >> 2] >= 0;
+                    vis[i] |= on ? 1u << j : 0u;
+                }
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float v = s[i][j >> 2][j & 3] * a.scale;
+                if (a.cap > 0.0f) v = a.cap * tanh_of(v * a.cap_inv) * LOG2E;
+                e[j] = vis[i] >> j & 1 ? v : -INFINITY;
+                top = fmaxf(top, e[j]);
+            }
+            if (vis[i]) seen |= 1u << i;
+            top = max_rows(top);
+            if (__ballot(top > m[i])) {
+                const float mn = fmaxf(m[i], top), f = mn == -INFINITY ? 1.0f : power(m[i] - mn);
+                m[i] = mn;
+                l[i] *= f;
+#pragma unroll
+                for (int c16 = 0; c16 < CB; ++c16) acc[i][c16] *= f;
+            }
+            const float at = m[i] == -INFINITY ? 0.0f : m[i];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float p = power(e[j] - at);
+                const __bf16 h = (__bf16)p;
+                pw[i][0][j] = h;
+                if constexpr (PP == 2) {
+                    pw[i][1][j] = (__bf16)(p - (float)h);
+                    l[i] += p;
+                } else {
+                    l[i] += (float)h;
+                }
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        // ---- O^T += V^T P^T
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+            const v8bf v = read_v(cb);
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+#pragma unroll
+                for (int p = PP - 1; p >= 0; --p) acc[i][cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pw[i][p], acc[i][cb], 0, 0, 0);
+        }
+        if (!all && __ballot(odd)) {
+            // the rows that do see a value that is not finite: counted as ones times ones
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int i = 0; i < Tok::VP; ++i) {
+                const int tok = (64 / LPR) * i + lane / LPR, c16 = lane % LPR;
+                const float scale = scale_of(x.vs[i]);
+                uint4* to = (uint4*)(mine + place_v(tok, c16));
+                v8bf v0 = decode8<BITS>(x.v[i], scale), v1 = decode8<BITS>(x.v[i] + BITS / 4, scale);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float z0 = (float)v0[e] * 0.0f, z1 = (float)v1[e] * 0.0f;
+                    v0[e] = (__bf16)(z0 != z0 ? 1.0f : 0.0f);
+                    v1[e] = (__bf16)(z1 != z1 ? 1.0f : 0.0f);
+                }
+                to[0] = __builtin_bit_cast(uint4, v0);
+                to[1] = __builtin_bit_cast(uint4, v1);
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                v8bf on;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) on[j] = (__bf16)(vis[i] >> j & 1 ? 1.0f : 0.0f);
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb) {
+                    const v4f n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(read_v(cb), on, v4f{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (n[e] > 0.0f) acc[i][cb][e] = __builtin_nanf("");
+                }
+            }
+        }
+    }
+
+    // ---- the four waves' sums, a block of rows at a time: thread (row, its D / 16 channels)
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+        const float sum = sum_rows(l[i]);
+        const uint64_t s = __ballot(seen >> i & 1);
+        const bool any = ((s | s >> 16 | s >> 32 | s >> 48) >> r16) & 1;
+        if (g == 0) {
+            stat[w][0][16 * i + r16] = m[i];
+            stat[w][1][16 * i + r16] = sum;
+            stat[w][2][16 * i + r16] = any ? 1.0f : 0.0f;
+        }
+    }
+    constexpr int CT = D / 16, Q4 = CT / 4;                // channels of a thread, in pieces of 4
+    const int row = tid >> 4, ch = (tid & 15) * CT;
+    const int unit = (head * ((int)gridDim.x / a.parts) + tile) * a.parts;   // the tile's first unit
+    const auto at_sum = [&](int p, int i) { return ((size_t)(unit + p) * RB + i) * 16 * D; };
+    const auto at_stat = [&](int p, int i) { return (((size_t)(unit + p) * RB + i) * 16 + row) * 4; };
+    const __amdgpu_buffer_rsrc_t sums = shared_floats(a.sums, SUM_FLOATS), stats = shared_floats(a.stats, STAT_FLOATS);
+    const auto finish = [&](int i, const v4f* o, float sum, bool any) {
+        const long long r = r0 + 16 * i + row;
+        if (r >= rows) return;
+        T* y = (T*)a.y + (f0 + r / a.G) * a.ldy + ((long long)head * a.G + r % a.G) * D + ch;
+#pragma unroll
+        for (int p = 0; p < Q4; ++p) {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = any ? o[p][e] / sum : 0.0f;
+            if constexpr (F32) {
+                *(v4f*)(y + 4 * p) = v4f{v[0], v[1], v[2], v[3]};
+            } else {
+                const v2b x{(__bf16)v[0], (__bf16)v[1]}, z{(__bf16)v[2], (__bf16)v[3]};
+                *(v2w*)(y + 4 * p) = v2w{__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, z)};
+            }
+        }
+    };
+    // (16-byte piece c of a row lies at c ^ row, so the lanes' stores and loads meet all banks)
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+        __syncthreads();
+        v4f* o = (v4f*)mine;
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) o[r16 * (D / 4) + ((4 * cb + g) ^ r16)] = acc[i][cb];
+        __syncthreads();
+        float top = -INFINITY, sum = 0.0f, any = 0.0f;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) top = fmaxf(top, stat[p][0][16 * i + row]);
+        v4f out[Q4];
+#pragma unroll
+        for (int p = 0; p < Q4; ++p) out[p] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const float mp = stat[p][0][16 * i + row], f = mp == -INFINITY ? 1.0f : power(mp - top);
+            sum += f * stat[p][1][16 * i + row];
+            any = fmaxf(any, stat[p][2][16 * i + row]);
+            const v4f* from = (const v4f*)lds[p] + row * (D / 4);
+#pragma unroll
+            for (int j = 0; j < Q4; ++j) out[j] += f * from[((ch >> 2) + j) ^ row];
+        }
+        if (used == 1) {
+            finish(i, out, sum, any > 0.0f);
+        } else {
+#pragma unroll
+            for (int j = 0; j < Q4; ++j) hand_over(sums, at_sum(part, i) + row * D + ch + 4 * j, out[j]);
+            if ((tid & 15) == 0) hand_over(stats, at_stat(part, i), v4f{top, sum, any, 0.0f});
+        }
+    }
+    if (used == 1) return;
+
+    // ---- the parts' sums, joined in order by the workgroup that ends last
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // (every wave's sums have arrived before the workgroup says so)
+    __syncthreads();
+    int* const count = a.arrivals + unit / a.parts;
+    if (tid == 0) arrived = __hip_atomic_fetch_add(count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (arrived != used - 1) return;
+    if (tid == 0) __hip_atomic_store(count, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);   // (for the next launch)
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+        float top = -INFINITY, sum = 0.0f, any = 0.0f;
+        for (int p = 0; p < used; ++p) top = fmaxf(top, take_over(stats, at_stat(p, i))[0]);
+        v4f out[Q4];
+#pragma unroll
+        for (int j = 0; j < Q4; ++j) out[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int p = 0; p < used; ++p) {
+            const v4f s = take_over(stats, at_stat(p, i));
+            const float f = s[0] == -INFINITY ? 1.0f : power(s[0] - top);
+            sum += f * s[1];
+            any = fmaxf(any, s[2]);
+#pragma unroll
+            for (int j = 0; j < Q4; ++j) out[j] += f * take_over(sums, at_sum(p, i) + row * D + ch + 4 * j);
+        }
+        finish(i, out, sum, any > 0.0f);
+    }
+}
+
+template <class T, int BITS, int D, int RB>
+hipError_t launch_attn(AttnArgs a, int kv_heads, hipStream_t st) {
+    const long long tiles = ((long long)a.N * a.G) / (16 * RB) + a.pages.seqs;
+    const long long blocks = (((long long)a.pages.ld << a.pages.shift) + 31) / 32;
+    a.parts = (int)std::max(1ll, std::min({(blocks + 3) / 4, MAX_UNITS / (tiles * kv_heads), 256ll}));
+    return launch(k_attn<T, BITS, D, RB>, dim3((unsigned)(tiles * a.parts), kv_heads), 256u, st, a);
+}
+
+template <class T, int BITS, int D>
+hipError_t launch_attn(const AttnArgs& a, int kv_heads, hipStream_t st) {
+    const long long rows = ((long long)a.N * a.G + a.pages.seqs - 1) / a.pages.seqs;   // of a sequence, in the mean
+    if (rows <= 16) return launch_attn<T, BITS, D, 1>(a, kv_heads, st);
+    if constexpr (sizeof(T) == 2)
+        if (rows > 32) return launch_attn<T, BITS, D, 4>(a, kv_heads, st);
+    return launch_attn<T, BITS, D, 2>(a, kv_heads, st);
+}
+
+void free_attn(dq_attn* a) {
+    if (!a) return;
+    DeviceGuard dg(a->device);
+    (void)hipFree(a->sums);
+    (void)hipFree(a->arrivals);
+    delete a;
+}
+
+}  // namespace
+}  // namespace dq
+
+using namespace dq;
+
+extern "C" {
+
+dq_status dq_attn_create(int32_t device, dq_attn** out) {
+    set_error("");
+    if (!out) return fail(DQ_ERR_INVALID_ARG, "out is NULL");
+    *out = nullptr;
+    const dq_status st = known_device(device);
+    if (st != DQ_OK) return st;
+    DeviceGuard dg(device);
+    if (!dg.ok) return fail(DQ_ERR_DEVICE, "hipSetDevice failed");
+    auto* a = new (std::nothrow) dq_attn();
+    if (!a) return fail(DQ_ERR_OUT_OF_MEMORY, "host allocation failed");
+    std::unique_ptr<dq_attn, void (*)(dq_attn*)> guard(a, free_attn);
+    a->device = device;
+    hipError_t e;
+    if ((e = hipMalloc((void**)&a->sums, (SUM_FLOATS + STAT_FLOATS) * 4)) != hipSuccess) {
+        a->sums = nullptr;
+        return hip_fail(e, "hipMalloc workspace");
+    }
+    if ((e = hipMalloc((void**)&a->arrivals, MAX_UNITS * 4)) != hipSuccess) {
+        a->arrivals = nullptr;
+        return hip_fail(e, "hipMalloc workspace");
+    }
+    if ((e = hipMemset(a->arrivals, 0, MAX_UNITS * 4)) != hipSuccess || (e = hipDeviceSynchronize()) != hipSuccess)
+        return hip_fail(e, "workspace init");
+    *out = guard.release();
+    return DQ_OK;
+}
+
+void dq_attn_destroy(dq_attn* a) { free_attn(a); }
+
+dq_status dq_attn_rows(const dq_kv* kv, const dq_seqs* seqs, int64_t N, const void* q_dev, int64_t ldq, dq_dtype dt,
+                       int32_t q_heads, const dq_attn_ops* ops, dq_attn* a, void* y_dev, int64_t ldy, int32_t device,
+                       void* stream) {
+    set_error("");
+    dq_status st = check_kv(kv);
+    if (st != DQ_OK || (st = check_seqs(seqs)) != DQ_OK) return st;
+    const int D = kv->head_dim;
+    if (D != 64 && D != 128) return fail(DQ_ERR_SHAPE, "attention takes a head_dim of 64 or 128");
+    if (dt != DQ_F32 && dt != DQ_BF16) return fail(DQ_ERR_INVALID_ARG, "unknown dtype");
+    if (N < 0 || N > 1 << 24) return fail(DQ_ERR_SHAPE, "N must be in [0, 2^24]");   // (a launch takes fewer than 2^32 threads)
+    if (q_heads < 1 || q_heads % kv->heads != 0 || (int64_t)q_heads * D > 32768)
+        return fail(DQ_ERR_SHAPE, "q_heads must be a multiple of the cache's heads with q_heads * head_dim <= 32768");
+    if (N * (q_heads / kv->heads) > 1 << 27) return fail(DQ_ERR_SHAPE, "N * q_heads / heads must be at most 2^27");
+    if (!ops || !a) return fail(DQ_ERR_INVALID_ARG, "ops or workspace is NULL");
+    const double most = 18446744073709551616.0;            // 2^64
+    if (!(ops->scale > 0.0) || !(ops->scale <= most)) return fail(DQ_ERR_INVALID_ARG, "scale must be in (0, 2^64]");
+    if (ops->cap != 0.0 && !(ops->cap >= 1.0 / most && ops->cap <= most)) return fail(DQ_ERR_INVALID_ARG, "cap must be 0 or in [2^-64, 2^64]");
+    if (ops->block < 0 || ops->block >= int64_t(1) << 31 || ops->window < 0 || ops->window >= int64_t(1) << 31)
+        return fail(DQ_ERR_SHAPE, "block and window must be in [0, 2^31)");
+    if (ops->block == 0 && ops->window != 0) return fail(DQ_ERR_INVALID_ARG, "a window needs a block of 1 or more");
+    if ((uintptr_t)ops->prefix_dev % 4 != 0) return fail(DQ_ERR_INVALID_ARG, "prefix_dev must be 4-byte aligned");
+    if (a->device != device) return fail(DQ_ERR_INVALID_ARG, "the workspace is on another device");
+    if (N == 0) return DQ_OK;
+    if (!q_dev || !y_dev) return fail(DQ_ERR_INVALID_ARG, "q_dev or y_dev is NULL");
+    if (((uintptr_t)q_dev | (uintptr_t)y_dev) % 16 != 0) return fail(DQ_ERR_INVALID_ARG, "q_dev and y_dev must be 16-byte aligned");
+    const int64_t esz = dt == DQ_BF16 ? 2 : 4, C = (int64_t)q_heads * D;
+    for (const int64_t ld : {ldq, ldy})
+        if (ld < C || ld > (int64_t(1) << 40) / N || ld * esz % 16 != 0)
+            return fail(DQ_ERR_SHAPE, "the row strides must be at least the row's width and a multiple of 16 bytes");
+    const Span y{y_dev, N, ldy * esz, C * esz};
+    const int64_t cb = kv_code_bytes(kv), sb = kv_scale_bytes(kv);
+    const struct {
+        Span s;
+        const char* name;
+    } in[] = {{{q_dev, N, ldq * esz, C * esz}, "q_dev"}, {{kv->k_codes, 1, cb, cb}, "k_codes"}, {{kv->k_scales, 1, sb, sb}, "k_scales"},
+              {{kv->v_codes, 1, cb, cb}, "v_codes"}, {{kv->v_scales, 1, sb, sb}, "v_scales"},
+              {{seqs->first_dev, 1, 4 * (seqs->seqs + 1), 4 * (seqs->seqs + 1)}, "first_dev"},
+              {{seqs->length_dev, 1, 4 * seqs->seqs, 4 * seqs->seqs}, "length_dev"},
+              {{seqs->pages_dev, 1, 4 * seqs->seqs * seqs->pages_ld, 4 * seqs->seqs * seqs->pages_ld}, "pages_dev"},
+              {{ops->prefix_dev, 1, 4 * seqs->seqs, 4 * seqs->seqs}, "prefix_dev"}};
+    for (const auto& i : in)
+        if (overlap(y, i.s)) return fail(DQ_ERR_INVALID_ARG, std::string("y_dev overlaps ") + i.name);
+    DeviceGuard dg(device);
+    if (!dg.ok) return fail(DQ_ERR_DEVICE, "hipSetDevice failed");
+    AttnArgs k{};
+    k.q = q_dev, k.y = y_dev;
+    k.ldq = ldq, k.ldy = ldy;
+    k.codes[0] = kv->k_codes, k.codes[1] = kv->v_codes;
+    k.scales[0] = kv->k_scales, k.scales[1] = kv->v_scales;
+    k.pages = pages_of(kv, seqs);
+    k.prefix = ops->prefix_dev;
+    k.N = (int)N, k.G = q_heads / kv->heads;
+    k.block = ops->block, k.window = ops->window;
+    k.cap = (float)ops->cap;
+    k.cap_inv = ops->cap != 0.0 ? (float)(1.0 / ops->cap) : 0.0f;
+    k.scale = (float)(ops->cap != 0.0 ? ops->scale : ops->scale * 1.4426950408889634);
+    k.sums = a->sums, k.stats = a->sums + SUM_FLOATS;
+    k.arrivals = a->arrivals;
+    const auto go = [&](auto bits, auto dim) {
+        constexpr int B = decltype(bits)::value, W = decltype(dim)::value;
+        return dt == DQ_BF16 ? launch_attn<uint16_t, B, W>(k, kv->heads, (hipStream_t)stream)
+                             : launch_attn<float, B, W>(k, kv->heads, (hipStream_t)stream);
+    };
+    const auto by_dim = [&](auto bits) {
+        return D == 64 ? go(bits, std::integral_constant<int, 64>{}) : go(bits, std::integral_constant<int, 128>{});
+    };
+    const hipError_t e = kv->bits == 8 ? by_dim(std::integral_constant<int, 8>{}) : by_dim(std::integral_constant<int, 4>{});
+    return e == hipSuccess ? DQ_OK : hip_fail(e, "attention launch");
+}
+
+}  // extern "C"

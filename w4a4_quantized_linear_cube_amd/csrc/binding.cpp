@@ -9,6 +9,8 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
+
 #include "dq.h"
 
 namespace {
@@ -168,11 +170,167 @@ PyObject* rmsnorm8(PyObject*, PyObject* const* v, Py_ssize_t n) {
     });
 }
 
+// Attribute `name` of a handle or description of dq.py as an address (0 for None, with *ok kept).
+void* address_of(PyObject* o, const char* name, bool* ok) {
+    if (o == Py_None) return nullptr;
+    PyObject* v = PyObject_GetAttrString(o, name);
+    void* p = v && PyLong_Check(v) ? PyLong_AsVoidPtr(v) : nullptr;
+    Py_XDECREF(v);
+    if (!p || PyErr_Occurred()) *ok = false;
+    return p;
+}
+int64_t number_of(PyObject* o, const char* name, bool* ok) {
+    PyObject* v = PyObject_GetAttrString(o, name);
+    const int64_t n = v && PyLong_Check(v) ? PyLong_AsLongLong(v) : -1;
+    Py_XDECREF(v);
+    if (PyErr_Occurred()) *ok = false;
+    return n;
+}
+
+// A contiguous 1-D gain of n values, or None.
+bool gain_of(PyObject* o, int64_t n, int device, void** p, dq_dtype* d, bool* any) {
+    *p = nullptr;
+    if (o == Py_None) return true;
+    if (!THPVariable_Check(o)) return false;
+    const at::Tensor& g = THPVariable_Unpack(o);
+    dq_dtype mine;
+    if (!g.defined() || g.layout() != c10::kStrided || !g.is_cuda() || g.dim() != 1 || g.size(0) != n || !g.is_contiguous() ||
+        (int)g.get_device() != device || !dtype_of(g.scalar_type(), &mine) || (*any && mine != *d))
+        return false;
+    *d = mine;
+    *any = true;
+    *p = g.data_ptr();
+    return (uintptr_t)*p % 16 == 0;
+}
+
+// A contiguous int32 tensor of n values (and `c` columns, where that is not 0), or None.
+bool ints_of(PyObject* o, int64_t n, int64_t c, int device, const int32_t** p) {
+    *p = nullptr;
+    if (o == Py_None) return true;
+    if (!THPVariable_Check(o)) return false;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (!t.defined() || t.layout() != c10::kStrided || !t.is_cuda() || t.scalar_type() != c10::ScalarType::Int ||
+        t.dim() != (c ? 2 : 1) || t.size(0) != n || (c && t.size(1) != c) || !t.is_contiguous() || (int)t.get_device() != device)
+        return false;
+    *p = (const int32_t*)t.data_ptr();
+    return true;
+}
+
+// The norm and rotation of a call: (norm, eps, rope, pos) with the gains' dtype.
+bool ops_of(PyObject* norm, PyObject* eps, PyObject* rope, PyObject* pos, int64_t n, int device, dq_head_ops* ops) {
+    if (!PyLong_Check(norm) || !PyFloat_Check(eps)) return false;
+    const long k = PyLong_AsLong(norm);
+    if (k < 0 || k > 2) return false;
+    ops->norm = (dq_norm)k;
+    ops->eps = PyFloat_AS_DOUBLE(eps);
+    bool ok = true;
+    ops->rope = (const dq_rope*)address_of(rope, "address", &ok);
+    if (!ok) return false;
+    if (!ops->rope) return pos == Py_None;
+    if (number_of(rope, "device", &ok) != device || !ok) return false;
+    return ints_of(pos, n, ops->rope->axes, device, &ops->pos_dev);
+}
+
+// norm_rope(x, heads, y, norm, gain, eps, rope, pos, stream)
+PyObject* norm_rope(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    return guarded([&](int* status) {
+        Matrix x, y;
+        dq_dtype dx, dy;
+        dq_head_ops ops{};
+        void *stream, *gain;
+        bool any = false;
+        if (n != 9 || !matrix(v[0], 16, &x) || !PyLong_Check(v[1]) || !matrix(v[2], 16, &y) || !dtype_of(x.type, &dx) ||
+            !dtype_of(y.type, &dy) || y.n != x.n || y.c != x.c || y.device != x.device)
+            return false;
+        const long heads = PyLong_AsLong(v[1]);
+        if (heads < 1 || heads > x.c || x.c % heads || !ops_of(v[3], v[5], v[6], v[7], x.n, x.device, &ops)) return false;
+        if ((ops.norm == DQ_NORM_NONE && v[4] != Py_None) ||
+            !gain_of(v[4], ops.norm == DQ_NORM_HEAD ? x.c / heads : x.c, x.device, &gain, &ops.gain_dt, &any) ||
+            !stream_of(v[8], x.device, &stream) || x.c / heads > INT32_MAX)
+            return false;
+        Released released;
+        *status = dq_norm_rope(x.p, x.ld, dx, x.n, (int32_t)heads, (int32_t)(x.c / heads), gain, &ops, y.p, y.ld, dy, x.device, stream);
+        return true;
+    });
+}
+
+// kv_write(kv, seqs, k, v, q, y, norm, gain, gain_q, eps, rope, pos, stream)
+PyObject* kv_write(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    return guarded([&](int* status) {
+        Matrix k, val, q, y;
+        dq_dtype dt, dv, dq = DQ_F32, dy = DQ_F32;
+        dq_head_ops ops{};
+        void *stream, *gk, *gq;
+        bool any = false, ok = true;
+        if (n != 13) return false;
+        const dq_kv* kv = (const dq_kv*)address_of(v[0], "address", &ok);
+        const dq_seqs* seqs = (const dq_seqs*)address_of(v[1], "address", &ok);
+        if (!ok || !kv || !seqs) return false;
+        const int device = (int)number_of(v[0], "device", &ok);
+        const int64_t C = (int64_t)kv->heads * kv->head_dim;
+        if (number_of(v[1], "device", &ok) != device || !ok || !matrix(v[2], 16, &k) || !matrix(v[3], 16, &val) || k.c != C || val.c != C ||
+            val.n != k.n || k.device != device || val.device != device || !dtype_of(k.type, &dt) || !dtype_of(val.type, &dv) || dv != dt)
+            return false;
+        if ((v[4] == Py_None) != (v[5] == Py_None)) return false;
+        if (v[4] != Py_None && (!matrix(v[4], 16, &q) || !matrix(v[5], 16, &y) || q.n != k.n || y.n != k.n || q.c != y.c || q.c < 1 ||
+                                q.c % kv->head_dim || q.device != device || y.device != device || !dtype_of(q.type, &dq) || dq != dt ||
+                                !dtype_of(y.type, &dy)))
+            return false;
+        if (!ops_of(v[6], v[9], v[10], v[11], k.n, device, &ops)) return false;
+        if ((ops.norm == DQ_NORM_NONE && (v[7] != Py_None || v[8] != Py_None)) || (v[4] == Py_None && v[8] != Py_None)) return false;
+        if (!gain_of(v[7], ops.norm == DQ_NORM_HEAD ? kv->head_dim : C, device, &gk, &ops.gain_dt, &any) ||
+            !gain_of(v[8], ops.norm == DQ_NORM_HEAD ? kv->head_dim : q.c, device, &gq, &ops.gain_dt, &any) ||
+            !stream_of(v[12], device, &stream))
+            return false;
+        Released released;
+        *status = dq_kv_write(kv, seqs, k.n, dt, k.p, k.ld, val.p, val.ld, gk, q.p, q.ld, (int32_t)(q.c / kv->head_dim), gq, y.p, y.ld, dy,
+                              &ops, device, stream);
+        return true;
+    });
+}
+
+// attn_rows(kv, seqs, q, a, y, scale (below 0: head_dim ** -0.5), block, window, prefix, cap, stream)
+PyObject* attn_rows(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    return guarded([&](int* status) {
+        Matrix q, y;
+        dq_dtype dt, dy;
+        dq_attn_ops ops{};
+        void* stream;
+        bool ok = true;
+        if (n != 11) return false;
+        const dq_kv* kv = (const dq_kv*)address_of(v[0], "address", &ok);
+        const dq_seqs* seqs = (const dq_seqs*)address_of(v[1], "address", &ok);
+        dq_attn* a = (dq_attn*)address_of(v[3], "address", &ok);
+        if (!ok || !kv || !seqs || !a) return false;
+        const int device = (int)number_of(v[0], "device", &ok);
+        if (number_of(v[1], "device", &ok) != device || number_of(v[3], "device", &ok) != device || !ok || !matrix(v[2], 16, &q) ||
+            !matrix(v[4], 16, &y) || !dtype_of(q.type, &dt) || !dtype_of(y.type, &dy) || dy != dt || y.n != q.n || y.c != q.c || q.c < 1 ||
+            q.c % ((int64_t)kv->heads * kv->head_dim) || q.device != device || y.device != device || !PyFloat_Check(v[5]) ||
+            !PyLong_Check(v[6]) || !PyLong_Check(v[7]) || !PyFloat_Check(v[9]))
+            return false;
+        // (block and window first: what PyLong_AsLongLong cannot take raises, and the binding's own checks say so)
+        ops.block = PyLong_AsLongLong(v[6]);
+        ops.window = PyLong_AsLongLong(v[7]);
+        if (PyErr_Occurred() || !ints_of(v[8], seqs->seqs, 0, device, &ops.prefix_dev) || !stream_of(v[10], device, &stream)) return false;
+        ops.scale = PyFloat_AS_DOUBLE(v[5]);
+        if (ops.scale == -1.0) ops.scale = 1.0 / std::sqrt((double)kv->head_dim);
+        ops.cap = PyFloat_AS_DOUBLE(v[9]);
+        Released released;
+        *status = dq_attn_rows(kv, seqs, q.n, q.p, q.ld, dt, (int32_t)(q.c / kv->head_dim), &ops, a, y.p, y.ld, device, stream);
+        return true;
+    });
+}
+
 PyMethodDef methods[] = {
     {"linear_rows", (PyCFunction)(void (*)(void))linear_rows, METH_FASTCALL, "dq_linear_rows(pair, x, y, stream)"},
     {"linear_rows8", (PyCFunction)(void (*)(void))linear_rows8, METH_FASTCALL, "dq_linear_rows8(pair, codes, scales, y, stream)"},
     {"rmsnorm8", (PyCFunction)(void (*)(void))rmsnorm8, METH_FASTCALL,
      "dq_rmsnorm8(x, gain, eps, codes, scales, residual, h, y, group, stream)"},
+    {"norm_rope", (PyCFunction)(void (*)(void))norm_rope, METH_FASTCALL, "dq_norm_rope(x, heads, y, norm, gain, eps, rope, pos, stream)"},
+    {"kv_write", (PyCFunction)(void (*)(void))kv_write, METH_FASTCALL,
+     "dq_kv_write(kv, seqs, k, v, q, y, norm, gain, gain_q, eps, rope, pos, stream)"},
+    {"attn_rows", (PyCFunction)(void (*)(void))attn_rows, METH_FASTCALL,
+     "dq_attn_rows(kv, seqs, q, a, y, scale, block, window, prefix, cap, stream)"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_dqcall", "Native calls of libdq.so's small entry points", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

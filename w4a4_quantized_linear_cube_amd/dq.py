@@ -32,9 +32,11 @@ EXPORTS = ("dq_last_error", "dq_status_str", "dq_lowrank_factors", "dq_prepare_w
            "dq_linear6", "dq_act6_export", "dq_orbit_prepare", "dq_orbit_destroy", "dq_orbit_export",
            "dq_orbit_act_create", "dq_orbit_act_destroy", "dq_orbit_quantize_act", "dq_orbit_forward", "dq_orbit_linear",
            "dq_orbit_act_export", "dq_import_weights", "dq_rows_create", "dq_rows_destroy", "dq_linear_rows",
-           "dq_linear_rows8", "dq_rmsnorm8")
+           "dq_linear_rows8", "dq_rmsnorm8", "dq_rope_table", "dq_norm_rope", "dq_kv_write", "dq_kv_read", "dq_attn_create",
+           "dq_attn_destroy", "dq_attn_rows")
 DQ_FP6_E2M3, DQ_FP6_E3M2 = 2, 3
 FP6_FORMATS = {"fp6_e2m3": DQ_FP6_E2M3, "fp6_e3m2": DQ_FP6_E3M2}
+NORMS = {None: 0, "head": 1, "row": 2}
 
 
 class DQError(RuntimeError):
@@ -113,6 +115,13 @@ def load():
         "dq_linear_rows8": ([P, P, P, I64, P, P, ctypes.c_int, I64, P], ctypes.c_int),
         "dq_rmsnorm8": ([P, I64, P, I64, ctypes.c_int, P, ctypes.c_int, ctypes.c_double, I64, I64, I32, P, I64, P, P, P, I64,
                          I32, P], ctypes.c_int),
+        "dq_rope_table": ([P, I32, I64, P, I32, P], ctypes.c_int),
+        "dq_norm_rope": ([P, I64, ctypes.c_int, I64, I32, I32, P, P, P, I64, ctypes.c_int, I32, P], ctypes.c_int),
+        "dq_kv_write": ([P, P, I64, ctypes.c_int, P, I64, P, I64, P, P, I64, I32, P, P, I64, ctypes.c_int, P, I32, P], ctypes.c_int),
+        "dq_kv_read": ([P, P, I64, P, I64, P, I64, ctypes.c_int, I32, P], ctypes.c_int),
+        "dq_attn_create": ([I32, PP], ctypes.c_int),
+        "dq_attn_destroy": ([P], None),
+        "dq_attn_rows": ([P, P, I64, P, I64, ctypes.c_int, I32, P, P, P, I64, I32, P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -688,3 +697,302 @@ def dq_rmsnorm8(x, gain, eps: float, codes=None, scales=None, residual=None, h=N
     ptr = lambda t: None if t is None else t.data_ptr()
     _check(load().dq_rmsnorm8(ptr(x), ldx, ptr(residual), ldr, _dtype_of(x), ptr(gain), gdt, eps, n, c, group, ptr(h), ldh,
                               ptr(codes), ptr(scales), ptr(y), ldy, dev, _stream_on(stream, dev)), f)
+
+
+# ----------------------------------------------------------------------- heads ----
+class _Rope(ctypes.Structure):
+    _fields_ = [("axes", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("pairs", ctypes.c_int32 * 3),
+                ("positions", ctypes.c_int64 * 3), ("table", ctypes.c_void_p * 3)]
+
+
+class _HeadOps(ctypes.Structure):
+    _fields_ = [("norm", ctypes.c_int), ("gain_dt", ctypes.c_int), ("eps", ctypes.c_double), ("rope", ctypes.c_void_p),
+                ("pos", ctypes.c_void_p)]
+
+
+class _KV(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_tokens", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("bits", ctypes.c_int32)]
+
+
+class _Seqs(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int64), ("first", ctypes.c_void_p), ("length", ctypes.c_void_p), ("pages", ctypes.c_void_p),
+                ("pages_ld", ctypes.c_int64)]
+
+
+class _AttnOps(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_double), ("cap", ctypes.c_double), ("block", ctypes.c_int64), ("window", ctypes.c_int64),
+                ("prefix", ctypes.c_void_p)]
+
+
+def _on_gpu(func: str, name: str, t) -> int:
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _invalid(func, f"{name} must be a torch tensor on a GPU")
+    return t.get_device()
+
+
+class Rope:
+    """The position axes of a rotation: for each a table [positions][pairs][2] of
+    (cos, sin) in fp32 on one GPU, as dq_rope_table fills it.  Holds the tensors."""
+
+    def __init__(self, tables, interleaved: bool = True):
+        import torch
+        f = "Rope"
+        tables = list(tables)
+        if not 1 <= len(tables) <= 3:
+            _invalid(f, "a rotation has 1 to 3 axes")
+        self.device = _on_gpu(f, "table", tables[0])
+        for t in tables:
+            if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.shape[2] != 2 or 0 in t.shape:
+                _invalid(f, "a table must be a tensor [positions][pairs][2]")
+            _device_tensor(f, "table", t, t.shape, (torch.float32,), self.device, 8)
+        self.tables, self.axes = tables, len(tables)
+        self.c = _Rope(self.axes, int(bool(interleaved)))
+        for i, t in enumerate(tables):
+            self.c.positions[i], self.c.pairs[i], self.c.table[i] = t.shape[0], t.shape[1], t.data_ptr()
+        self.address = ctypes.addressof(self.c)
+
+
+class KV:
+    """A paged cache: k_codes and v_codes [pages][heads][page_tokens][head_dim]
+    in E4M3 (float8_e4m3fn, or uint8), or [..][head_dim / 2] in packed E2M1
+    (uint8, bits=4); k_scales and v_scales [..][head_dim / 32] in E8M0.  Holds
+    the tensors; fill the scales with zeros (or write every place) before they are read."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, bits: Optional[int] = None):
+        import torch
+        f = "KV"
+        self.device = _on_gpu(f, "k_codes", k_codes)
+        if k_codes.dim() != 4 or not isinstance(k_scales, torch.Tensor) or k_scales.dim() != 4:
+            _invalid(f, "codes and scales must be [pages][heads][page_tokens][..]")
+        pages, heads, tokens, width = k_codes.shape
+        dim = 32 * k_scales.shape[3]
+        held = 8 if width == dim else 4 if 2 * width == dim else 0
+        if not held or bits not in (None, held):
+            _invalid(f, f"{width} code bytes and {dim // 32} scales a token are neither 8 nor 4 bits" if not held else
+                     f"the codes are of {held} bits, not {bits}")
+        types = (torch.float8_e4m3fn, torch.uint8) if held == 8 else (torch.uint8,)
+        for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
+            _device_tensor(f, name, t, (pages, heads, tokens, width), types, self.device, 16)
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            _device_tensor(f, name, t, (pages, heads, tokens, dim // 32), (torch.float8_e8m0fnu, torch.uint8), self.device, 4)
+        self.tensors = (k_codes, k_scales, v_codes, v_scales)
+        self.pages, self.heads, self.page_tokens, self.head_dim, self.bits = pages, heads, tokens, dim, held
+        self.c = _KV(*(t.data_ptr() for t in self.tensors), pages, tokens, heads, dim, held)
+        self.address = ctypes.addressof(self.c)
+
+
+class Seqs:
+    """A ragged batch: first [seqs + 1] (rows first[b] .. first[b + 1] - 1 are the
+    last ones of sequence b), length [seqs] (cached tokens, those rows'
+    included) and pages [seqs][n] (the cache's page of each page_tokens tokens),
+    int32 on one GPU.  Holds the tensors; their values may change between calls."""
+
+    def __init__(self, first, length, pages):
+        import torch
+        f = "Seqs"
+        self.device = _on_gpu(f, "first", first)
+        if not isinstance(pages, torch.Tensor) or pages.dim() != 2 or 0 in pages.shape:
+            _invalid(f, "pages must be a tensor [seqs][pages to a sequence]")
+        n = pages.shape[0]
+        for name, t, shape in (("first", first, (n + 1,)), ("length", length, (n,)), ("pages", pages, tuple(pages.shape))):
+            _device_tensor(f, name, t, shape, (torch.int32,), self.device, 4)
+        self.tensors, self.seqs = (first, length, pages), n
+        self.c = _Seqs(n, first.data_ptr(), length.data_ptr(), pages.data_ptr(), pages.shape[1])
+        self.address = ctypes.addressof(self.c)
+
+
+def _raw(stream):
+    return None if stream is None else getattr(stream, "cuda_stream", stream)
+
+
+def _head_ops(func: str, norm, gains, eps, rope, pos, n: int, dim: int, device: int, in_cache: bool):
+    """The _HeadOps of a call; gains: (name, tensor or None, heads) of each part that is normed."""
+    import torch
+    if norm not in NORMS:
+        _invalid(func, f"norm must be one of {list(NORMS)}")
+    types = (torch.bfloat16, torch.float32)
+    dts = set()
+    for name, g, heads in gains:
+        if g is None:
+            continue
+        if norm is None:
+            _invalid(func, f"{name} without a norm")
+        _device_tensor(func, name, g, (dim if norm == "head" else heads * dim,), types, device, 16)
+        dts.add(_dtype_of(g))
+    if len(dts) > 1:
+        _invalid(func, "the gains must have one dtype")
+    if rope is None:
+        if pos is not None:
+            _invalid(func, "pos without a rope")
+    else:
+        if not isinstance(rope, Rope):
+            _invalid(func, "rope must be a Rope")
+        if rope.device != device:
+            _invalid(func, f"the rope's tables are on cuda:{rope.device}; expected cuda:{device}")
+        if pos is not None:
+            _device_tensor(func, "pos", pos, (n, rope.axes), (torch.int32,), device, 4)
+        elif rope.axes != 1:
+            _invalid(func, "a rotation by several axes needs pos")
+    return _HeadOps(NORMS[norm], dts.pop() if dts else DQ_F32, float(eps), rope.address if rope else None,
+                    pos.data_ptr() if pos is not None else None)
+
+
+def dq_rope_table(freq, positions: int, table, stream=None):
+    """Fills table [positions][pairs][2] (fp32, on a GPU) with (cos, sin) of p freq[j], angles in fp64."""
+    import torch
+    f = "dq_rope_table"
+    fr = np.ascontiguousarray(np.asarray(freq, dtype=np.float64))
+    if fr.ndim != 1:
+        _invalid(f, "freq must be 1-D")
+    dev = _on_gpu(f, "table", table)
+    _device_tensor(f, "table", table, (positions, fr.shape[0], 2), (torch.float32,), dev, 8)
+    _check(load().dq_rope_table(_ptr(fr), fr.shape[0], positions, table.data_ptr(), dev, _stream_on(stream, dev)), f)
+
+
+def dq_norm_rope(x, heads: int, y, norm: Optional[str] = None, gain=None, eps: float = 1e-6, rope: Optional[Rope] = None, pos=None,
+                 stream=None):
+    """y [N][heads * head_dim] = the heads of x normed (norm "head" or "row", with
+    gain [head_dim] or [heads * head_dim]) and rotated by their rows' positions
+    pos [N][axes] (int32; None: the row's number); either in bf16 or fp32, y may
+    be x itself."""
+    f = "dq_norm_rope"
+    call = _CALL or _native()
+    if call is not None:
+        status = call.norm_rope(x, heads, y, NORMS.get(norm, -1), gain, eps, rope, pos, _raw(stream))
+        if status is not None:
+            return _check(status, f) if status else None
+    import torch
+    dev = _on_gpu(f, "x", x)
+    if x.dim() != 2 or not isinstance(heads, int) or heads < 1 or x.shape[1] % heads:
+        _invalid(f, "x must be 2-D, its width a multiple of heads")
+    n, c = x.shape
+    types = (torch.bfloat16, torch.float32)
+    ldx, ldy = _row_tensor(f, "x", x, (n, c), types, dev, 16), _row_tensor(f, "y", y, (n, c), types, dev, 16)
+    ops = _head_ops(f, norm, [("gain", gain, heads)], eps, rope, pos, n, c // heads, dev, False)
+    _check(load().dq_norm_rope(x.data_ptr(), ldx, _dtype_of(x), n, heads, c // heads, None if gain is None else gain.data_ptr(),
+                               ctypes.byref(ops), y.data_ptr(), ldy, _dtype_of(y), dev, _stream_on(stream, dev)), f)
+
+
+def _cache_batch(func: str, kv, seqs):
+    if not isinstance(kv, KV) or not isinstance(seqs, Seqs):
+        _invalid(func, "kv must be a KV and seqs a Seqs")
+    if seqs.device != kv.device:
+        _invalid(func, f"the batch is on cuda:{seqs.device}; expected cuda:{kv.device}")
+    return kv.device
+
+
+def dq_kv_write(kv: KV, seqs: Seqs, k, v, q=None, y=None, norm: Optional[str] = None, gain=None, gain_q=None, eps: float = 1e-6,
+                rope: Optional[Rope] = None, pos=None, stream=None):
+    """Codes the N rows' keys k (normed with `gain` and rotated as in
+    dq_norm_rope; pos None: by their places in their sequences) and values v into
+    the cache; with queries q [N][q heads * head_dim] (normed with `gain_q`) y
+    receives them in bf16 or fp32."""
+    f = "dq_kv_write"
+    call = _CALL or _native()
+    if call is not None and isinstance(kv, KV) and isinstance(seqs, Seqs):
+        status = call.kv_write(kv, seqs, k, v, q, y, NORMS.get(norm, -1), gain, gain_q, eps, rope, pos, _raw(stream))
+        if status is not None:
+            return _check(status, f) if status else None
+    import torch
+    dev = _cache_batch(f, kv, seqs)
+    types = (torch.bfloat16, torch.float32)
+    n = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() == 2 else 0
+    c = kv.heads * kv.head_dim
+    ldk = _row_tensor(f, "k", k, (n, c), types, dev, 16)
+    ldv = _row_tensor(f, "v", v, (n, c), (k.dtype,), dev, 16)
+    if (q is None) != (y is None):
+        _invalid(f, "give both q and y or neither")
+    qh = ldq = ldy = ydt = 0
+    if q is not None:
+        cq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 2 else 0
+        if not cq or cq % kv.head_dim:
+            _invalid(f, "q must be 2-D, its width a multiple of head_dim")
+        qh = cq // kv.head_dim
+        ldq, ldy = _row_tensor(f, "q", q, (n, cq), (k.dtype,), dev, 16), _row_tensor(f, "y", y, (n, cq), types, dev, 16)
+        ydt = _dtype_of(y)
+    elif gain_q is not None:
+        _invalid(f, "gain_q without q")
+    ops = _head_ops(f, norm, [("gain", gain, kv.heads), ("gain_q", gain_q, qh)], eps, rope, pos, n, kv.head_dim, dev, True)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    _check(load().dq_kv_write(kv.address, seqs.address, n, _dtype_of(k), ptr(k), ldk, ptr(v), ldv, ptr(gain), ptr(q), ldq, qh,
+                              ptr(gain_q), ptr(y), ldy, ydt, ctypes.byref(ops), dev, _stream_on(stream, dev)), f)
+
+
+def dq_kv_read(kv: KV, seqs: Seqs, k=None, v=None, stream=None):
+    """The values of the rows' tokens: k and v [N][heads * head_dim] in bf16 or fp32, or one of them."""
+    import torch
+    f = "dq_kv_read"
+    dev = _cache_batch(f, kv, seqs)
+    given = [t for t in (k, v) if t is not None]
+    if not given:
+        _invalid(f, "give k or v")
+    n = given[0].shape[0] if isinstance(given[0], torch.Tensor) and given[0].dim() == 2 else 0
+    ld = [0 if t is None else _row_tensor(f, name, t, (n, kv.heads * kv.head_dim),
+                                          (torch.bfloat16, torch.float32) if t is given[0] else (given[0].dtype,), dev, 16)
+          for name, t in (("k", k), ("v", v))]
+    ptr = lambda t: None if t is None else t.data_ptr()
+    _check(load().dq_kv_read(kv.address, seqs.address, n, ptr(k), ld[0], ptr(v), ld[1], _dtype_of(given[0]), dev,
+                             _stream_on(stream, dev)), f)
+
+
+class Attn:
+    """Owns a dq_attn handle (a workspace for one stream at a time)."""
+
+    def __init__(self, handle: ctypes.c_void_p, device: int):
+        self.handle, self.device = handle, device
+        self.address = handle.value
+
+    def __del__(self):
+        if getattr(self, "handle", None) and _LIB is not None:
+            _LIB.dq_attn_destroy(self.handle)
+            self.handle = None
+
+
+def dq_attn_create(device: int = 0) -> Attn:
+    """Workspace of dq_attn_rows on one GPU."""
+    h = ctypes.c_void_p()
+    _check(load().dq_attn_create(device, ctypes.byref(h)), "dq_attn_create")
+    return Attn(h, device)
+
+
+def _scale(scale):
+    """The native call's scale: -1.0 for None, and None (not a number: refused there) for a -1.0 that was given."""
+    return -1.0 if scale is None else None if scale == -1.0 else scale
+
+
+def dq_attn_rows(kv: KV, seqs: Seqs, q, a: Attn, y, scale: Optional[float] = None, block: int = 1, window: int = 0, prefix=None,
+                 cap: float = 0.0, stream=None):
+    """y [N][q heads * head_dim] = softmax(scale q k) v of each row over the
+    tokens of its sequence that it sees, in q's type; scale None is
+    head_dim ** -0.5.  block 0: all tokens; else those up to the end of the row's
+    own block of `block` tokens (1: causal), of them the last `window` (0: all),
+    and the first prefix[b] (int32 [seqs], or None).  cap > 0: scores cap *
+    tanh(s / cap)."""
+    f = "dq_attn_rows"
+    call = _CALL or _native()
+    if call is not None and isinstance(kv, KV) and isinstance(seqs, Seqs) and isinstance(a, Attn):
+        status = call.attn_rows(kv, seqs, q, a, y, _scale(scale), block, window, prefix, cap, _raw(stream))
+        if status is not None:
+            return _check(status, f) if status else None
+    import torch
+    dev = _cache_batch(f, kv, seqs)
+    if not isinstance(a, Attn) or a.device != dev:
+        _invalid(f, f"a must be a workspace of cuda:{dev}")
+    types = (torch.bfloat16, torch.float32)
+    n, c = q.shape if isinstance(q, torch.Tensor) and q.dim() == 2 else (0, 0)
+    if not c or c % (kv.heads * kv.head_dim):
+        _invalid(f, "q must be 2-D, its heads a multiple of the cache's")
+    ldq = _row_tensor(f, "q", q, (n, c), types, dev, 16)
+    ldy = _row_tensor(f, "y", y, (n, c), (q.dtype,), dev, 16)
+    if prefix is not None:
+        _device_tensor(f, "prefix", prefix, (seqs.seqs,), (torch.int32,), dev, 4)
+    for name, i in (("block", block), ("window", window)):
+        if not isinstance(i, int) or not 0 <= i < 2 ** 31:
+            _invalid(f, f"{name} must be an integer in [0, 2^31)")
+    ops = _AttnOps(kv.head_dim ** -0.5 if scale is None else float(scale), float(cap), block, window,
+                   None if prefix is None else prefix.data_ptr())
+    _check(load().dq_attn_rows(kv.address, seqs.address, n, q.data_ptr(), ldq, _dtype_of(q), c // kv.head_dim, ctypes.byref(ops),
+                               a.handle, y.data_ptr(), ldy, dev, _stream_on(stream, dev)), f)
