@@ -23,30 +23,37 @@ struct Place {
     int t, page;
 };
 
-// The sequence that holds `row`: the last b with first[b] <= row, -1 if none.
-// All 64 lanes take part, each with a row of its own (`one`: the same row in the
-// whole wave); up to 64 sequences cost one load.
-__device__ __forceinline__ int sequence_of(const int* first, int seqs, long long row, bool one) {
-    const int lane = threadIdx.x & 63, step = (seqs + 63) >> 6;
-    const int f = lane * step < seqs ? first[lane * step] : INT32_MAX;
-    int b;
-    if (one) {
-        b = __popcll(__ballot(f <= row)) - 1;
-    } else {
-        b = -1;
-#pragma unroll
-        for (int s = 32; s > 0; s >>= 1)
-            if (__shfl(f, b + s, 64) <= row) b += s;
-        if (b < 63 && __shfl(f, b + 1, 64) <= row) ++b;
-    }
-    if (b < 0 || step == 1) return b;
-    int lo = b * step, n = min(step, seqs - lo);    // the answer is one of lo .. lo + n - 1
+// The sequences' starts, ends and lengths, as a wave looks them up: up to 63 of
+// them lie in its lanes after one round of loads; of more the lanes hold every
+// step-th start.
+struct Starts {
+    int first, length, step;
+};
+__device__ __forceinline__ Starts starts_of(const Pages& p) {
+    const int lane = threadIdx.x & 63, step = (p.seqs + 63) / 64, i = min(lane * step, p.seqs);
+    return {p.first[i], p.length[min(i, p.seqs - 1)], step};
+}
+
+// A sequence: its rows [f0, f1) and its length; f0 > f1 - 1 for none.
+struct Sequence {
+    int b, f0, f1, length;
+};
+// The last sequence b with at(first[b], b) <= x, by the lanes (x is the wave's).
+template <class At>
+__device__ __forceinline__ Sequence sequence_of(const Pages& p, const Starts& s, long long x, At at) {
+    const int lane = threadIdx.x & 63;
+    int b = __popcll(__ballot(lane * s.step < p.seqs && at(s.first, lane * s.step) <= x)) - 1;
+    if (b < 0) return {0, 0, 0, 0};
+    if (s.step == 1 && p.seqs < 64)
+        return {b, __builtin_amdgcn_readlane(s.first, b), __builtin_amdgcn_readlane(s.first, b + 1), __builtin_amdgcn_readlane(s.length, b)};
+    b *= s.step;
+    int n = min(s.step, p.seqs - b);                // the answer is one of b .. b + n - 1
     while (n > 1) {
         const int h = n >> 1;
-        if (first[lo + h] <= row) lo += h, n -= h;
+        if (at(p.first[b + h], b + h) <= x) b += h, n -= h;
         else n = h;
     }
-    return lo;
+    return {b, p.first[b], p.first[b + 1], p.length[b]};
 }
 
 // Page `i` of sequence b, or -1 where the table has none or names none of the cache's.
@@ -56,12 +63,17 @@ __device__ __forceinline__ int page_of(const Pages& p, int b, int i) {
     return (uint32_t)page < (uint32_t)p.pages ? page : -1;
 }
 
-__device__ __forceinline__ Place place_of(const Pages& p, long long row, bool one) {
-    const int b = sequence_of(p.first, p.seqs, row, one);
-    if (b < 0) return {NOWHERE, -1};
-    const long long f1 = p.first[b + 1], len = p.length[b];
-    if (row >= f1) return {NOWHERE, -1};
-    const int t = (int)max(len - f1 + row, -(1ll << 30));
+// The place of a wave's lanes' rows: `row` of its first lane, and one more for each `tpr` lanes.
+__device__ __forceinline__ Place place_of(const Pages& p, const Starts& s, long long row, int tpr) {
+    const int lane = threadIdx.x & 63;
+    int b = 0, t = NOWHERE;
+    for (int i = 0; i < 64; i += tpr, ++row) {      // (once where a row takes the wave)
+        const Sequence q = sequence_of(p, s, row, [](int f, int) { return (long long)f; });
+        const int at = row >= q.f0 && row < q.f1 ? (int)max((long long)q.length - q.f1 + row, -(1ll << 30)) : NOWHERE;
+        const bool mine = lane >= i;
+        b = mine ? q.b : b;
+        t = mine ? at : t;
+    }
     return {t, t < 0 ? -1 : page_of(p, b, t >> p.shift)};
 }
 
@@ -70,7 +82,7 @@ __device__ __forceinline__ long long token_row(const Pages& p, Place at, int hea
     return (((long long)at.page * p.heads + head) << p.shift) + (at.t & ((1 << p.shift) - 1));
 }
 
-typedef float v2f __attribute__((ext_vector_type(2)));
+
 
 // A scale code as the converters take it: 2^(e - 127), NaN for 255.
 __device__ __forceinline__ float scale_of(uint32_t e) { return __uint_as_float(e == 255 ? 0x7fc00000u : max(e << 23, 0x00400000u)); }

@@ -8,6 +8,7 @@ namespace dq {
 
 typedef uint32_t v4w __attribute__((ext_vector_type(4)));
 typedef uint32_t v2w __attribute__((ext_vector_type(2)));
+typedef float v2f __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ v4w get16(const void* p) { return *(const v4w*)p; }
 template <bool NT, class V>
 __device__ __forceinline__ void put(void* p, V v) {
@@ -17,6 +18,16 @@ __device__ __forceinline__ void put(void* p, V v) {
 
 template <class T> struct Stream;
 template <> struct Stream<uint16_t> {
+    // 8 channels as they are loaded, and their values: for code that has more to load before it uses them
+    typedef v4w Raw;
+    static __device__ __forceinline__ Raw raw(const uint16_t* p) { return get16(p); }
+    static __device__ __forceinline__ void values(Raw w, float* v) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
     static __device__ __forceinline__ void load(const uint16_t* p, float* v) {
         const v4w w = get16(p);
 #pragma unroll
@@ -34,6 +45,17 @@ template <> struct Stream<uint16_t> {
     }
 };
 template <> struct Stream<float> {
+    struct Raw {
+        v4w a, b;
+    };
+    static __device__ __forceinline__ Raw raw(const float* p) { return {get16(p), get16(p + 4)}; }
+    static __device__ __forceinline__ void values(Raw w, float* v) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = __uint_as_float(w.a[i]);
+            v[4 + i] = __uint_as_float(w.b[i]);
+        }
+    }
     static __device__ __forceinline__ void load(const float* p, float* v) {
         const v4w a = get16(p), b = get16(p + 4);
 #pragma unroll

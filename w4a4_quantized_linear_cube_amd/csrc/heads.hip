@@ -38,7 +38,6 @@ struct Part {
 
 struct Turn {
     const float* table[3];
-    int end[3];             // first pair behind each axis
     int count[3], positions[3];
     int pairs, axes, interleaved;
     const int* pos;         // [N][axes] or null
@@ -70,44 +69,76 @@ __device__ __forceinline__ float row_factor(double s, int channels, double eps) 
     return (float)(1.0 / sqrt(s / (double)channels + eps));
 }
 
-// The coefficients of one lane's 8 channels at one row: out = v cc + partner ss.
+// A kernel's argument as a value of its own: the compiler would else turn a
+// choice between two arguments into a load from the chosen one's address.
+__device__ __forceinline__ int fixed(int v) { return __builtin_amdgcn_readfirstlane(v); }
+typedef const __attribute__((address_space(1))) float* Table;
+__device__ __forceinline__ Table fixed(const float* p) {
+    const uint64_t v = (uint64_t)(uintptr_t)p;
+    return (Table)(uintptr_t)((uint64_t)(uint32_t)fixed((int)(v >> 32)) << 32 | (uint32_t)fixed((int)v));
+}
+
+// The coefficients of one lane's 8 channels at one row: out = v c + partner s,
+// for channels of `on`.
 struct Coef {
     float c[8], s[8];
     uint32_t on;            // channels that are rotated
 };
-__device__ __forceinline__ float2 pair_at(const Turn& r, const int (&at)[3], int j) {
-    const bool a1 = j >= r.end[0], a2 = j >= r.end[1];
-    const int k = j - (a2 ? r.end[1] : a1 ? r.end[0] : 0), n = a2 ? r.count[2] : a1 ? r.count[1] : r.count[0];
-    const int p = a2 ? at[2] : a1 ? at[1] : at[0], most = a2 ? r.positions[2] : a1 ? r.positions[1] : r.positions[0];
-    const float* table = a2 ? r.table[2] : a1 ? r.table[1] : r.table[0];
-    if ((uint32_t)p >= (uint32_t)most) return make_float2(__builtin_nanf(""), __builtin_nanf(""));
-    return *(const float2*)(table + 2 * ((size_t)(uint32_t)p * n + k));
+// (cos, sin) of COUNT pairs from j0 on, all loads issued before any is used
+// (pairs past the last: the last's).
+template <int COUNT>
+__device__ __forceinline__ void pairs_from(const Turn& r, const int (&at)[3], int j0, float2 (&cs)[COUNT]) {
+    typedef const __attribute__((address_space(1))) v2f* From;
+    const float nan = __builtin_nanf("");
+    const int n0 = fixed(r.count[0]), n1 = fixed(r.count[1]), e0 = n0, e1 = n0 + n1, last = fixed(r.pairs) - 1;
+    const bool in0 = (uint32_t)at[0] < (uint32_t)r.positions[0];
+    // (each axis' row from where pair 0 would be, at position 0 where its own is outside)
+    const Table w0 = fixed(r.table[0]) + 2 * ((size_t)(in0 ? (uint32_t)at[0] : 0u) * n0);
+    v2f got[COUNT];
+    if (r.axes == 1) {
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) got[i] = *(From)(w0 + 2 * min(j0 + i, last));
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) cs[i] = in0 ? make_float2(got[i][0], got[i][1]) : make_float2(nan, nan);
+        return;
+    }
+    const bool in1 = (uint32_t)at[1] < (uint32_t)r.positions[1], in2 = (uint32_t)at[2] < (uint32_t)r.positions[2];
+    const Table w1 = fixed(r.table[1]) + 2 * ((long long)((size_t)(in1 ? (uint32_t)at[1] : 0u) * n1) - e0);
+    const Table w2 = fixed(r.table[2]) + 2 * ((long long)((size_t)(in2 ? (uint32_t)at[2] : 0u) * fixed(r.count[2])) - e1);
+    bool in[COUNT];
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+        const int j = min(j0 + i, last);
+        const bool a1 = j >= e0, a2 = j >= e1;
+        got[i] = *(From)((a2 ? w2 : a1 ? w1 : w0) + 2 * j);
+        in[i] = a2 ? in2 : a1 ? in1 : in0;
+    }
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) cs[i] = in[i] ? make_float2(got[i][0], got[i][1]) : make_float2(nan, nan);
 }
 __device__ __forceinline__ Coef coefficients(const Turn& r, const int (&at)[3], int lane) {
     Coef k;
-    k.on = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) k.c[e] = 1.0f, k.s[e] = 0.0f;
+    const int turned = 2 * r.pairs - 8 * lane;      // of the lane's channels, if pairs are side by side
     if (r.interleaved) {
+        float2 cs[4];
+        pairs_from<4>(r, at, 4 * lane, cs);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (4 * lane + i >= r.pairs) continue;
-            const float2 v = pair_at(r, at, 4 * lane + i);
-            k.c[2 * i] = k.c[2 * i + 1] = v.x;
-            k.s[2 * i] = -v.y;
-            k.s[2 * i + 1] = v.y;
-            k.on |= 3u << (2 * i);
+            k.c[2 * i] = k.c[2 * i + 1] = cs[i].x;
+            k.s[2 * i] = -cs[i].y;
+            k.s[2 * i + 1] = cs[i].y;
         }
-    } else if (8 * lane < 2 * r.pairs) {
+        k.on = turned >= 8 ? 0xffu : turned <= 0 ? 0u : (1u << turned) - 1;
+    } else {
+        float2 cs[8];
         const bool second = 8 * lane >= r.pairs;
-        const int j = 8 * lane - (second ? r.pairs : 0);
+        pairs_from<8>(r, at, 8 * lane - (second ? r.pairs : 0), cs);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float2 v = pair_at(r, at, j + e);
-            k.c[e] = v.x;
-            k.s[e] = second ? v.y : -v.y;
+        for (int i = 0; i < 8; ++i) {
+            k.c[i] = cs[i].x;
+            k.s[i] = second ? cs[i].y : -cs[i].y;
         }
-        k.on = 0xff;
+        k.on = turned > 0 ? 0xffu : 0u;
     }
     return k;
 }
@@ -160,13 +191,28 @@ __device__ __forceinline__ uint32_t encode_group(float* v, v2w& d) {
     }
 }
 
+__device__ __forceinline__ void load_gains(const HeadsArgs& a, const Part& p, int lane, int c, float* g) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] = 1.0f;
+    if (!p.g) return;
+    const int at = 8 * (p.norm == DQ_NORM_HEAD ? lane : min(c, p.nch - 1));
+    if (a.g_bf16) Stream<uint16_t>::load((const uint16_t*)p.g + at, g);
+    else Stream<float>::load((const float*)p.g + at, g);
+}
+
 // A row's part is held in registers by tpr threads (of several blocks, where no
 // sum crosses them), CH chunks of 8 channels each, chunk i of thread t: i tpr + t.
 // tpr is a multiple of the lanes to a head, so a thread's chunks are at one place
 // of their heads and share the rotation's coefficients.
+// Loads come in rounds without a branch between them (rows and chunks past the
+// end read the last one): the row's values, gains and sequences, then its
+// coefficients and page.
 template <class T, int CH>
 __global__ __launch_bounds__(1024) void k_heads(HeadsArgs a) {
     __shared__ double sums[64];                     // [row of the block][block of 64 chunks]
+    // (the arguments' cache lines, all at once)
+    asm volatile("" ::"s"(a.part[0].nch), "s"(a.part[1].ldy), "s"(a.part[2].g), "s"(a.part[2].turn), "s"(a.turn.table[1]), "s"(a.pages.first),
+                 "s"(a.N), "s"(a.nt));
     int seg = blockIdx.y, pi = 0;
     if (seg >= a.part[0].segs) {
         seg -= a.part[0].segs, pi = 1;
@@ -174,37 +220,36 @@ __global__ __launch_bounds__(1024) void k_heads(HeadsArgs a) {
     }
     const Part& p = a.part[pi];
     const int tpr = a.tpr, shift = __builtin_ctz(tpr), t = threadIdx.x & (tpr - 1), sub = threadIdx.x >> shift;
-    const long long row = a.first + (long long)blockIdx.x * (blockDim.x >> shift) + sub;
+    const long long row0 = a.first + (long long)blockIdx.x * (blockDim.x >> shift), row = row0 + sub, near = min(row, a.N - 1);
     const bool live = row < a.N;
     const int c0 = seg * tpr * CH + t, lane = t & (a.lph - 1);
-    float v[CH][8];
-    if (live) {
-        const T* xp = (const T*)p.x + row * p.ld;
+    typename Stream<T>::Raw raw[CH];
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
-            if (c0 + i * tpr < p.nch) Stream<T>::load(xp + 8 * (c0 + i * tpr), v[i]);
+    for (int i = 0; i < CH; ++i) raw[i] = Stream<T>::raw((const T*)p.x + near * p.ld + 8 * min(c0 + i * tpr, p.nch - 1));
+    float gain[8];          // (of a thread's one chunk)
+    if constexpr (CH == 1) load_gains(a, p, lane, c0, gain);
+    int pos[3] = {(int)near, 0, 0};
+    if (p.turn && a.turn.pos) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) pos[i] = a.turn.pos[near * a.turn.axes + min(i, a.turn.axes - 1)];
     }
-    // the row's place, while its values are on their way
     Place at{-1, -1};
-    if (a.pages.first) at = place_of(a.pages, min(row, a.N - 1), tpr >= 64);
-    Coef k{};
-    if (p.turn && live) {
-        int pos[3] = {0, 0, 0};
-        if (a.turn.pos) {
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-                if (i < a.turn.axes) pos[i] = a.turn.pos[row * a.turn.axes + i];
-        } else {
-            pos[0] = a.pages.first ? at.t : (int)row;
-        }
-        k = coefficients(a.turn, pos, lane);
+    if (a.pages.first) {
+        const Starts starts = starts_of(a.pages);
+        at = place_of(a.pages, starts, row0 + ((threadIdx.x & ~63u) >> shift), tpr);
+        if (!a.turn.pos) pos[0] = at.t;
     }
+    Coef k{};
+    if (p.turn) k = coefficients(a.turn, pos, lane);
+    float v[CH][8];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) Stream<T>::values(raw[i], v[i]);
     if (p.norm != DQ_NORM_NONE) {
         double q[CH];
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             q[i] = 0.0;
-            if (live && c0 + i * tpr < p.nch) {
+            if (c0 + i * tpr < p.nch) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) q[i] = __builtin_fma((double)v[i][j], (double)v[i][j], q[i]);
             }
@@ -235,20 +280,9 @@ __global__ __launch_bounds__(1024) void k_heads(HeadsArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int c = c0 + i * tpr;
-            if (!live || c >= p.nch) continue;
-            float g[8];
-            const int gc = 8 * (p.norm == DQ_NORM_HEAD ? lane : c);
-            if (!p.g) {
+            if constexpr (CH > 1) load_gains(a, p, lane, c0 + i * tpr, gain);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) g[j] = 1.0f;
-            } else if (a.g_bf16) {
-                Stream<uint16_t>::load((const uint16_t*)p.g + gc, g);
-            } else {
-                Stream<float>::load((const float*)p.g + gc, g);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = (v[i][j] * f[i]) * g[j];
+            for (int j = 0; j < 8; ++j) v[i][j] = (v[i][j] * f[i]) * gain[j];
         }
     }
     if (p.turn) {
@@ -323,7 +357,7 @@ __global__ __launch_bounds__(512) void k_read(ReadArgs a) {
     const int w = blockIdx.y + a.part0, tpr = a.tpr, shift = __builtin_ctz(tpr);
     const long long row = a.first + (long long)blockIdx.x * (blockDim.x >> shift) + (threadIdx.x >> shift);
     const int t = threadIdx.x & (tpr - 1);
-    const Place at = place_of(a.pages, min(row, a.N - 1), tpr >= 64);
+    const Place at = place_of(a.pages, starts_of(a.pages), row - ((threadIdx.x & 63) >> shift), tpr);
     if (row >= a.N || at.t == NOWHERE) return;
     T* y = (T*)a.y[w] + row * a.ldy[w];
     constexpr int W = BITS == 8 ? 4 : 2;            // words of codes to a chunk
@@ -469,14 +503,16 @@ dq_status check_ops(const dq_head_ops* ops, int head_dim, Turn* t) {
     if ((uintptr_t)ops->pos_dev % 4 != 0) return fail(DQ_ERR_INVALID_ARG, "pos_dev must be 4-byte aligned");
     int64_t pairs = 0;
     for (int i = 0; i < 3; ++i) {
-        t->end[i] = (int)pairs;
-        if (i >= r->axes) continue;
+        if (i >= r->axes) {                         // (never chosen, but its address is formed)
+            t->table[i] = t->table[0];
+            t->positions[i] = 1;
+            continue;
+        }
         if (r->pairs[i] < 1 || r->pairs[i] > MAX_PAIRS) return fail(DQ_ERR_SHAPE, "an axis has 1 to 128 pairs");
         if (r->positions[i] < 1 || r->positions[i] >= int64_t(1) << 31) return fail(DQ_ERR_SHAPE, "positions must be in [1, 2^31)");
         if (!r->table_dev[i]) return fail(DQ_ERR_INVALID_ARG, "table_dev is NULL");
         if ((uintptr_t)r->table_dev[i] % 8 != 0) return fail(DQ_ERR_INVALID_ARG, "table_dev must be 8-byte aligned");
         pairs += r->pairs[i];
-        t->end[i] = (int)pairs;
         t->table[i] = r->table_dev[i];
         t->count[i] = r->pairs[i];
         t->positions[i] = (int)r->positions[i];
