@@ -18,29 +18,33 @@
 //     of LDS as bf16 and comes back transposed.
 // The four waves of a workgroup take blocks of tokens in turn, without a
 // barrier, and join at the end; a long cache is split over workgroups, whose sums
-// meet in the workspace: whichever ends last joins them in order.
+// a second launch joins in order.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 #include <cmath>
 #include <memory>
 #include <new>
+#include <type_traits>
 
 #include "dq.h"
 #include "dq_heads.h"
 
 struct dq_attn {
     int device = 0;
-    float* sums = nullptr;     // [unit][row block][16][D] sums, then [unit][row block][16][4] statistics
-    int* arrivals = nullptr;   // parts that have ended, of each tile and head (0 between launches)
+    float* sums = nullptr;     // [unit][row block][16][D] sums, then [unit][row block][16][4] statistics, then tiles
 };
 
 namespace dq {
 namespace {
 
 // Units (tiles x key heads x parts) that may meet in the workspace, and blocks of 16 rows to one.
-constexpr int MAX_UNITS = 2048, MAX_RB = 4;
+constexpr int MAX_UNITS = 2048, MAX_RB = 4, MAX_PARTS = 256;
 constexpr size_t SUM_FLOATS = size_t(MAX_UNITS) * MAX_RB * 16 * 128, STAT_FLOATS = size_t(MAX_UNITS) * MAX_RB * 16 * 4;
+// A tile that is in parts: how many (0 or 1: nothing to join), its rows, and its sequence's first row and rows before it.
+struct TileInfo {
+    int used, rows, f0, r0;
+};
 constexpr float LOG2E = 1.44269504088896340736f;
 
 struct AttnArgs {
@@ -54,28 +58,16 @@ struct AttnArgs {
     int N, G;               // query rows; query heads to a key head
     int parts;              // workgroups that may share a tile's tokens
     long long block, window;
-    float scale, cap, cap_inv;   // scale: of the scores in base 2, or (with a cap) of the scores
+    float scale;            // of q k, for powers of 2; 1 with a cap
+    float cap, cap_in;      // the cap (0: none), and scale / cap
     float* sums;
     float* stats;
-    int* arrivals;
+    TileInfo* tiles;        // [key head][tile]
 };
 
-typedef unsigned v4u __attribute__((ext_vector_type(4)));
 typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
-
-// Sums that workgroups hand to each other pass the caches of one XCD by (the
-// agent scope's cache bit), so none needs writing back or invalidating.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t shared_floats(float* p, size_t floats) {
-    return __builtin_amdgcn_make_buffer_rsrc(p, (short)0, (int)(floats * 4), 0x00020000);
-}
-__device__ __forceinline__ void hand_over(__amdgpu_buffer_rsrc_t r, size_t at, v4f v) {
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, v), r, (int)(at * 4), 0, 16);
-}
-__device__ __forceinline__ v4f take_over(__amdgpu_buffer_rsrc_t r, size_t at) {
-    return __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(at * 4), 0, 16));
-}
 
 // Maximum and sum over the four lanes that hold one row.
 __device__ __forceinline__ float max_rows(float v) {
@@ -93,6 +85,8 @@ __device__ __forceinline__ float sum_rows(float v) {
     const v2w b = __builtin_bit_cast(v2w, __builtin_amdgcn_permlane32_swap(x, x, false, false));
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
+typedef const __attribute__((address_space(4))) int* Scalars;   // (nothing that the kernel writes)
+
 __device__ __forceinline__ float power(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // tanh: (1 - t) / (1 + t) with t = e^-2|x|, and its series where that cancels.
@@ -143,10 +137,52 @@ struct Tokens {
     static constexpr int VW = 16 * BITS / 32;
     uint32_t k[2][KW], v[VP][VW];
     uint32_t ks[2], vs[VP];
+
+    // Whether one of the lane's values may not be finite: a NaN code, or a scale
+    // that is NaN or so large that a value may pass bf16's range.
+    __device__ __forceinline__ bool not_finite() const {
+        uint32_t nan = 0, large = 0;
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            large |= ((vs[i] & 0x7f7f7f7fu) + 0x0a0a0a0au) & vs[i];   // (a code of 246 or more: carries into the sign's place, which it has)
+            if constexpr (BITS == 8) {
+#pragma unroll
+                for (int j = 0; j < VW; ++j) nan |= (v[i][j] & 0x7f7f7f7fu) + 0x01010101u;   // (0x7f: carries into the sign's place)
+            }
+        }
+        return ((nan | large) & 0x80808080u) != 0;
+    }
 };
+// Of 8 bf16 values those that are not finite: as ones (else zeros), or put to zero.
+template <bool ONES>
+__device__ __forceinline__ v8bf not_finite_of(v8bf v) {
+    v4w w = __builtin_bit_cast(v4w, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t c = (((w[i] & 0x7f807f80u) + 0x00800080u) >> 15) & 0x00010001u;   // (a full exponent carries into the sign's place)
+        w[i] = ONES ? c * 0x3f80u : w[i] & ~(c * 0xffffu);
+    }
+    return __builtin_bit_cast(v8bf, w);
+}
+
+// Four channels of a row: the weighted values over the weights' sum, or zero where no token was seen.
+__device__ __forceinline__ void store4(float* y, v4f o, float sum, bool any) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = any ? o[e] / sum : 0.0f;
+    *(v4f*)y = o;
+}
+__device__ __forceinline__ void store4(uint16_t* y, v4f o, float sum, bool any) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = any ? o[e] / sum : 0.0f;
+    const v2b a{(__bf16)o[0], (__bf16)o[1]}, b{(__bf16)o[2], (__bf16)o[3]};
+    *(v2w*)y = v2w{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
+}
+
+// Waves to a SIMD that the registers are kept for.
+constexpr int waves_of(bool f32, int D, int RB) { return D == 64 ? (RB == 1 ? (f32 ? 3 : 4) : RB == 2 ? 2 : 1) : RB == 1 ? (f32 ? 2 : 3) : RB == 2 && !f32 ? 2 : 1; }
 
 template <class T, int BITS, int D, int RB>
-__global__ __launch_bounds__(256) void k_attn(AttnArgs a) {
+__global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(AttnArgs a) {
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int QP = F32 ? 3 : 1, PP = F32 ? 2 : 1;      // bf16 parts of q and of the weights
     constexpr int TR = 16 * RB, CB = D / 16, NJ = D / 32;  // rows of a tile; blocks of 16 channels; steps of 32 channels
@@ -154,76 +190,148 @@ __global__ __launch_bounds__(256) void k_attn(AttnArgs a) {
     using Tok = Tokens<BITS, D>;
     __shared__ __attribute__((aligned(16))) uint8_t lds[4][64 * D];   // a wave's V [32][D] bf16, then its sums [16][D] fp32
     __shared__ float stat[4][3][TR];
-    __shared__ int arrived;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, g = lane >> 4;
     const int part = (int)blockIdx.x % a.parts, tile = (int)blockIdx.x / a.parts, head = blockIdx.y;
 
+    // (what is the same in the whole wave is kept in scalar registers)
+    const auto one = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+    // (the arguments' cache lines, all at once)
+    asm volatile("" ::"s"(a.q), "s"(a.scales[1]), "s"(a.prefix), "s"(a.tiles));
+
     // ---- the tile's sequence and rows.  Sequence b's tiles are numbered from
     // floor(first[b] G / TR) + b on, which leaves each as many as it needs.
-    int b;
-    {
-        const int* first = a.pages.first;
-        const int B = a.pages.seqs, step = (B + 63) >> 6;
-        const auto base = [&](int i) { return ((long long)first[i] * a.G) / TR + i; };
-        b = __popcll(__ballot(lane * step < B && base(min(lane * step, B - 1)) <= tile)) - 1;
-        if (b < 0) return;
-        int lo = b * step, n = min(step, B - lo);
-        while (n > 1) {
-            const int h = n >> 1;
-            if (base(lo + h) <= tile) lo += h, n -= h;
-            else n = h;
-        }
-        b = __builtin_amdgcn_readfirstlane(lo);
-    }
-    const int f0 = min(max(a.pages.first[b], 0), a.N), f1 = min(max(a.pages.first[b + 1], f0), a.N);
-    const int length = max(a.pages.length[b], 0);
+    const auto base_of = [&](int first, int i) { return min(max(first, 0), a.N) * a.G / TR + i; };
+    const Starts starts = starts_of(a.pages);
+    const Sequence sq = sequence_of(a.pages, starts, tile, [&](int f, int i) { return (long long)base_of(f, i); });
+    const int b = one(sq.b), f0 = one(min(max(sq.f0, 0), a.N)), f1 = one(min(max(sq.f1, f0), a.N)), length = one(max(sq.length, 0));
     const int L = (int)min((long long)length, min((long long)a.pages.ld << a.pages.shift, (1ll << 31) - 64));   // tokens that may have a page
-    const long long rows = (long long)(f1 - f0) * a.G, r0 = ((long long)tile - (((long long)a.pages.first[b] * a.G) / TR + b)) * TR;
-    if (r0 < 0 || r0 >= rows) return;
-    const int pf = a.block && a.prefix ? min(max(a.prefix[b], 0), L) : 0;
+    const int rows = (f1 - f0) * a.G, r0 = (tile - base_of(sq.f0, b)) * TR;
+    const int tiles = (int)gridDim.x / a.parts;
+    TileInfo* const info = a.tiles + head * tiles + tile;
+    const bool tells = a.parts > 1 && part == 0 && tid == 0;
+    if (r0 < 0 || r0 >= rows) {
+        if (tells) *info = TileInfo{0, 0, 0, 0};
+        return;
+    }
+    const int pf = a.block && a.prefix ? min(max(((Scalars)(uintptr_t)a.prefix)[b], 0), L) : 0;
 
     // ---- what each row sees: [lo, hi) and [0, pf)
-    const long long t0 = (long long)length - (f1 - f0);    // the first row's place
-    const auto end_of = [&](long long t) {
-        const long long q = t >= 0 ? t / a.block : -((-t + a.block - 1) / a.block);
-        return (q + 1) * a.block;
+    const int t0 = length - (f1 - f0);                     // the first row's place
+    const auto sees = [&](int r, int* lo, int* hi) {       // r: packed row
+        *lo = 0, *hi = L;
+        if (!a.block) return;
+        const int t = t0 + (int)((uint32_t)r / (uint32_t)a.G);
+        // the end of the row's block (0 before the first token)
+        const long long e = t < 0 ? 0 : a.block == 1 ? t + 1ll : (long long)((uint32_t)t / (uint32_t)a.block + 1) * a.block;
+        *hi = (int)min(e, (long long)L);
+        if (a.window) *lo = (int)min(max(e - a.window, 0ll), (long long)L);
     };
-    const auto sees = [&](long long r, int* lo, int* hi) {  // r: packed row
-        if (!a.block) {
-            *lo = 0, *hi = L;
-            return;
-        }
-        const long long e = end_of(t0 + r / a.G);
-        *hi = (int)min(max(e, 0ll), (long long)L);
-        *lo = a.window ? (int)min(max(e - a.window, 0ll), (long long)L) : 0;
-    };
-    int lo[RB], hi[RB];
-#pragma unroll
-    for (int i = 0; i < RB; ++i) {
-        lo[i] = hi[i] = 0;
-        if (r0 + 16 * i + r16 < rows) sees(r0 + 16 * i + r16, &lo[i], &hi[i]);
-    }
     int lo0, hi0, lo1, hi1;                                // of the tile's first and last row
     sees(r0, &lo0, &hi0);
     sees(min(rows, r0 + TR) - 1, &lo1, &hi1);
+    lo0 = one(lo0), hi0 = one(hi0), lo1 = one(lo1), hi1 = one(hi1);
     // blocks of 32 tokens that some row sees: [0, na) and [b0, b0 + nb)
-    int na = (pf + 31) >> 5, b0 = lo0 >> 5, nb = max(((hi1 + 31) >> 5) - b0, 0);
-    if (hi1 <= lo0) nb = 0;
-    if (na >= b0) nb = max(max(b0 + nb, na), 0), b0 = 0, na = 0;
+    int na = (pf + 31) >> 5, b0 = lo0 >> 5, nb = hi1 > lo0 ? ((hi1 + 31) >> 5) - b0 : 0;
+    if (na >= b0) nb = max(b0 + nb, na), b0 = 0, na = 0;
     const int blocks = na + nb;
-    int per = (blocks + a.parts - 1) / a.parts;
-    per = (per + 3) & ~3;                                  // (whole rounds of the four waves)
+    const int per = ((blocks + a.parts - 1) / a.parts + 3) & ~3;   // (whole rounds of the four waves)
     const int used = blocks ? (blocks + per - 1) / per : 1;
+    if (tells) *info = TileInfo{used, min(rows - r0, TR), f0, r0};
     if (part >= used) return;
     const int c_end = min(blocks, (part + 1) * per);
+
+    // ---- the cache
+    const auto token0 = [&](int c) { return (c < na ? c : c - na + b0) << 5; };
+    struct Two {
+        int p[2];
+    };
+    const auto pages_at = [&](int c) {                     // pages of a block's two halves
+        // (both loads at once: places past the table's end read its last entry, a block past the last the last block's)
+        const int t = token0(max(min(c, blocks - 1), 0)), i0 = t >> a.pages.shift, i1 = (t + 16) >> a.pages.shift;
+        // (scalar loads: a wave's wait for them does not wait for the cache's)
+        const Scalars table = (Scalars)(uintptr_t)(a.pages.table + (size_t)b * a.pages.ld);
+        const int p0 = table[min(i0, a.pages.ld - 1)], p1 = table[min(i1, a.pages.ld - 1)];
+        Two r;
+        r.p[0] = t < L && (uint32_t)p0 < (uint32_t)a.pages.pages ? p0 : -1;
+        r.p[1] = t + 16 < L && (uint32_t)p1 < (uint32_t)a.pages.pages ? p1 : -1;
+        return r;
+    };
+    const int mask = (1 << a.pages.shift) - 1;
+    // the aligned word that holds a row's scale codes (with D 64 two rows'), and the place of one in it
+    const auto scale_word = [&](const uint8_t* p, long long row) { return *(const uint32_t*)(p + (row * (D / 32) & ~3ll)); };
+    const auto scale_in = [](uint32_t word, int row, int group) {
+        return scale_of(word >> (8 * (D == 128 ? group : 2 * (row & 1) + group)) & 0xff);
+    };
+    Tok x;
+    const auto row_of = [&](int c, Two pg, int h) {        // the cache's row of a half's first token (in page 0 where there is none)
+        return (((long long)max(pg.p[h], 0) * a.pages.heads + head) << a.pages.shift) + ((token0(max(min(c, blocks - 1), 0)) + 16 * h) & mask);
+    };
+    const auto load_keys = [&](int c, Two pg) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const long long row = row_of(c, pg, h) + r16;
+            load_words<Tok::KW>(a.codes[0] + row * (D * BITS / 8) + g * (Tok::KW * 4), x.k[h]);
+            x.ks[h] = scale_word(a.scales[0], row);
+        }
+    };
+    const auto load_values = [&](int c, Two pg) {
+#pragma unroll
+        for (int i = 0; i < Tok::VP; ++i) {                // piece i: token (64 / LPR) i + lane / LPR
+            const int tok = (64 / LPR) * i + lane / LPR, c16 = lane % LPR;
+            const long long row = row_of(c, pg, (64 / LPR) * i < 16 ? 0 : 1) + (tok & 15);
+            load_words<Tok::VW>(a.codes[1] + row * (D * BITS / 8) + c16 * (Tok::VW * 4), x.v[i]);
+            x.vs[i] = scale_word(a.scales[1], row);
+        }
+    };
+
+    v4f acc[RB][CB];
+    float m[RB], l[RB];
+    uint32_t seen = 0;                                     // row blocks whose row (of this lane) saw a token
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+        m[i] = -INFINITY, l[i] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < CB; ++c) acc[i][c] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    // V [32][D] bf16: 32 bytes (16 channels) of a token at slot c16 ^ its own, so
+    // that the transposing reads' 8 rows of 32 bytes meet 64 banks
+    uint8_t* const mine = lds[w];                          // (64 D bytes: the slots' exclusive or stays inside)
+    const auto place_v = [&](int tok, int c16) {
+        const int s = D == 128 ? tok & 7 : (tok >> 1) & 3;
+        return tok * (2 * D) + ((c16 ^ s) << 5);
+    };
+    const auto place_values = [&](auto change) {
+#pragma unroll
+        for (int i = 0; i < Tok::VP; ++i) {
+            const int tok = (64 / LPR) * i + lane / LPR, c16 = lane % LPR;
+            const float scale = scale_in(x.vs[i], tok, c16 / 2);
+            uint4* to = (uint4*)(mine + place_v(tok, c16));
+            to[0] = __builtin_bit_cast(uint4, change(decode8<BITS>(x.v[i], scale)));
+            to[1] = __builtin_bit_cast(uint4, change(decode8<BITS>(x.v[i] + BITS / 4, scale)));
+        }
+    };
+    const auto read_v = [&](int cb) {                      // V^T: channels 16 cb + lane % 16, tokens 4 g .. and 16 + 4 g ..
+        const int tok = 4 * g + (r16 >> 2), in = (r16 & 3) * 8;
+        const uint8_t* from = mine + ((place_v(tok, 0) + in) ^ (cb << 5));
+        const v4s p = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)from);
+        const v4s q = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(from + 32 * D));   // (16 tokens on)
+        typedef short v8s __attribute__((ext_vector_type(8)));
+        return __builtin_bit_cast(v8bf, v8s{p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]});
+    };
+
+    const int c_first = part * per + w;
+    Two pg = pages_at(c_first), pg_next = pages_at(c_first + 4);
+    load_keys(c_first, pg);
+    load_values(c_first, pg);
 
     // ---- q as the second operand: lane (row, g), channels (D / 4) g + 8 j ..
     v8bf q[RB][QP][NJ];
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
-        const long long r = min(r0 + 16 * i + r16, rows - 1);
-        const T* p = (const T*)a.q + (f0 + r / a.G) * a.ldq + ((long long)head * a.G + r % a.G) * D + (D / 4) * g;
+        const uint32_t r = min(r0 + 16 * i + r16, rows - 1), n = r / (uint32_t)a.G;
+        const T* p = (const T*)a.q + (long long)(f0 + n) * a.ldq + (head * a.G + (int)(r - n * a.G)) * D + (D / 4) * g;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             if constexpr (F32) {
@@ -251,88 +359,22 @@ __global__ __launch_bounds__(256) void k_attn(AttnArgs a) {
         }
     }
 
-    // ---- the cache
-    const auto token0 = [&](int c) { return (c < na ? c : c - na + b0) << 5; };
-    struct Two {
-        int p[2];
-    };
-    const auto pages_at = [&](int c) {                     // pages of a block's two halves
-        Two r;
-        const int t = token0(min(c, blocks - 1)), i0 = t >> a.pages.shift, i1 = (t + 16) >> a.pages.shift;
-        r.p[0] = blocks && t < L ? page_of(a.pages, b, i0) : -1;
-        r.p[1] = i1 == i0 ? r.p[0] : blocks && t + 16 < L ? page_of(a.pages, b, i1) : -1;
-        r.p[0] = __builtin_amdgcn_readfirstlane(r.p[0]);
-        r.p[1] = __builtin_amdgcn_readfirstlane(r.p[1]);
-        return r;
-    };
-    const int mask = (1 << a.pages.shift) - 1;
-    const auto load = [&](int c, Two pg) {
-        Tok x;
-        const int t = token0(min(c, blocks - 1));
-        long long base[2];                                 // the cache's row of each half's first token (page 0 where there is none)
+    int lo[RB], hi[RB];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            base[h] = (((long long)max(pg.p[h], 0) * a.pages.heads + head) << a.pages.shift) + ((t + 16 * h) & mask);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const long long row = base[h] + r16;
-            load_words<Tok::KW>(a.codes[0] + row * (D * BITS / 8) + g * (Tok::KW * 4), x.k[h]);
-            x.ks[h] = a.scales[0][row * (D / 32) + (D / 4 * g) / 32];
-        }
-#pragma unroll
-        for (int i = 0; i < Tok::VP; ++i) {                // piece i: token (64 / LPR) i + lane / LPR
-            const int tok = (64 / LPR) * i + lane / LPR, c16 = lane % LPR;
-            const long long row = ((64 / LPR) * i < 16 ? base[0] : base[1]) + (tok & 15);
-            load_words<Tok::VW>(a.codes[1] + row * (D * BITS / 8) + c16 * (Tok::VW * 4), x.v[i]);
-            x.vs[i] = a.scales[1][row * (D / 32) + c16 / 2];
-        }
-        return x;
-    };
+    for (int i = 0; i < RB; ++i) sees(min(r0 + 16 * i + r16, rows - 1), &lo[i], &hi[i]);
 
-    v4f acc[RB][CB];
-    float m[RB], l[RB];
-    uint32_t seen = 0;                                     // row blocks whose row (of this lane) saw a token
-#pragma unroll
-    for (int i = 0; i < RB; ++i) {
-        m[i] = -INFINITY, l[i] = 0.0f;
-#pragma unroll
-        for (int c = 0; c < CB; ++c) acc[i][c] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-
-    // V [32][D] bf16: 32 bytes (16 channels) of a token at slot c16 ^ its own, so
-    // that the transposing reads' 8 rows of 32 bytes meet 64 banks
-    uint8_t* const mine = lds[w];
-    const auto place_v = [&](int tok, int c16) {
-        const int s = D == 128 ? tok & 7 : (tok >> 1) & 3;
-        return tok * (2 * D) + ((c16 ^ s) << 5);
-    };
-    const auto read_v = [&](int cb) {                      // V^T: channels 16 cb + lane % 16, tokens 4 g .. and 16 + 4 g ..
-        const int tok = 4 * g + (r16 >> 2), in = (r16 & 3) * 8;
-        const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(mine + place_v(tok, cb) + in));
-        const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(mine + place_v(tok + 16, cb) + in));
-        typedef short v8s __attribute__((ext_vector_type(8)));
-        return __builtin_bit_cast(v8bf, v8s{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
-    };
-
-    const int c_first = part * per + w;
-    Two pg = pages_at(c_first);
-    Tok cur{};
-    if (c_first < c_end) cur = load(c_first, pg);
-    Two pg_next = pages_at(c_first + 4);
-    for (int c = c_first; c < c_end; c += 4) {
+    for (int c = c_first; c < c_end;) {
+        // (the next block's keys are loaded as soon as this one's are used, its values too: no registers for two blocks)
         const Two here = pg;
-        const Tok x = cur;
-        if (c + 4 < c_end) {
-            cur = load(c + 4, pg_next);
-            pg = pg_next;
-            pg_next = pages_at(c + 8);
-        }
+        const bool more = c + 4 < c_end;
+        pg = pg_next;
+        pg_next = pages_at(c + 8);
         const int t = token0(c);
         // ---- scores
         v4f s[RB][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float scale = scale_of(x.ks[h]);
+            const float scale = scale_in(x.ks[h], r16, D / 4 * g / 32);
 #pragma unroll
             for (int i = 0; i < RB; ++i) s[i][h] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -344,75 +386,66 @@ __global__ __launch_bounds__(256) void k_attn(AttnArgs a) {
                     for (int p = QP - 1; p >= 0; --p) s[i][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[i][p][j], s[i][h], 0, 0, 0);
             }
         }
+        if (more) load_keys(c + 4, pg);
         // ---- values into LDS
         const bool all = here.p[0] >= 0 && here.p[1] >= 0 && ((t >= lo1 && t + 32 <= hi0) || t + 32 <= pf);   // every row sees every token
-        bool odd = false;                                  // values that are not finite, where some row must not see them
+        // (a value that is not finite would reach rows that do not see it, times 0)
+        const bool odd = !all && __ballot(x.not_finite()) != 0;
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-        for (int i = 0; i < Tok::VP; ++i) {
-            const int tok = (64 / LPR) * i + lane / LPR, c16 = lane % LPR;
-            const float scale = scale_of(x.vs[i]);
-            uint4* to = (uint4*)(mine + place_v(tok, c16));
-            v8bf v0 = decode8<BITS>(x.v[i], scale), v1 = decode8<BITS>(x.v[i] + BITS / 4, scale);
-            if (!all) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    // (times 0: NaN for what is not finite)
-                    const float z0 = (float)v0[e] * 0.0f, z1 = (float)v1[e] * 0.0f;
-                    if (z0 != z0) odd = true, v0[e] = (__bf16)0.0f;
-                    if (z1 != z1) odd = true, v1[e] = (__bf16)0.0f;
-                }
-            }
-            to[0] = __builtin_bit_cast(uint4, v0);
-            to[1] = __builtin_bit_cast(uint4, v1);
-        }
+        if (!odd) place_values([](v8bf v) { return v; });
+        else place_values([](v8bf v) { return not_finite_of<false>(v); });
+        if (more) load_values(c + 4, pg);
         // ---- weights
         v8bf pw[RB][PP];
         uint32_t vis[RB];
+        const auto weigh = [&](auto masked) {
 #pragma unroll
-        for (int i = 0; i < RB; ++i) {
-            float e[8];
-            vis[i] = 0xff;
-            if (!all) {
-                vis[i] = 0;
+            for (int i = 0; i < RB; ++i) {
+                float e[8];
+                vis[i] = 0xff;
+                if constexpr (decltype(masked)::value) {
+                    vis[i] = 0;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int tok = t + 16 * (j >> 2) + 4 * g + (j & 3);
+                        const bool on = ((tok >= lo[i] && tok < hi[i]) || tok < pf) && here.p[j >> 2] >= 0;
+                        vis[i] |= on ? 1u << j : 0u;
+                    }
+                }
+                float top = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const int tok = t + 16 * (j >> 2) + 4 * g + (j & 3);
-                    const bool on = ((tok >= lo[i] && tok < hi[i]) || tok < pf) && here.p[j >> 2] >= 0;
-                    vis[i] |= on ? 1u << j : 0u;
+                    e[j] = s[i][j >> 2][j & 3];
+                    if (a.cap > 0.0f) e[j] = a.cap * LOG2E * tanh_of(e[j] * a.cap_in);
+                    if constexpr (decltype(masked)::value) e[j] = vis[i] >> j & 1 ? e[j] : -INFINITY;
+                    top = fmaxf(top, e[j]);
+                }
+                if (vis[i]) seen |= 1u << i;
+                top = max_rows(top) * a.scale;             // (1 with a cap)
+                if (__ballot(top > m[i])) {
+                    const float mn = fmaxf(m[i], top), f = mn == -INFINITY ? 1.0f : power(m[i] - mn);
+                    m[i] = mn;
+                    l[i] *= f;
+#pragma unroll
+                    for (int c16 = 0; c16 < CB; ++c16) acc[i][c16] *= f;
+                }
+                const float at = m[i] == -INFINITY ? 0.0f : m[i];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float p = power(__builtin_fmaf(e[j], a.scale, -at));
+                    const __bf16 h = (__bf16)p;
+                    pw[i][0][j] = h;
+                    if constexpr (PP == 2) {
+                        pw[i][1][j] = (__bf16)(p - (float)h);
+                        l[i] += p;
+                    } else {
+                        l[i] += (float)h;
+                    }
                 }
             }
-            float top = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float v = s[i][j >> 2][j & 3] * a.scale;
-                if (a.cap > 0.0f) v = a.cap * tanh_of(v * a.cap_inv) * LOG2E;
-                e[j] = vis[i] >> j & 1 ? v : -INFINITY;
-                top = fmaxf(top, e[j]);
-            }
-            if (vis[i]) seen |= 1u << i;
-            top = max_rows(top);
-            if (__ballot(top > m[i])) {
-                const float mn = fmaxf(m[i], top), f = mn == -INFINITY ? 1.0f : power(m[i] - mn);
-                m[i] = mn;
-                l[i] *= f;
-#pragma unroll
-                for (int c16 = 0; c16 < CB; ++c16) acc[i][c16] *= f;
-            }
-            const float at = m[i] == -INFINITY ? 0.0f : m[i];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float p = power(e[j] - at);
-                const __bf16 h = (__bf16)p;
-                pw[i][0][j] = h;
-                if constexpr (PP == 2) {
-                    pw[i][1][j] = (__bf16)(p - (float)h);
-                    l[i] += p;
-                } else {
-                    l[i] += (float)h;
-                }
-            }
-        }
+        };
+        if (all) weigh(std::false_type{});
+        else weigh(std::true_type{});
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         // ---- O^T += V^T P^T
 #pragma unroll
@@ -423,24 +456,11 @@ __global__ __launch_bounds__(256) void k_attn(AttnArgs a) {
 #pragma unroll
                 for (int p = PP - 1; p >= 0; --p) acc[i][cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pw[i][p], acc[i][cb], 0, 0, 0);
         }
-        if (!all && __ballot(odd)) {
+        if (odd) {
             // the rows that do see a value that is not finite: counted as ones times ones
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-            for (int i = 0; i < Tok::VP; ++i) {
-                const int tok = (64 / LPR) * i + lane / LPR, c16 = lane % LPR;
-                const float scale = scale_of(x.vs[i]);
-                uint4* to = (uint4*)(mine + place_v(tok, c16));
-                v8bf v0 = decode8<BITS>(x.v[i], scale), v1 = decode8<BITS>(x.v[i] + BITS / 4, scale);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float z0 = (float)v0[e] * 0.0f, z1 = (float)v1[e] * 0.0f;
-                    v0[e] = (__bf16)(z0 != z0 ? 1.0f : 0.0f);
-                    v1[e] = (__bf16)(z1 != z1 ? 1.0f : 0.0f);
-                }
-                to[0] = __builtin_bit_cast(uint4, v0);
-                to[1] = __builtin_bit_cast(uint4, v1);
-            }
+            load_values(c, here);
+            place_values([](v8bf v) { return not_finite_of<true>(v); });
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
@@ -452,10 +472,13 @@ __global__ __launch_bounds__(256) void k_attn(AttnArgs a) {
                     const v4f n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(read_v(cb), on, v4f{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (n[e] > 0.0f) acc[i][cb][e] = __builtin_nanf("");
+                        // (a count above 0: NaN, by its exponent and its fraction's first bit)
+                        acc[i][cb][e] = __uint_as_float(__float_as_uint(acc[i][cb][e]) | (__float_as_uint(n[e]) ? 0x7fc00000u : 0u));
                 }
             }
+            if (more) load_values(c + 4, pg);
         }
+        c += 4;
     }
 
     // ---- the four waves' sums, a block of rows at a time: thread (row, its D / 16 channels)
@@ -472,26 +495,13 @@ __global__ __launch_bounds__(256) void k_attn(AttnArgs a) {
     }
     constexpr int CT = D / 16, Q4 = CT / 4;                // channels of a thread, in pieces of 4
     const int row = tid >> 4, ch = (tid & 15) * CT;
-    const int unit = (head * ((int)gridDim.x / a.parts) + tile) * a.parts;   // the tile's first unit
-    const auto at_sum = [&](int p, int i) { return ((size_t)(unit + p) * RB + i) * 16 * D; };
-    const auto at_stat = [&](int p, int i) { return (((size_t)(unit + p) * RB + i) * 16 + row) * 4; };
-    const __amdgpu_buffer_rsrc_t sums = shared_floats(a.sums, SUM_FLOATS), stats = shared_floats(a.stats, STAT_FLOATS);
+    const size_t unit = ((size_t)(head * tiles + tile) * a.parts + part) * RB;
     const auto finish = [&](int i, const v4f* o, float sum, bool any) {
-        const long long r = r0 + 16 * i + row;
-        if (r >= rows) return;
-        T* y = (T*)a.y + (f0 + r / a.G) * a.ldy + ((long long)head * a.G + r % a.G) * D + ch;
+        const uint32_t r = r0 + 16 * i + row, n = r / (uint32_t)a.G;
+        if ((int)r >= rows) return;
+        T* y = (T*)a.y + (long long)(f0 + n) * a.ldy + (head * a.G + (int)(r - n * a.G)) * D + ch;
 #pragma unroll
-        for (int p = 0; p < Q4; ++p) {
-            float v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = any ? o[p][e] / sum : 0.0f;
-            if constexpr (F32) {
-                *(v4f*)(y + 4 * p) = v4f{v[0], v[1], v[2], v[3]};
-            } else {
-                const v2b x{(__bf16)v[0], (__bf16)v[1]}, z{(__bf16)v[2], (__bf16)v[3]};
-                *(v2w*)(y + 4 * p) = v2w{__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, z)};
-            }
-        }
+        for (int p = 0; p < Q4; ++p) store4(y + 4 * p, o[p], sum, any);
     };
     // (16-byte piece c of a row lies at c ^ row, so the lanes' stores and loads meet all banks)
 #pragma unroll
@@ -519,47 +529,75 @@ __global__ __launch_bounds__(256) void k_attn(AttnArgs a) {
         if (used == 1) {
             finish(i, out, sum, any > 0.0f);
         } else {
+            if (r0 + 16 * i + row >= rows) continue;
 #pragma unroll
-            for (int j = 0; j < Q4; ++j) hand_over(sums, at_sum(part, i) + row * D + ch + 4 * j, out[j]);
-            if ((tid & 15) == 0) hand_over(stats, at_stat(part, i), v4f{top, sum, any, 0.0f});
+            for (int j = 0; j < Q4; ++j) *(v4f*)(a.sums + ((unit + i) * 16 + row) * D + ch + 4 * j) = out[j];
+            if ((tid & 15) == 0) *(v4f*)(a.stats + ((unit + i) * 16 + row) * 4) = v4f{top, sum, any, 0.0f};
         }
     }
-    if (used == 1) return;
+}
 
-    // ---- the parts' sums, joined in order by the workgroup that ends last
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // (every wave's sums have arrived before the workgroup says so)
-    __syncthreads();
-    int* const count = a.arrivals + unit / a.parts;
-    if (tid == 0) arrived = __hip_atomic_fetch_add(count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    if (arrived != used - 1) return;
-    if (tid == 0) __hip_atomic_store(count, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);   // (for the next launch)
+// The sums of a tile's parts: a wave to a row, 16 bytes of a part to a lane, so
+// 256 / D parts to a load, and U loads on their way at once.
+template <class T, int D, int RB>
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
+    constexpr int LP = D / 4, PL = 64 / LP, U = 8;         // lanes to a part, parts to a load
+    const int lane = threadIdx.x & 63, row = (int)(blockIdx.x % (4 * RB)) * 4 + (threadIdx.x >> 6);
+    const int tiles = (int)gridDim.x / (4 * RB), tile = (int)blockIdx.x / (4 * RB), head = blockIdx.y;
+    const TileInfo info = a.tiles[head * tiles + tile];
+    if (info.used < 2 || row >= info.rows) return;
+    const size_t unit = (size_t)(head * tiles + tile) * a.parts * RB + (row >> 4), step = RB;
+    const auto at = [&](int p) { return (unit + p * step) * 16 + (row & 15); };
+    constexpr int SP = MAX_PARTS / 64;
+    v4f st[SP];
 #pragma unroll
-    for (int i = 0; i < RB; ++i) {
-        float top = -INFINITY, sum = 0.0f, any = 0.0f;
-        for (int p = 0; p < used; ++p) top = fmaxf(top, take_over(stats, at_stat(p, i))[0]);
-        v4f out[Q4];
+    for (int k = 0; k < SP; ++k) st[k] = *(const v4f*)(a.stats + at(min(64 * k + lane, info.used - 1)) * 4);
+    float top = -INFINITY, sum = 0.0f, any = 0.0f, f[SP];
 #pragma unroll
-        for (int j = 0; j < Q4; ++j) out[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-        for (int p = 0; p < used; ++p) {
-            const v4f s = take_over(stats, at_stat(p, i));
-            const float f = s[0] == -INFINITY ? 1.0f : power(s[0] - top);
-            sum += f * s[1];
-            any = fmaxf(any, s[2]);
+    for (int k = 0; k < SP; ++k) top = fmaxf(top, st[k][0]);
 #pragma unroll
-            for (int j = 0; j < Q4; ++j) out[j] += f * take_over(sums, at_sum(p, i) + row * D + ch + 4 * j);
-        }
-        finish(i, out, sum, any > 0.0f);
+    for (int s = 1; s < 64; s *= 2) top = fmaxf(top, __shfl_xor(top, s, 64));
+#pragma unroll
+    for (int k = 0; k < SP; ++k) {
+        f[k] = 64 * k + lane >= info.used ? 0.0f : st[k][0] == -INFINITY ? 1.0f : power(st[k][0] - top);
+        sum += 64 * k + lane < info.used ? f[k] * st[k][1] : 0.0f;
+        any = fmaxf(any, st[k][2]);
     }
+#pragma unroll
+    for (int s = 1; s < 64; s *= 2) sum += __shfl_xor(sum, s, 64), any = fmaxf(any, __shfl_xor(any, s, 64));
+    v4f out{0.0f, 0.0f, 0.0f, 0.0f};
+    const int sub = lane / LP, ch = 4 * (lane % LP);
+    for (int p0 = 0; p0 < info.used; p0 += U * PL) {
+        v4f from[U];
+        float w[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) from[u] = *(const v4f*)(a.sums + at(min(p0 + u * PL + sub, info.used - 1)) * D + ch);
+        const int k = p0 >> 6;                             // (U PL parts lie in one 64)
+        const float mine = k == 0 ? f[0] : k == 1 ? f[1] : k == 2 ? f[2] : f[3];
+#pragma unroll
+        for (int u = 0; u < U; ++u) w[u] = __shfl(mine, (p0 + u * PL + sub) & 63, 64);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) out[e] = p0 + u * PL + sub < info.used ? out[e] + w[u] * from[u][e] : out[e];
+    }
+#pragma unroll
+    for (int s = LP; s < 64; s *= 2)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[e] += __shfl_xor(out[e], s, 64);
+    if (lane >= LP) return;
+    const uint32_t r = info.r0 + row, n = r / (uint32_t)a.G;
+    store4((T*)a.y + (long long)(info.f0 + n) * a.ldy + (head * a.G + (int)(r - n * a.G)) * D + ch, out, sum, any > 0.0f);
 }
 
 template <class T, int BITS, int D, int RB>
 hipError_t launch_attn(AttnArgs a, int kv_heads, hipStream_t st) {
     const long long tiles = ((long long)a.N * a.G) / (16 * RB) + a.pages.seqs;
     const long long blocks = (((long long)a.pages.ld << a.pages.shift) + 31) / 32;
-    a.parts = (int)std::max(1ll, std::min({(blocks + 3) / 4, MAX_UNITS / (tiles * kv_heads), 256ll}));
-    return launch(k_attn<T, BITS, D, RB>, dim3((unsigned)(tiles * a.parts), kv_heads), 256u, st, a);
+    a.parts = (int)std::max(1ll, std::min({(blocks + 3) / 4, MAX_UNITS / (tiles * kv_heads), (long long)MAX_PARTS}));
+    const hipError_t e = launch(k_attn<T, BITS, D, RB>, dim3((unsigned)(tiles * a.parts), kv_heads), 256u, st, a);
+    if (e != hipSuccess || a.parts == 1) return e;
+    return launch(k_attn_join<T, D, RB>, dim3((unsigned)(tiles * 4 * RB), kv_heads), 256u, st, a);
 }
 
 template <class T, int BITS, int D>
@@ -575,7 +613,6 @@ void free_attn(dq_attn* a) {
     if (!a) return;
     DeviceGuard dg(a->device);
     (void)hipFree(a->sums);
-    (void)hipFree(a->arrivals);
     delete a;
 }
 
@@ -599,16 +636,10 @@ dq_status dq_attn_create(int32_t device, dq_attn** out) {
     std::unique_ptr<dq_attn, void (*)(dq_attn*)> guard(a, free_attn);
     a->device = device;
     hipError_t e;
-    if ((e = hipMalloc((void**)&a->sums, (SUM_FLOATS + STAT_FLOATS) * 4)) != hipSuccess) {
+    if ((e = hipMalloc((void**)&a->sums, (SUM_FLOATS + STAT_FLOATS) * 4 + MAX_UNITS * sizeof(TileInfo))) != hipSuccess) {
         a->sums = nullptr;
         return hip_fail(e, "hipMalloc workspace");
     }
-    if ((e = hipMalloc((void**)&a->arrivals, MAX_UNITS * 4)) != hipSuccess) {
-        a->arrivals = nullptr;
-        return hip_fail(e, "hipMalloc workspace");
-    }
-    if ((e = hipMemset(a->arrivals, 0, MAX_UNITS * 4)) != hipSuccess || (e = hipDeviceSynchronize()) != hipSuccess)
-        return hip_fail(e, "workspace init");
     *out = guard.release();
     return DQ_OK;
 }
@@ -669,10 +700,10 @@ dq_status dq_attn_rows(const dq_kv* kv, const dq_seqs* seqs, int64_t N, const vo
     k.N = (int)N, k.G = q_heads / kv->heads;
     k.block = ops->block, k.window = ops->window;
     k.cap = (float)ops->cap;
-    k.cap_inv = ops->cap != 0.0 ? (float)(1.0 / ops->cap) : 0.0f;
-    k.scale = (float)(ops->cap != 0.0 ? ops->scale : ops->scale * 1.4426950408889634);
+    k.cap_in = ops->cap != 0.0 ? (float)(ops->scale / ops->cap) : 0.0f;
+    k.scale = ops->cap != 0.0 ? 1.0f : (float)(ops->scale * 1.4426950408889634);
     k.sums = a->sums, k.stats = a->sums + SUM_FLOATS;
-    k.arrivals = a->arrivals;
+    k.tiles = (TileInfo*)(k.stats + STAT_FLOATS);
     const auto go = [&](auto bits, auto dim) {
         constexpr int B = decltype(bits)::value, W = decltype(dim)::value;
         return dt == DQ_BF16 ? launch_attn<uint16_t, B, W>(k, kv->heads, (hipStream_t)stream)

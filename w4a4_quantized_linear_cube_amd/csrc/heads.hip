@@ -416,13 +416,13 @@ int pow2_at_least(int n, int least) {
 }
 
 // Threads to a row of nch chunks (a power of two from `least` to `most`) and chunks
-// to a thread (up to 5; one, where a row takes less than a wave) that leave the
-// fewest lanes idle; of equal ones the fewest threads.
-void share_row(int nch, int least, int most, int* tpr, int* ch) {
+// to a thread (up to 5; one, where a row has fewer than `wave` threads) that leave
+// the fewest lanes idle; of equal ones the fewest threads.
+void share_row(int nch, int least, int most, int wave, int* tpr, int* ch) {
     int best = 1 << 30;
     for (int t = least; t <= most; t *= 2) {
         const int c = (nch + t - 1) / t;
-        if (c > 5 || (c > 1 && t < 64)) continue;
+        if (c > 5 || (c > 1 && t < wave)) continue;
         if (c * t < best) best = c * t, *tpr = t, *ch = c;
     }
 }
@@ -439,7 +439,7 @@ hipError_t launch_heads(HeadsArgs a, int parts, hipStream_t st) {
         a.tpr = std::min(pow2_at_least(nch, a.lph), row_norm ? 1024 : 256);
         ch = row_norm ? (nch + a.tpr - 1) / a.tpr : 1;
     } else {
-        share_row(nch, a.lph, 1024, &a.tpr, &ch);
+        share_row(nch, a.lph, 1024, 64, &a.tpr, &ch);
     }
     a.nt = !few;
     int segs = 0;
@@ -467,7 +467,7 @@ hipError_t launch_heads(HeadsArgs a, int parts, hipStream_t st) {
 template <class T, int BITS>
 hipError_t launch_read(ReadArgs a, int parts, hipStream_t st) {
     int ch = 1;
-    share_row(a.nch, a.lph, 512, &a.tpr, &ch);
+    share_row(a.nch, a.lph, 512, 64, &a.tpr, &ch);
     const int threads = std::max(256, a.tpr), rows = threads / a.tpr;
     const long long most = (1ll << 31) / threads;
     hipError_t e = hipSuccess;
