@@ -38,13 +38,18 @@ struct dq_attn {
 namespace dq {
 namespace {
 
-// Units (tiles x key heads x parts) that may meet in the workspace, and blocks of 16 rows to one.
-constexpr int MAX_UNITS = 2048, MAX_RB = 4, MAX_PARTS = 256;
-constexpr size_t SUM_FLOATS = size_t(MAX_UNITS) * MAX_RB * 16 * 128, STAT_FLOATS = size_t(MAX_UNITS) * MAX_RB * 16 * 4;
-// A tile that is in parts: how many (0 or 1: nothing to join), its rows, and its sequence's first row and rows before it.
+// Parts of tiles (a tile: up to 16 RB rows that share a key head; a part: some of
+// the tokens they see) that may meet in the workspace, and blocks of 16 rows to one.
+constexpr int MAX_SLOTS = 2048, MAX_RB = 4;
+constexpr size_t SUM_FLOATS = size_t(MAX_SLOTS) * MAX_RB * 16 * 128, STAT_FLOATS = size_t(MAX_SLOTS) * MAX_RB * 16 * 4;
+// A tile in parts: how many (0 or 1: nothing to join), its rows, its sequence's
+// first row and the rows before it, and the first part's slot.
 struct TileInfo {
-    int used, rows, f0, r0;
+    int used, rows, f0, r0, slot, pad[3];
 };
+// In blocks of 32 tokens: what a tile costs beside them (its start and end take
+// a workgroup as long), and the least that a workgroup takes.
+constexpr int TILE_COST = 8, LEAST_SHARE = 8;
 constexpr float LOG2E = 1.44269504088896340736f;
 
 struct AttnArgs {
@@ -56,7 +61,8 @@ struct AttnArgs {
     Pages pages;
     const int* prefix;
     int N, G;               // query rows; query heads to a key head
-    int parts;              // workgroups that may share a tile's tokens
+    int shares;             // workgroups that share a key head's tokens (0: one to a tile)
+    int most;               // tiles of a key head at most
     long long block, window;
     float scale;            // of q k, for powers of 2; 1 with a cap
     float cap, cap_in;      // the cap (0: none), and scale / cap
@@ -115,16 +121,23 @@ __device__ __forceinline__ v8bf decode8(const uint32_t* w, float scale) {
     return v8bf{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
 }
 
+// An address that is the same in the whole wave, in scalar registers.
+typedef const __attribute__((address_space(1))) uint8_t* Bytes;
+__device__ __forceinline__ Bytes scalar(const uint8_t* p) {
+    const uint64_t v = (uint64_t)(uintptr_t)p;
+    return (Bytes)(uintptr_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
+                              (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
+}
 template <int N>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
+__device__ __forceinline__ void load_words(Bytes p, uint32_t* w) {
     if constexpr (N >= 4) {
 #pragma unroll
         for (int i = 0; i < N; i += 4) {
-            const v4w v = *(const v4w*)(p + 4 * i);
+            const v4w v = *(const __attribute__((address_space(1))) v4w*)(p + 4 * i);
             w[i] = v[0], w[i + 1] = v[1], w[i + 2] = v[2], w[i + 3] = v[3];
         }
     } else {
-        const v2w v = *(const v2w*)p;
+        const v2w v = *(const __attribute__((address_space(1))) v2w*)p;
         w[0] = v[0], w[1] = v[1];
     }
 }
@@ -178,6 +191,82 @@ __device__ __forceinline__ void store4(uint16_t* y, v4f o, float sum, bool any) 
     *(v2w*)y = v2w{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
 }
 
+// Tokens that a sequence's row of the page table reaches.
+__device__ __forceinline__ long long reach(const Pages& p) { return min((long long)p.ld << p.shift, (1ll << 31) - 64); }
+
+// The inclusive sum over the wave's lanes, in order.
+template <class V>
+__device__ __forceinline__ V scan(V v) {
+    const auto moved = [](V x, auto ctrl, auto rows) {
+        return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value, decltype(rows)::value, 0xF, true));
+    };
+    using std::integral_constant;
+    const integral_constant<int, 0xF> all{};
+    v += moved(v, integral_constant<int, 0x111>{}, all);   // 1, 2, 4 and 8 lanes down in each row of 16
+    v += moved(v, integral_constant<int, 0x112>{}, all);
+    v += moved(v, integral_constant<int, 0x114>{}, all);
+    v += moved(v, integral_constant<int, 0x118>{}, all);
+    v += moved(v, integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});   // a row's last lane to the next row, in every other row
+    v += moved(v, integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});   // the first half's last lane to the second half
+    return v;
+}
+
+// One workgroup's work for one tile: blocks c0 .. c1 - 1 of the tokens that tile
+// `tile` of sequence b sees.
+struct Work {
+    int b, f0, f1, length, tile, c0, c1;
+    int parts, slot, number;  // of the tile: its parts; this one's slot; its number
+    bool head;                // its first part
+};
+// Up to 64 sequences: a lane holds one.  Their tiles stand in a row, each as long
+// as the blocks of tokens it sees at most and TILE_COST, and a workgroup takes an equal stretch of it: a
+// part of a long tile, or several short ones, whatever the lengths (64 sequences
+// of up to 8192 tokens: XX us, as three parts each 148).
+struct Batch64 {
+    int f0, f1, length, tiles;
+    int cost, upto, tiles_upto, pad;   // of one tile; of this sequence's and earlier tiles together
+};
+template <int TR>
+__device__ __forceinline__ Batch64 batch_of(const AttnArgs& a) {
+    const Pages& p = a.pages;
+    const int lane = threadIdx.x & 63, i = min(lane, p.seqs - 1);
+    const int first = p.first[i], next = p.first[i + 1], len = p.length[i], keep = a.prefix ? a.prefix[i] : 0;
+    Batch64 x;
+    x.f0 = min(max(first, 0), a.N), x.f1 = min(max(next, x.f0), a.N), x.length = max(len, 0);
+    x.tiles = lane < p.seqs ? ((x.f1 - x.f0) * a.G + TR - 1) / TR : 0;
+    const long long L = min((long long)x.length, reach(p));
+    long long tokens = L;                                  // that a tile's rows see, or a few more
+    if (a.block && a.window) tokens = min(L, min(L, a.window + a.block + TR) + min((long long)max(keep, 0), L) + 64);
+    x.cost = (int)((tokens + 31) / 32) + 1 + TILE_COST;
+    x.tiles_upto = scan(x.tiles);
+    x.upto = a.shares ? scan(x.tiles * x.cost) : 0;
+    x.pad = 0;
+    return x;
+}
+__device__ __forceinline__ Batch64 of_lane(const Batch64& x, int b) {
+    const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, b); };
+    return {of(x.f0), of(x.f1), of(x.length), of(x.tiles), of(x.cost), of(x.upto), of(x.tiles_upto), 0};
+}
+// One tile to a workgroup: the u-th; tile -1 past the last.  (Of more than 64
+// sequences, b's are numbered from floor(first[b] G / TR) + b on, which leaves
+// each as many as it needs.)
+template <int TR>
+__device__ __forceinline__ Work whole_tile(const AttnArgs& a, int u) {
+    const Pages& p = a.pages;
+    const auto one = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+    if (p.seqs <= 64) {
+        const Batch64 x = batch_of<TR>(a);
+        const int b = (int)__popcll(__ballot(x.tiles_upto <= u));
+        if (b > 63) return {0, 0, 0, 0, -1, 0, 0, 1, 0, 0, true};
+        const Batch64 y = of_lane(x, b);
+        return {b, y.f0, y.f1, y.length, u - y.tiles_upto + y.tiles, 0, INT32_MAX, 1, 0, 0, true};
+    }
+    const auto base_of = [&](int first, int i) { return min(max(first, 0), a.N) * a.G / TR + i; };
+    const Sequence q = sequence_of(p, starts_of(p), u, [&](int f, int i) { return (long long)base_of(f, i); });
+    const int f0 = min(max(q.f0, 0), a.N), f1 = min(max(q.f1, f0), a.N);
+    return {one(q.b), one(f0), one(f1), one(max(q.length, 0)), one(u - base_of(q.f0, q.b)), 0, INT32_MAX, 1, 0, 0, true};
+}
+
 // Waves to a SIMD that the registers are kept for.
 constexpr int waves_of(bool f32, int D, int RB) { return D == 64 ? (RB == 1 ? (f32 ? 3 : 4) : RB == 2 ? 2 : 1) : RB == 1 ? (f32 ? 2 : 3) : RB == 2 && !f32 ? 2 : 1; }
 
@@ -190,31 +279,51 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
     using Tok = Tokens<BITS, D>;
     __shared__ __attribute__((aligned(16))) uint8_t lds[4][64 * D];   // a wave's V [32][D] bf16, then its sums [16][D] fp32
     __shared__ float stat[4][3][TR];
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r16 = lane & 15, g = lane >> 4;
-    const int part = (int)blockIdx.x % a.parts, tile = (int)blockIdx.x / a.parts, head = blockIdx.y;
-
+    __shared__ Batch64 batch[64];
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int u = blockIdx.x, head = blockIdx.y;
     // (what is the same in the whole wave is kept in scalar registers)
     const auto one = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
     // (the arguments' cache lines, all at once)
     asm volatile("" ::"s"(a.q), "s"(a.scales[1]), "s"(a.prefix), "s"(a.tiles));
-
-    // ---- the tile's sequence and rows.  Sequence b's tiles are numbered from
-    // floor(first[b] G / TR) + b on, which leaves each as many as it needs.
-    const auto base_of = [&](int first, int i) { return min(max(first, 0), a.N) * a.G / TR + i; };
-    const Starts starts = starts_of(a.pages);
-    const Sequence sq = sequence_of(a.pages, starts, tile, [&](int f, int i) { return (long long)base_of(f, i); });
-    const int b = one(sq.b), f0 = one(min(max(sq.f0, 0), a.N)), f1 = one(min(max(sq.f1, f0), a.N)), length = one(max(sq.length, 0));
-    const int L = (int)min((long long)length, min((long long)a.pages.ld << a.pages.shift, (1ll << 31) - 64));   // tokens that may have a page
-    const int rows = (f1 - f0) * a.G, r0 = (tile - base_of(sq.f0, b)) * TR;
-    const int tiles = (int)gridDim.x / a.parts;
-    TileInfo* const info = a.tiles + head * tiles + tile;
-    const bool tells = a.parts > 1 && part == 0 && tid == 0;
-    if (r0 < 0 || r0 >= rows) {
-        if (tells) *info = TileInfo{0, 0, 0, 0};
-        return;
+    Work work;
+    int pos = 0, end = 0, share = 0;                       // of the row of tiles: what is left to this workgroup
+    if (a.shares) {
+        const Batch64 x = batch_of<TR>(a);
+        batch[tid & 63] = x;                                   // (every wave the same)
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        const int total = __builtin_amdgcn_readlane(x.upto, 63), tiles = __builtin_amdgcn_readlane(x.tiles_upto, 63);
+        share = one(max((int)(((uint32_t)total + a.shares - 1) / (uint32_t)a.shares), LEAST_SHARE));
+        pos = (int)min((long long)u * share, (long long)total), end = min(total, pos + share);
+        if (u >= tiles && u < a.most && tid == 0) a.tiles[(size_t)head * a.most + u].used = 0;   // (no tile of that number)
+    } else {
+        work = whole_tile<TR>(a, u);
     }
+    for (;;) {
+    int lane = tid & 63;
+    asm volatile("" : "+v"(lane));                         // (what goes by the lane is formed for each tile, not kept over all of them)
+    const int r16 = lane & 15, g = lane >> 4;
+    if (a.shares) {
+        if (pos >= end) return;
+        const int b = (int)__popcll(__ballot(batch[lane].upto <= pos));
+        const Batch64 x = batch[b];
+        const int tiles = one(x.tiles), cost = one(x.cost), begin = one(x.upto) - tiles * cost, tile = (pos - begin) / cost;
+        const int first = begin + tile * cost, from = pos - first, to = min(cost, from + end - pos), number = one(x.tiles_upto) - tiles + tile;
+        pos += to - from;
+        work = {b, one(x.f0), one(x.f1), one(x.length), tile, max(from - TILE_COST, 0), max(to - TILE_COST, 0), 0, u + number, number, false};
+        if (work.c0 >= work.c1) continue;                  // (the part that stands for the tile's cost)
+        const int head_of = (first + TILE_COST) / share;   // the workgroup of its first block
+        work.parts = (first + cost - 1) / share - head_of + 1;
+        work.head = u == head_of;
+    }
+    const int b = one(work.b), f0 = one(work.f0), f1 = one(work.f1), length = one(work.length);
+    const int L = (int)min((long long)length, reach(a.pages));
+    const int rows = (f1 - f0) * a.G, r0 = one(work.tile) * TR;
+    if (r0 < 0 || r0 >= rows) return;                      // (no such tile; of shares there is none)
     const int pf = a.block && a.prefix ? min(max(((Scalars)(uintptr_t)a.prefix)[b], 0), L) : 0;
+    const int used = one(work.parts);
+    if (a.shares && work.head && tid == 0)
+        a.tiles[(size_t)head * a.most + work.number] = TileInfo{used, min(rows - r0, TR), f0, r0, work.slot, {0, 0, 0}};
 
     // ---- what each row sees: [lo, hi) and [0, pf)
     const int t0 = length - (f1 - f0);                     // the first row's place
@@ -235,58 +344,60 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
     int na = (pf + 31) >> 5, b0 = lo0 >> 5, nb = hi1 > lo0 ? ((hi1 + 31) >> 5) - b0 : 0;
     if (na >= b0) nb = max(b0 + nb, na), b0 = 0, na = 0;
     const int blocks = na + nb;
-    const int per = ((blocks + a.parts - 1) / a.parts + 3) & ~3;   // (whole rounds of the four waves)
-    const int used = blocks ? (blocks + per - 1) / per : 1;
-    if (tells) *info = TileInfo{used, min(rows - r0, TR), f0, r0};
-    if (part >= used) return;
-    const int c_end = min(blocks, (part + 1) * per);
+    const int c_end = min(blocks, one(work.c1));
 
     // ---- the cache
     const auto token0 = [&](int c) { return (c < na ? c : c - na + b0) << 5; };
+    // Pages of a block's two halves, as the table has them (places past its end:
+    // its last entry; a block past the part's last: the last's), and those that
+    // are the cache's, or -1.  Scalar loads: a wave's wait for them does not wait for the cache's.
     struct Two {
         int p[2];
     };
-    const auto pages_at = [&](int c) {                     // pages of a block's two halves
-        // (both loads at once: places past the table's end read its last entry, a block past the last the last block's)
-        const int t = token0(max(min(c, blocks - 1), 0)), i0 = t >> a.pages.shift, i1 = (t + 16) >> a.pages.shift;
-        // (scalar loads: a wave's wait for them does not wait for the cache's)
-        const Scalars table = (Scalars)(uintptr_t)(a.pages.table + (size_t)b * a.pages.ld);
-        const int p0 = table[min(i0, a.pages.ld - 1)], p1 = table[min(i1, a.pages.ld - 1)];
-        Two r;
-        r.p[0] = t < L && (uint32_t)p0 < (uint32_t)a.pages.pages ? p0 : -1;
-        r.p[1] = t + 16 < L && (uint32_t)p1 < (uint32_t)a.pages.pages ? p1 : -1;
-        return r;
+    const Scalars table = (Scalars)(uintptr_t)(a.pages.table + (size_t)b * a.pages.ld);
+    const auto near = [&](int c) { return max(min(c, c_end - 1), 0); };
+    const auto entries = [&](int c) {
+        const int t = token0(near(c));
+        return Two{{table[min(t >> a.pages.shift, a.pages.ld - 1)], table[min((t + 16) >> a.pages.shift, a.pages.ld - 1)]}};
+    };
+    const auto pages_at = [&](int c, Two e) {
+        const int t = token0(near(c));
+        return Two{{t < L && (uint32_t)e.p[0] < (uint32_t)a.pages.pages ? e.p[0] : -1,
+                    t + 16 < L && (uint32_t)e.p[1] < (uint32_t)a.pages.pages ? e.p[1] : -1}};
     };
     const int mask = (1 << a.pages.shift) - 1;
-    // the aligned word that holds a row's scale codes (with D 64 two rows'), and the place of one in it
-    const auto scale_word = [&](const uint8_t* p, long long row) { return *(const uint32_t*)(p + (row * (D / 32) & ~3ll)); };
+    // A load's address is a block's, which is scalar, and an offset that is the
+    // lane's.  Scale codes come as the aligned word that holds a row's (with D 64 two rows').
+    constexpr int RC = D * BITS / 8, RS = D / 32;          // bytes of a row's codes and scale codes
     const auto scale_in = [](uint32_t word, int row, int group) {
         return scale_of(word >> (8 * (D == 128 ? group : 2 * (row & 1) + group)) & 0xff);
     };
+    const uint32_t key_at = r16 * RC + g * (Tok::KW * 4), key_scale_at = r16 * RS & ~3;
+    const uint32_t value_at = lane / LPR * RC + lane % LPR * (Tok::VW * 4), value_scale_at = lane / LPR * RS & ~3;
     Tok x;
     const auto row_of = [&](int c, Two pg, int h) {        // the cache's row of a half's first token (in page 0 where there is none)
-        return (((long long)max(pg.p[h], 0) * a.pages.heads + head) << a.pages.shift) + ((token0(max(min(c, blocks - 1), 0)) + 16 * h) & mask);
+        return (((long long)max(pg.p[h], 0) * a.pages.heads + head) << a.pages.shift) + ((token0(near(c)) + 16 * h) & mask);
     };
     const auto load_keys = [&](int c, Two pg) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const long long row = row_of(c, pg, h) + r16;
-            load_words<Tok::KW>(a.codes[0] + row * (D * BITS / 8) + g * (Tok::KW * 4), x.k[h]);
-            x.ks[h] = scale_word(a.scales[0], row);
+            const long long row = row_of(c, pg, h);
+            load_words<Tok::KW>(scalar(a.codes[0] + row * RC) + key_at, x.k[h]);
+            x.ks[h] = *(const __attribute__((address_space(1))) uint32_t*)(scalar(a.scales[0] + row * RS) + key_scale_at);
         }
     };
     const auto load_values = [&](int c, Two pg) {
 #pragma unroll
         for (int i = 0; i < Tok::VP; ++i) {                // piece i: token (64 / LPR) i + lane / LPR
-            const int tok = (64 / LPR) * i + lane / LPR, c16 = lane % LPR;
-            const long long row = row_of(c, pg, (64 / LPR) * i < 16 ? 0 : 1) + (tok & 15);
-            load_words<Tok::VW>(a.codes[1] + row * (D * BITS / 8) + c16 * (Tok::VW * 4), x.v[i]);
-            x.vs[i] = scale_word(a.scales[1], row);
+            const long long row = row_of(c, pg, (64 / LPR) * i < 16 ? 0 : 1) + (64 / LPR) * i % 16;
+            load_words<Tok::VW>(scalar(a.codes[1] + row * RC) + value_at, x.v[i]);
+            x.vs[i] = *(const __attribute__((address_space(1))) uint32_t*)(scalar(a.scales[1] + row * RS) + value_scale_at);
         }
     };
 
     v4f acc[RB][CB];
     float m[RB], l[RB];
+    uint32_t nan[RB] = {};                                 // the sums that are NaN by what the masked blocks hold
     uint32_t seen = 0;                                     // row blocks whose row (of this lane) saw a token
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
@@ -321,8 +432,8 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
         return __builtin_bit_cast(v8bf, v8s{p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]});
     };
 
-    const int c_first = part * per + w;
-    Two pg = pages_at(c_first), pg_next = pages_at(c_first + 4);
+    const int c_first = one(work.c0) + w;
+    Two pg = pages_at(c_first, entries(c_first)), later = entries(c_first + 4);
     load_keys(c_first, pg);
     load_values(c_first, pg);
 
@@ -364,11 +475,13 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
     for (int i = 0; i < RB; ++i) sees(min(r0 + 16 * i + r16, rows - 1), &lo[i], &hi[i]);
 
     for (int c = c_first; c < c_end;) {
-        // (the next block's keys are loaded as soon as this one's are used, its values too: no registers for two blocks)
+        // (The next block's keys are loaded as soon as this one's are used, its
+        // values too: no registers for two blocks.  Past the last block the last
+        // is loaded again: with a branch there the waits, which count loads,
+        // would have to assume that there were none.)
         const Two here = pg;
-        const bool more = c + 4 < c_end;
-        pg = pg_next;
-        pg_next = pages_at(c + 8);
+        pg = pages_at(c + 4, later);
+        later = entries(c + 8);
         const int t = token0(c);
         // ---- scores
         v4f s[RB][2];
@@ -386,7 +499,7 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
                     for (int p = QP - 1; p >= 0; --p) s[i][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[i][p][j], s[i][h], 0, 0, 0);
             }
         }
-        if (more) load_keys(c + 4, pg);
+        load_keys(c + 4, pg);
         // ---- values into LDS
         const bool all = here.p[0] >= 0 && here.p[1] >= 0 && ((t >= lo1 && t + 32 <= hi0) || t + 32 <= pf);   // every row sees every token
         // (a value that is not finite would reach rows that do not see it, times 0)
@@ -394,10 +507,11 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         if (!odd) place_values([](v8bf v) { return v; });
         else place_values([](v8bf v) { return not_finite_of<false>(v); });
-        if (more) load_values(c + 4, pg);
+        load_values(c + 4, pg);
         // ---- weights
         v8bf pw[RB][PP];
         uint32_t vis[RB];
+        float grown[RB];                                   // what the sums so far are worth by the new maximum
         const auto weigh = [&](auto masked) {
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
@@ -414,21 +528,22 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
                 }
                 float top = -INFINITY;
 #pragma unroll
+                for (int j = 0; j < 8; ++j) e[j] = s[i][j >> 2][j & 3];
+                if (a.cap > 0.0f) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) e[j] = a.cap * LOG2E * tanh_of(e[j] * a.cap_in);
+                }
+#pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    e[j] = s[i][j >> 2][j & 3];
-                    if (a.cap > 0.0f) e[j] = a.cap * LOG2E * tanh_of(e[j] * a.cap_in);
                     if constexpr (decltype(masked)::value) e[j] = vis[i] >> j & 1 ? e[j] : -INFINITY;
                     top = fmaxf(top, e[j]);
                 }
                 if (vis[i]) seen |= 1u << i;
                 top = max_rows(top) * a.scale;             // (1 with a cap)
-                if (__ballot(top > m[i])) {
-                    const float mn = fmaxf(m[i], top), f = mn == -INFINITY ? 1.0f : power(m[i] - mn);
-                    m[i] = mn;
-                    l[i] *= f;
-#pragma unroll
-                    for (int c16 = 0; c16 < CB; ++c16) acc[i][c16] *= f;
-                }
+                const float mn = fmaxf(m[i], top);
+                grown[i] = mn == m[i] ? 1.0f : power(m[i] - mn);   // (also where both are infinite, whose sums are NaN by the weights)
+                m[i] = mn;
+                l[i] *= grown[i];
                 const float at = m[i] == -INFINITY ? 0.0f : m[i];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -446,6 +561,12 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
         };
         if (all) weigh(std::false_type{});
         else weigh(std::true_type{});
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+            if (__ballot(grown[i] != 1.0f)) {
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb) acc[i][cb] *= grown[i];
+            }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         // ---- O^T += V^T P^T
 #pragma unroll
@@ -471,12 +592,10 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
                 for (int cb = 0; cb < CB; ++cb) {
                     const v4f n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(read_v(cb), on, v4f{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        // (a count above 0: NaN, by its exponent and its fraction's first bit)
-                        acc[i][cb][e] = __uint_as_float(__float_as_uint(acc[i][cb][e]) | (__float_as_uint(n[e]) ? 0x7fc00000u : 0u));
+                    for (int e = 0; e < 4; ++e) nan[i] |= __float_as_uint(n[e]) ? 1u << (4 * cb + e) : 0u;
                 }
             }
-            if (more) load_values(c + 4, pg);
+            load_values(c + 4, pg);
         }
         c += 4;
     }
@@ -495,7 +614,7 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
     }
     constexpr int CT = D / 16, Q4 = CT / 4;                // channels of a thread, in pieces of 4
     const int row = tid >> 4, ch = (tid & 15) * CT;
-    const size_t unit = ((size_t)(head * tiles + tile) * a.parts + part) * RB;
+    const size_t unit = ((size_t)head * (a.shares + a.most) + work.slot) * RB;
     const auto finish = [&](int i, const v4f* o, float sum, bool any) {
         const uint32_t r = r0 + 16 * i + row, n = r / (uint32_t)a.G;
         if ((int)r >= rows) return;
@@ -509,7 +628,11 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
         __syncthreads();
         v4f* o = (v4f*)mine;
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) o[r16 * (D / 4) + ((4 * cb + g) ^ r16)] = acc[i][cb];
+        for (int cb = 0; cb < CB; ++cb) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][cb][e] = nan[i] >> (4 * cb + e) & 1 ? __builtin_nanf("") : acc[i][cb][e];
+            o[r16 * (D / 4) + ((4 * cb + g) ^ r16)] = acc[i][cb];
+        }
         __syncthreads();
         float top = -INFINITY, sum = 0.0f, any = 0.0f;
 #pragma unroll
@@ -535,6 +658,9 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
             if ((tid & 15) == 0) *(v4f*)(a.stats + ((unit + i) * 16 + row) * 4) = v4f{top, sum, any, 0.0f};
         }
     }
+    if (!a.shares) return;
+    __syncthreads();                                       // (the sums in LDS are read)
+    }
 }
 
 // The sums of a tile's parts: a wave to a row, 16 bytes of a part to a lane, so
@@ -542,44 +668,43 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
 template <class T, int D, int RB>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     constexpr int LP = D / 4, PL = 64 / LP, U = 8;         // lanes to a part, parts to a load
-    const int lane = threadIdx.x & 63, row = (int)(blockIdx.x % (4 * RB)) * 4 + (threadIdx.x >> 6);
-    const int tiles = (int)gridDim.x / (4 * RB), tile = (int)blockIdx.x / (4 * RB), head = blockIdx.y;
-    const TileInfo info = a.tiles[head * tiles + tile];
+    const int lane = threadIdx.x & 63, row = (int)(blockIdx.x % (4 * RB)) * 4 + (threadIdx.x >> 6), head = blockIdx.y;
+    const TileInfo info = a.tiles[(size_t)head * a.most + blockIdx.x / (4 * RB)];
     if (info.used < 2 || row >= info.rows) return;
-    const size_t unit = (size_t)(head * tiles + tile) * a.parts * RB + (row >> 4), step = RB;
+    const size_t unit = ((size_t)head * (a.shares + a.most) + info.slot) * RB + (row >> 4), step = RB;
     const auto at = [&](int p) { return (unit + p * step) * 16 + (row & 15); };
-    constexpr int SP = MAX_PARTS / 64;
-    v4f st[SP];
-#pragma unroll
-    for (int k = 0; k < SP; ++k) st[k] = *(const v4f*)(a.stats + at(min(64 * k + lane, info.used - 1)) * 4);
-    float top = -INFINITY, sum = 0.0f, any = 0.0f, f[SP];
-#pragma unroll
-    for (int k = 0; k < SP; ++k) top = fmaxf(top, st[k][0]);
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2) top = fmaxf(top, __shfl_xor(top, s, 64));
-#pragma unroll
-    for (int k = 0; k < SP; ++k) {
-        f[k] = 64 * k + lane >= info.used ? 0.0f : st[k][0] == -INFINITY ? 1.0f : power(st[k][0] - top);
-        sum += 64 * k + lane < info.used ? f[k] * st[k][1] : 0.0f;
-        any = fmaxf(any, st[k][2]);
-    }
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2) sum += __shfl_xor(sum, s, 64), any = fmaxf(any, __shfl_xor(any, s, 64));
+    // 64 parts at a time, a lane holding one's statistics, with the maximum and the sums so far rescaled
+    float top = -INFINITY, sum = 0.0f, any = 0.0f;
     v4f out{0.0f, 0.0f, 0.0f, 0.0f};
     const int sub = lane / LP, ch = 4 * (lane % LP);
-    for (int p0 = 0; p0 < info.used; p0 += U * PL) {
-        v4f from[U];
-        float w[U];
+    for (int p64 = 0; p64 < info.used; p64 += 64) {
+        const int n = min(info.used - p64, 64);
+        const v4f st = *(const v4f*)(a.stats + at(p64 + min(lane, n - 1)) * 4);
+        float m = st[0];
 #pragma unroll
-        for (int u = 0; u < U; ++u) from[u] = *(const v4f*)(a.sums + at(min(p0 + u * PL + sub, info.used - 1)) * D + ch);
-        const int k = p0 >> 6;                             // (U PL parts lie in one 64)
-        const float mine = k == 0 ? f[0] : k == 1 ? f[1] : k == 2 ? f[2] : f[3];
+        for (int s = 1; s < 64; s *= 2) m = fmaxf(m, __shfl_xor(m, s, 64));
+        m = fmaxf(m, top);
+        const float old = m == -INFINITY ? 1.0f : power(top - m);
+        const float f = lane >= n ? 0.0f : st[0] == -INFINITY ? 1.0f : power(st[0] - m);
+        top = m;
+        float more = lane < n ? f * st[1] : 0.0f;
 #pragma unroll
-        for (int u = 0; u < U; ++u) w[u] = __shfl(mine, (p0 + u * PL + sub) & 63, 64);
+        for (int s = 1; s < 64; s *= 2) more += __shfl_xor(more, s, 64);
+        sum = sum * old + more;
+        any = fmaxf(any, __ballot(st[2] > 0.0f) ? 1.0f : 0.0f);
+        out *= old;
+        for (int p0 = 0; p0 < n; p0 += U * PL) {
+            v4f from[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+            for (int u = 0; u < U; ++u) from[u] = *(const v4f*)(a.sums + at(p64 + min(p0 + u * PL + sub, n - 1)) * D + ch);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) out[e] = p0 + u * PL + sub < info.used ? out[e] + w[u] * from[u][e] : out[e];
+            for (int u = 0; u < U; ++u) {
+                const int p = p0 + u * PL + sub;
+                const float wt = __shfl(f, p & 63, 64);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) out[e] = p < n ? out[e] + wt * from[u][e] : out[e];
+            }
+        }
     }
 #pragma unroll
     for (int s = LP; s < 64; s *= 2)
@@ -592,12 +717,16 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 
 template <class T, int BITS, int D, int RB>
 hipError_t launch_attn(AttnArgs a, int kv_heads, hipStream_t st) {
-    const long long tiles = ((long long)a.N * a.G) / (16 * RB) + a.pages.seqs;
+    const long long tiles = ((long long)a.N * a.G) / (16 * RB) + a.pages.seqs;   // at most, of one key head
     const long long blocks = (((long long)a.pages.ld << a.pages.shift) + 31) / 32;
-    a.parts = (int)std::max(1ll, std::min({(blocks + 3) / 4, MAX_UNITS / (tiles * kv_heads), (long long)MAX_PARTS}));
-    const hipError_t e = launch(k_attn<T, BITS, D, RB>, dim3((unsigned)(tiles * a.parts), kv_heads), 256u, st, a);
-    if (e != hipSuccess || a.parts == 1) return e;
-    return launch(k_attn_join<T, D, RB>, dim3((unsigned)(tiles * 4 * RB), kv_heads), 256u, st, a);
+    // as many workgroups as the card holds at once, if the tiles do not make them by themselves
+    const long long full = 256 * waves_of(sizeof(T) == 4, D, RB) / kv_heads;
+    a.most = (int)tiles;
+    a.shares = a.pages.seqs <= 64 && blocks > LEAST_SHARE && tiles < full && (full + tiles) * kv_heads <= MAX_SLOTS && tiles * (blocks + 16) < 1ll << 30
+                   ? (int)full : 0;
+    const hipError_t e = launch(k_attn<T, BITS, D, RB>, dim3((unsigned)(a.shares ? a.shares : tiles), kv_heads), 256u, st, a);
+    if (e != hipSuccess || !a.shares) return e;
+    return launch(k_attn_join<T, D, RB>, dim3((unsigned)tiles * 4 * RB, kv_heads), 256u, st, a);
 }
 
 template <class T, int BITS, int D>
@@ -636,7 +765,7 @@ dq_status dq_attn_create(int32_t device, dq_attn** out) {
     std::unique_ptr<dq_attn, void (*)(dq_attn*)> guard(a, free_attn);
     a->device = device;
     hipError_t e;
-    if ((e = hipMalloc((void**)&a->sums, (SUM_FLOATS + STAT_FLOATS) * 4 + MAX_UNITS * sizeof(TileInfo))) != hipSuccess) {
+    if ((e = hipMalloc((void**)&a->sums, (SUM_FLOATS + STAT_FLOATS) * 4 + MAX_SLOTS * sizeof(TileInfo))) != hipSuccess) {
         a->sums = nullptr;
         return hip_fail(e, "hipMalloc workspace");
     }
