@@ -289,6 +289,30 @@ PyObject* kv_write(PyObject*, PyObject* const* v, Py_ssize_t n) {
     });
 }
 
+// kv_read(kv, seqs, k, v, stream)
+PyObject* kv_read(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    return guarded([&](int* status) {
+        Matrix m[2];
+        dq_dtype dt = DQ_F32;
+        void* stream;
+        bool ok = true;
+        if (n != 5 || (v[2] == Py_None && v[3] == Py_None)) return false;
+        const dq_kv* kv = (const dq_kv*)address_of(v[0], "address", &ok);
+        const dq_seqs* seqs = (const dq_seqs*)address_of(v[1], "address", &ok);
+        if (!ok || !kv || !seqs) return false;
+        const int device = (int)number_of(v[0], "device", &ok);
+        if (number_of(v[1], "device", &ok) != device || !ok || !stream_of(v[4], device, &stream)) return false;
+        const int one = v[2] != Py_None ? 0 : 1;
+        for (int i = one; i < 2; ++i)
+            if (v[2 + i] != Py_None && (!matrix(v[2 + i], 16, &m[i]) || m[i].c != (int64_t)kv->heads * kv->head_dim || m[i].device != device ||
+                                        !dtype_of(m[i].type, &dt) || m[i].n != m[one].n || m[i].type != m[one].type))
+                return false;
+        Released released;
+        *status = dq_kv_read(kv, seqs, m[one].n, m[0].p, m[0].ld, m[1].p, m[1].ld, dt, device, stream);
+        return true;
+    });
+}
+
 // attn_rows(kv, seqs, q, a, y, scale (below 0: head_dim ** -0.5), block, window, prefix, cap, stream)
 PyObject* attn_rows(PyObject*, PyObject* const* v, Py_ssize_t n) {
     return guarded([&](int* status) {
@@ -329,6 +353,7 @@ PyMethodDef methods[] = {
     {"norm_rope", (PyCFunction)(void (*)(void))norm_rope, METH_FASTCALL, "dq_norm_rope(x, heads, y, norm, gain, eps, rope, pos, stream)"},
     {"kv_write", (PyCFunction)(void (*)(void))kv_write, METH_FASTCALL,
      "dq_kv_write(kv, seqs, k, v, q, y, norm, gain, gain_q, eps, rope, pos, stream)"},
+    {"kv_read", (PyCFunction)(void (*)(void))kv_read, METH_FASTCALL, "dq_kv_read(kv, seqs, k, v, stream)"},
     {"attn_rows", (PyCFunction)(void (*)(void))attn_rows, METH_FASTCALL,
      "dq_attn_rows(kv, seqs, q, a, y, scale, block, window, prefix, cap, stream)"},
     {nullptr, nullptr, 0, nullptr}};

@@ -923,8 +923,13 @@ def dq_kv_write(kv: KV, seqs: Seqs, k, v, q=None, y=None, norm: Optional[str] = 
 
 def dq_kv_read(kv: KV, seqs: Seqs, k=None, v=None, stream=None):
     """The values of the rows' tokens: k and v [N][heads * head_dim] in bf16 or fp32, or one of them."""
-    import torch
     f = "dq_kv_read"
+    call = _CALL or _native()
+    if call is not None and isinstance(kv, KV) and isinstance(seqs, Seqs):
+        status = call.kv_read(kv, seqs, k, v, _raw(stream))
+        if status is not None:
+            return _check(status, f) if status else None
+    import torch
     dev = _cache_batch(f, kv, seqs)
     given = [t for t in (k, v) if t is not None]
     if not given:
