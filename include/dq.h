@@ -510,7 +510,7 @@ dq_status dq_kv_read(const dq_kv* kv, const dq_seqs* seqs, int64_t N, void* k_de
                      dq_dtype dt, int32_t device, void* stream);
 
 /* Workspace of dq_attn_rows on one device: sums of the parts that a long cache
- * is split into (72 MiB).  Must not be used by two streams at once (two captured
+ * is split into (34 MiB).  Must not be used by two streams at once (two captured
  * graphs that share one must not run at once either). */
 typedef struct dq_attn dq_attn;
 dq_status dq_attn_create(int32_t device, dq_attn** out);
@@ -540,7 +540,7 @@ typedef struct {
  * bf16: weights are rounded to bf16 for their product with v and summed as
  * rounded; fp32: q is taken at its full precision, weights to 16 bits.
  * Tuned for few rows: those of a sequence that share a key head are taken up to
- * 64 (rows times heads) at a time, each such group reading the cache again.
+ * 32 (rows times heads) at a time, each such group reading the cache again.
  * Repeated calls agree bit for bit. */
 dq_status dq_attn_rows(const dq_kv* kv, const dq_seqs* seqs, int64_t N, const void* q_dev, int64_t ldq, dq_dtype dt,
                        int32_t q_heads, const dq_attn_ops* ops, dq_attn* a, void* y_dev, int64_t ldy, int32_t device,

@@ -40,7 +40,7 @@ namespace {
 
 // Parts of tiles (a tile: up to 16 RB rows that share a key head; a part: some of
 // the tokens they see) that may meet in the workspace, and blocks of 16 rows to one.
-constexpr int MAX_SLOTS = 2048, MAX_RB = 4;
+constexpr int MAX_SLOTS = 2048, MAX_RB = 2;
 constexpr size_t SUM_FLOATS = size_t(MAX_SLOTS) * MAX_RB * 16 * 128, STAT_FLOATS = size_t(MAX_SLOTS) * MAX_RB * 16 * 4;
 // A tile in parts: how many (0 or 1: nothing to join), its rows, its sequence's
 // first row and the rows before it, and the first part's slot.
@@ -269,7 +269,7 @@ __device__ __forceinline__ Work whole_tile(const AttnArgs& a, int u) {
 }
 
 // Waves to a SIMD that the registers are kept for.
-constexpr int waves_of(bool f32, int D, int RB) { return D == 64 ? (RB == 1 ? (f32 ? 3 : 4) : RB == 2 ? 2 : 1) : RB == 1 ? (f32 ? 2 : 3) : RB == 2 && !f32 ? 2 : 1; }
+constexpr int waves_of(bool f32, int D, int RB) { return RB == 1 ? (f32 ? (D == 64 ? 3 : 2) : D == 64 ? 4 : 3) : f32 && D == 128 ? 1 : 2; }
 
 template <class T, int BITS, int D, int RB>
 __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(AttnArgs a) {
@@ -682,7 +682,13 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     const int sub = lane / LP, ch = 4 * (lane % LP);
     for (int p64 = 0; p64 < info.used; p64 += 64) {
         const int n = min(info.used - p64, 64);
+        v4f from[U];
+        const auto fetch = [&](int p0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) from[u] = *(const v4f*)(a.sums + at(p64 + min(p0 + u * PL + sub, n - 1)) * D + ch);
+        };
         const v4f st = *(const v4f*)(a.stats + at(p64 + min(lane, n - 1)) * 4);
+        fetch(0);
         float m = st[0];
 #pragma unroll
         for (int s = 1; s < 64; s *= 2) m = fmaxf(m, __shfl_xor(m, s, 64));
@@ -697,9 +703,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
         any = fmaxf(any, __ballot(st[2] > 0.0f) ? 1.0f : 0.0f);
         out *= old;
         for (int p0 = 0; p0 < n; p0 += U * PL) {
-            v4f from[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) from[u] = *(const v4f*)(a.sums + at(p64 + min(p0 + u * PL + sub, n - 1)) * D + ch);
+            if (p0) fetch(p0);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int p = p0 + u * PL + sub;
@@ -730,9 +734,9 @@ hipError_t launch_attn(AttnArgs a, int kv_heads, hipStream_t st) {
                    ? (int)full : 0;
     const hipError_t e = launch(k_attn<T, BITS, D, RB>, dim3((unsigned)(a.shares ? a.shares : tiles), kv_heads), 256u, st, a);
     if (e != hipSuccess || !a.shares) return e;
-    // (a wave to a row while that is not more workgroups than compute units: 1 x 4096 14.0 -> 12.3 us; else four rows to
-    // a wave: 64 sequences 118 -> 116)
-    a.join = tiles * kv_heads * RB <= 64 ? 4 : 1;
+    // (a wave to a row while that makes no more workgroups than the card holds at once: 1 x 4096 14.0 -> 12.3 us; else
+    // four rows to a wave: 64 sequences 118 -> 116)
+    a.join = tiles * kv_heads * RB <= 512 ? 4 : 1;
     return launch(k_attn_join<T, D, RB>, dim3((unsigned)tiles * RB * a.join, kv_heads), 256u, st, a);
 }
 
@@ -740,8 +744,6 @@ template <class T, int BITS, int D>
 hipError_t launch_attn(const AttnArgs& a, int kv_heads, hipStream_t st) {
     const long long rows = ((long long)a.N * a.G + a.pages.seqs - 1) / a.pages.seqs;   // of a sequence, in the mean
     if (rows <= 16) return launch_attn<T, BITS, D, 1>(a, kv_heads, st);
-    if constexpr (sizeof(T) == 2)
-        if (rows > 32) return launch_attn<T, BITS, D, 4>(a, kv_heads, st);
     return launch_attn<T, BITS, D, 2>(a, kv_heads, st);
 }
 
