@@ -40,10 +40,13 @@ class Batch:
         self.first = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
         self.length = np.asarray(length, np.int32)
         self.n = int(self.first[-1]) + tail
-        width = max(1, max(-(-int(l) // page_tokens) for l in length))
-        self.count = len(rows) * width + spare
-        g = np.random.default_rng(seed)
-        self.pages = g.permutation(self.count)[:len(rows) * width].reshape(len(rows), width).astype(np.int32)
+        need = [-(-int(l) // page_tokens) for l in length]
+        self.count = max(1, sum(need) + spare)
+        order = np.random.default_rng(seed).permutation(self.count)
+        # (what lies behind a sequence's last page is never looked at: it names no page)
+        self.pages = np.full((len(rows), max(1, max(need))), 2 ** 30, np.int32)
+        for b, k in enumerate(need):
+            self.pages[b, :k], order = order[:k], order[k:]
         self.P, self.device = page_tokens, device
 
     def seqs(self, dq):

@@ -185,7 +185,8 @@ def test_a_decoding_step(dqm):
     w2 = dqm.dq_prepare_weights_lowrank(torch.randn(ci, qc, generator=g) / 16, None, None)
     r1, r2, work = dqm.dq_rows_create(w1, B), dqm.dq_rows_create(w2, B), dqm.dq_attn_create(0)
     rope = dqm.Rope([torch.from_numpy(heads.table(10000.0 ** (-np.arange(dim // 2) / (dim // 2)), 64)).to(DEV)], False)
-    batch = Batch([1] * B, [40, 7, 16], P, DEV, seed=55)
+    batch = Batch([1] * B, [40 + steps, 7 + steps, 16 + steps], P, DEV, seed=55)     # (pages for what the steps add)
+    batch.length = batch.length - steps
     start = host_cache(batch, kv_heads, dim, 8, 57)
     gain = (1 + 0.1 * torch.randn(dim, generator=g)).to(DEV)
 

@@ -729,6 +729,17 @@ hipError_t launch_attn(AttnArgs a, int kv_heads, hipStream_t st) {
     const long long blocks = (((long long)a.pages.ld << a.pages.shift) + 31) / 32;
     // as many workgroups as the card holds at once, if the tiles do not make them by themselves
     const long long full = 256 * waves_of(sizeof(T) == 4, D, RB) / kv_heads;
+    if (a.pages.seqs > 64 && tiles < full) {               // (64 sequences at a time)
+        hipError_t e = hipSuccess;
+        for (int i = 0; i < a.pages.seqs && e == hipSuccess; i += 64) {
+            AttnArgs some = a;
+            some.pages.first += i, some.pages.length += i, some.pages.table += (size_t)i * a.pages.ld;
+            if (a.prefix) some.prefix += i;
+            some.pages.seqs = std::min(64, a.pages.seqs - i);
+            e = launch_attn<T, BITS, D, RB>(some, kv_heads, st);
+        }
+        return e;
+    }
     a.most = (int)tiles;
     a.shares = a.pages.seqs <= 64 && blocks > LEAST_SHARE && tiles < full && (full + tiles) * kv_heads <= MAX_SLOTS && tiles * (blocks + 16) < 1ll << 30
                    ? (int)full : 0;
