@@ -329,7 +329,9 @@ __global__ __launch_bounds__(1024) void k_heads(HeadsArgs a) {
         uint32_t e;
         if (p.kind == TO_FP8) {
             e = encode_group<false>(v[i], d);
-            *(v2w*)((uint8_t*)p.y + (tok * a.lph + lane) * 8) = d;
+            v2w* to = (v2w*)((uint8_t*)p.y + (tok * a.lph + lane) * 8);
+            if (a.nt) put<true>(to, d);
+            else put<false>(to, d);
         } else {
             e = encode_group<true>(v[i], d);
             *(uint32_t*)((uint8_t*)p.y + (tok * a.lph + lane) * 4) = d[0];
@@ -347,51 +349,40 @@ struct ReadArgs {
     Pages pages;
     long long N, first;
     int lph;                // lanes of 16 channels to a head
-    int nch, tpr;           // chunks of 16 channels to a row
+    int nch, tpr, segs;     // chunks of 16 channels to a row; threads and workgroups to one
     int part0;              // 1: only values are read
 };
 
-// A thread decodes CH chunks of 16 channels (half an MX group) of a row.
-template <class T, int BITS, int CH>
-__global__ __launch_bounds__(512) void k_read(ReadArgs a) {
-    const int w = blockIdx.y + a.part0, tpr = a.tpr, shift = __builtin_ctz(tpr);
-    const long long row = a.first + (long long)blockIdx.x * (blockDim.x >> shift) + (threadIdx.x >> shift);
-    const int t = threadIdx.x & (tpr - 1);
+// A thread decodes 16 channels (half an MX group) of a row: with one chunk to a
+// thread there are twice the waves that two leave (32760 x 12 heads 70 -> 56 us, 5.5 TB/s).
+template <class T, int BITS>
+__global__ __launch_bounds__(256) void k_read(ReadArgs a) {
+    const int w = (int)blockIdx.y / a.segs + a.part0, tpr = a.tpr, shift = __builtin_ctz(tpr);
+    const long long row = a.first + (long long)blockIdx.x * (256 >> shift) + (threadIdx.x >> shift);
+    const int c = ((int)blockIdx.y % a.segs) * tpr + (threadIdx.x & (tpr - 1));
     const Place at = place_of(a.pages, starts_of(a.pages), row - ((threadIdx.x & 63) >> shift), tpr);
-    if (row >= a.N || at.t == NOWHERE) return;
-    T* y = (T*)a.y[w] + row * a.ldy[w];
-    constexpr int W = BITS == 8 ? 4 : 2;            // words of codes to a chunk
-    uint32_t code[CH][W];
-    uint32_t e[CH];
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        const int c = i * tpr + t;
-        e[i] = 0;
-#pragma unroll
-        for (int j = 0; j < W; ++j) code[i][j] = 0;
-        if (c >= a.nch || at.page < 0) continue;
+    if (row >= a.N || at.t == NOWHERE || c >= a.nch) return;
+    constexpr int W = BITS == 8 ? 4 : 2;            // words of codes
+    uint32_t code[W] = {}, e = 0;
+    if (at.page >= 0) {
         const long long tok = token_row(a.pages, at, c / a.lph);
         const int lane = c & (a.lph - 1);
         const uint32_t* p = (const uint32_t*)a.codes[w] + (tok * a.lph + lane) * W;
         if constexpr (BITS == 8) {
             const v4w v = *(const v4w*)p;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) code[i][j] = v[j];
+            for (int j = 0; j < 4; ++j) code[j] = v[j];
         } else {
             const v2w v = *(const v2w*)p;
-            code[i][0] = v[0], code[i][1] = v[1];
+            code[0] = v[0], code[1] = v[1];
         }
-        e[i] = a.scales[w][tok * (a.lph >> 1) + (lane >> 1)];
+        e = a.scales[w][tok * (a.lph >> 1) + (lane >> 1)];
     }
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        const int c = i * tpr + t;
-        if (c >= a.nch) continue;
-        float v[16];
-        decode16<BITS>(code[i], e[i], v);
-        Stream<T>::template store<true>(y + 16 * c, v);
-        Stream<T>::template store<true>(y + 16 * c + 8, v + 8);
-    }
+    float v[16];
+    decode16<BITS>(code, e, v);
+    T* y = (T*)a.y[w] + row * a.ldy[w] + 16 * c;
+    Stream<T>::template store<true>(y, v);
+    Stream<T>::template store<true>(y + 8, v + 8);
 }
 
 struct TableArgs {
@@ -415,14 +406,14 @@ int pow2_at_least(int n, int least) {
     return p;
 }
 
-// Threads to a row of nch chunks (a power of two from `least` to `most`) and chunks
-// to a thread (up to 5; one, where a row has fewer than `wave` threads) that leave
-// the fewest lanes idle; of equal ones the fewest threads.
-void share_row(int nch, int least, int most, int wave, int* tpr, int* ch) {
+// Threads to a row of nch chunks (a power of two from `least` on) and chunks to a
+// thread (up to 5; one, where a row takes less than a wave) that leave the fewest
+// lanes idle; of equal ones the fewest threads.
+void share_row(int nch, int least, int* tpr, int* ch) {
     int best = 1 << 30;
-    for (int t = least; t <= most; t *= 2) {
+    for (int t = least; t <= 1024; t *= 2) {
         const int c = (nch + t - 1) / t;
-        if (c > 5 || (c > 1 && t < wave)) continue;
+        if (c > 5 || (c > 1 && t < 64)) continue;
         if (c * t < best) best = c * t, *tpr = t, *ch = c;
     }
 }
@@ -439,7 +430,7 @@ hipError_t launch_heads(HeadsArgs a, int parts, hipStream_t st) {
         a.tpr = std::min(pow2_at_least(nch, a.lph), row_norm ? 1024 : 256);
         ch = row_norm ? (nch + a.tpr - 1) / a.tpr : 1;
     } else {
-        share_row(nch, a.lph, 1024, 64, &a.tpr, &ch);
+        share_row(nch, a.lph, &a.tpr, &ch);
     }
     a.nt = !few;
     int segs = 0;
@@ -466,21 +457,17 @@ hipError_t launch_heads(HeadsArgs a, int parts, hipStream_t st) {
 
 template <class T, int BITS>
 hipError_t launch_read(ReadArgs a, int parts, hipStream_t st) {
-    int ch = 1;
-    share_row(a.nch, a.lph, 512, 64, &a.tpr, &ch);
-    const int threads = std::max(256, a.tpr), rows = threads / a.tpr;
-    const long long most = (1ll << 31) / threads;
-    hipError_t e = hipSuccess;
-    for (; a.first < a.N && e == hipSuccess; a.first += most * rows) {
-        const dim3 grid((unsigned)std::min(most, (a.N - a.first + rows - 1) / rows), parts);
-        switch (ch) {
-            case 1: e = launch(k_read<T, BITS, 1>, grid, threads, st, a); break;
-            case 2: e = launch(k_read<T, BITS, 2>, grid, threads, st, a); break;
-            case 3: e = launch(k_read<T, BITS, 3>, grid, threads, st, a); break;
-            case 4: e = launch(k_read<T, BITS, 4>, grid, threads, st, a); break;
-            default: e = launch(k_read<T, BITS, 5>, grid, threads, st, a); break;
-        }
+    // as many threads as leave the fewest idle, of equal ones the most
+    int best = 1 << 30;
+    for (int t = a.lph; t <= 256; t *= 2) {
+        const int n = (a.nch + t - 1) / t;
+        if (n * t <= best && (n == 1 || t >= 64)) best = n * t, a.tpr = t, a.segs = n;
     }
+    const int rows = 256 / a.tpr;
+    const long long most = (1ll << 31) / 256;
+    hipError_t e = hipSuccess;
+    for (; a.first < a.N && e == hipSuccess; a.first += most * rows)
+        e = launch(k_read<T, BITS>, dim3((unsigned)std::min(most, (a.N - a.first + rows - 1) / rows), parts * a.segs), 256u, st, a);
     return e;
 }
 
