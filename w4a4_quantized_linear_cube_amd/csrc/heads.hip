@@ -65,9 +65,7 @@ __device__ __forceinline__ double sum_group(double v, int n) {
     return v;
 }
 
-__device__ __forceinline__ float row_factor(double s, int channels, double eps) {
-    return (float)(1.0 / sqrt(s / (double)channels + eps));
-}
+__device__ __forceinline__ float factor_of(double mean, double eps) { return (float)(1.0 / sqrt(mean + eps)); }
 
 // A kernel's argument as a value of its own: the compiler would else turn a
 // choice between two arguments into a load from the chosen one's address.
@@ -256,8 +254,24 @@ __global__ __launch_bounds__(1024) void k_heads(HeadsArgs a) {
         }
         float f[CH];
         if (p.norm == DQ_NORM_HEAD) {
+            // (a head has a power of two of channels: its mean by an exact product.)  All
+            // of a head's lanes hold its sum, so each forms the factor of one of
+            // the thread's CH heads and they are exchanged: a square root
+            // and a division in fp64 take as long as the rest
+            const double share = 1.0 / (double)(8 * a.lph);
 #pragma unroll
-            for (int i = 0; i < CH; ++i) f[i] = row_factor(sum_group(q[i], a.lph), 8 * a.lph, a.eps);
+            for (int i = 0; i < CH; ++i) q[i] = sum_group(q[i], a.lph) * share;
+            if (CH == 1 || a.lph < CH) {
+#pragma unroll
+                for (int i = 0; i < CH; ++i) f[i] = factor_of(q[i], a.eps);
+            } else {
+                double mine = q[0];
+#pragma unroll
+                for (int i = 1; i < CH; ++i) mine = lane == i ? q[i] : mine;
+                const float g = factor_of(mine, a.eps);
+#pragma unroll
+                for (int i = 0; i < CH; ++i) f[i] = __shfl(g, (int)(threadIdx.x & 63) - lane + i, 64);
+            }
         } else {
             // blocks of 64 chunks by their lanes, then the blocks by their number's bits
             double s;
@@ -274,7 +288,7 @@ __global__ __launch_bounds__(1024) void k_heads(HeadsArgs a) {
                 __syncthreads();
                 s = sum_group((t & 63) < CH * waves ? mine[t & 63] : 0.0, 64);
             }
-            const float g = row_factor(s, 8 * p.nch, a.eps);
+            const float g = factor_of(s / (double)(8 * p.nch), a.eps);
 #pragma unroll
             for (int i = 0; i < CH; ++i) f[i] = g;
         }
