@@ -491,11 +491,12 @@ typedef struct {
  *         projection do); gain_k_dev, gain_q_dev, y_dev (q's output, [N][q_heads *
  *         head_dim] of dtype ydt; may be q_dev itself, same dtype and stride) as in dq_norm_rope
  * Scales as everywhere here: the smallest 2^e, e >= -127, with max|v| <= q_max 2^e
- * over 32 channels (448, or 6 for E2M1), codes to nearest, ties to even.  Infinite and NaN elements do
- * not enter the scale and get the E4M3 NaN code; E2M1 has none, so they turn
- * their group's scale code to 255.  Rows without a token in the cache are not coded
- * (their queries are still rotated).  Where two rows of a call share a place its codes are
- * undefined.  Cache, q, k, v and y must not share memory otherwise. */
+ * over 32 channels (448, or 6 for E2M1), codes to nearest, ties to even.
+ * Infinite and NaN elements do not enter the scale and get the E4M3 NaN code;
+ * E2M1 has none, so they turn their group's scale code to 255.  Rows without a
+ * token in the cache are not coded (their queries are still rotated).  Where two
+ * rows of a call share a place its codes are undefined.  Cache, q, k, v and y
+ * must not share memory otherwise. */
 dq_status dq_kv_write(const dq_kv* kv, const dq_seqs* seqs, int64_t N, dq_dtype dt, const void* k_dev, int64_t ldk,
                       const void* v_dev, int64_t ldv, const void* gain_k_dev, const void* q_dev, int64_t ldq, int32_t q_heads,
                       const void* gain_q_dev, void* y_dev, int64_t ldy, dq_dtype ydt, const dq_head_ops* ops, int32_t device,
@@ -504,8 +505,8 @@ dq_status dq_kv_write(const dq_kv* kv, const dq_seqs* seqs, int64_t N, dq_dtype 
 /* The values of the N rows' tokens, k_dev and v_dev [N][heads * head_dim] of dtype
  * dt (either may be NULL, not both), rows ld elements apart, 16-byte aligned:
  * exact where the type holds them (E4M3 and E2M1 values from 2^-126 to 2^127 in
- * either; beyond, infinite).  A row without a token in the cache is zero.  To read whole sequences give
- * first_dev as the sums of the lengths. */
+ * either; beyond, infinite).  A row without a token in the cache is zero.  To
+ * read whole sequences give first_dev as the sums of the lengths. */
 dq_status dq_kv_read(const dq_kv* kv, const dq_seqs* seqs, int64_t N, void* k_dev, int64_t ldk, void* v_dev, int64_t ldv,
                      dq_dtype dt, int32_t device, void* stream);
 
@@ -522,8 +523,8 @@ void dq_attn_destroy(dq_attn* a);
  * block 0: all L (window must then be 0, prefix has no effect).  block 1 is the causal mask; with
  * block the tokens of a frame, a row sees its own frame and those before it. */
 typedef struct {
-    double scale;                  /* (0, 2^64]; head_dim ** -0.5 as a rule */
-    double cap;                    /* scores cap tanh(s / cap); 0: as they are; else [2^-64, 2^64] */
+    double scale;                  /* [2^-32, 2^32]; head_dim ** -0.5 as a rule */
+    double cap;                    /* scores cap tanh(s / cap); 0: as they are; else [2^-32, 2^32] */
     int64_t block, window;         /* [0, 2^31) */
     const int32_t* prefix_dev;     /* [seqs], or NULL */
 } dq_attn_ops;

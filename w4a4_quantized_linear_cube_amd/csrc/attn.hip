@@ -199,7 +199,8 @@ __device__ __forceinline__ long long reach(const Pages& p) { return min((long lo
 template <class V>
 __device__ __forceinline__ V scan(V v) {
     const auto moved = [](V x, auto ctrl, auto rows) {
-        return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value, decltype(rows)::value, 0xF, true));
+        constexpr int C = decltype(ctrl)::value, R = decltype(rows)::value;
+        return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), C, R, 0xF, true));
     };
     using std::integral_constant;
     const integral_constant<int, 0xF> all{};
@@ -220,9 +221,9 @@ struct Work {
     bool head;                // its first part
 };
 // Up to 64 sequences: a lane holds one.  Their tiles stand in a row, each as long
-// as the blocks of tokens it sees at most and TILE_COST, and a workgroup takes an equal stretch of it: a
-// part of a long tile, or several short ones, whatever the lengths (64 sequences
-// of up to 8192 tokens: XX us, as three parts each 148).
+// as the blocks of tokens that it sees at most, and TILE_COST, and a workgroup
+// takes an equal stretch of the row: a part of a long tile or several short ones,
+// whatever the lengths (64 sequences of 132 to 8192 tokens 111 us; three parts to each tile 144).
 struct Batch64 {
     int f0, f1, length, tiles;
     int cost, upto, tiles_upto, pad;   // of one tile; of this sequence's and earlier tiles together
@@ -294,373 +295,376 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
         batch[tid & 63] = x;                                   // (every wave the same)
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         const int total = __builtin_amdgcn_readlane(x.upto, 63), tiles = __builtin_amdgcn_readlane(x.tiles_upto, 63);
+        // (more tiles than there can be: first_dev is not ascending, and nothing is done)
+        const bool fit = tiles <= a.most;
+        if (u >= (fit ? tiles : 0) && u < a.most && tid == 0) a.tiles[(size_t)head * a.most + u].used = 0;   // (no tile of that number)
+        if (!fit) return;
         share = one(max((int)(((uint32_t)total + a.shares - 1) / (uint32_t)a.shares), LEAST_SHARE));
         pos = (int)min((long long)u * share, (long long)total), end = min(total, pos + share);
-        if (u >= tiles && u < a.most && tid == 0) a.tiles[(size_t)head * a.most + u].used = 0;   // (no tile of that number)
     } else {
         work = whole_tile<TR>(a, u);
     }
     for (;;) {
-    int lane = tid & 63;
-    asm volatile("" : "+v"(lane));                         // (what goes by the lane is formed for each tile, not kept over all of them)
-    const int r16 = lane & 15, g = lane >> 4;
-    if (a.shares) {
-        if (pos >= end) return;
-        const int b = (int)__popcll(__ballot(batch[lane].upto <= pos));
-        const Batch64 x = batch[b];
-        const int tiles = one(x.tiles), cost = one(x.cost), begin = one(x.upto) - tiles * cost, tile = (pos - begin) / cost;
-        const int first = begin + tile * cost, from = pos - first, to = min(cost, from + end - pos), number = one(x.tiles_upto) - tiles + tile;
-        pos += to - from;
-        work = {b, one(x.f0), one(x.f1), one(x.length), tile, max(from - TILE_COST, 0), max(to - TILE_COST, 0), 0, u + number, number, false};
-        if (work.c0 >= work.c1) continue;                  // (the part that stands for the tile's cost)
-        const int head_of = (first + TILE_COST) / share;   // the workgroup of its first block
-        work.parts = (first + cost - 1) / share - head_of + 1;
-        work.head = u == head_of;
-    }
-    const int b = one(work.b), f0 = one(work.f0), f1 = one(work.f1), length = one(work.length);
-    const int L = (int)min((long long)length, reach(a.pages));
-    const int rows = (f1 - f0) * a.G, r0 = one(work.tile) * TR;
-    if (r0 < 0 || r0 >= rows) return;                      // (no such tile; of shares there is none)
-    const int pf = a.block && a.prefix ? min(max(((Scalars)(uintptr_t)a.prefix)[b], 0), L) : 0;
-    const int used = one(work.parts);
-    if (a.shares && work.head && tid == 0)
-        a.tiles[(size_t)head * a.most + work.number] = TileInfo{used, min(rows - r0, TR), f0, r0, work.slot, {0, 0, 0}};
-
-    // ---- what each row sees: [lo, hi) and [0, pf)
-    const int t0 = length - (f1 - f0);                     // the first row's place
-    const auto sees = [&](int r, int* lo, int* hi) {       // r: packed row
-        *lo = 0, *hi = L;
-        if (!a.block) return;
-        const int t = t0 + (int)((uint32_t)r / (uint32_t)a.G);
-        // the end of the row's block (0 before the first token)
-        const long long e = t < 0 ? 0 : a.block == 1 ? t + 1ll : (long long)((uint32_t)t / (uint32_t)a.block + 1) * a.block;
-        *hi = (int)min(e, (long long)L);
-        if (a.window) *lo = (int)min(max(e - a.window, 0ll), (long long)L);
-    };
-    int lo0, hi0, lo1, hi1;                                // of the tile's first and last row
-    sees(r0, &lo0, &hi0);
-    sees(min(rows, r0 + TR) - 1, &lo1, &hi1);
-    lo0 = one(lo0), hi0 = one(hi0), lo1 = one(lo1), hi1 = one(hi1);
-    // blocks of 32 tokens that some row sees: [0, na) and [b0, b0 + nb)
-    int na = (pf + 31) >> 5, b0 = lo0 >> 5, nb = hi1 > lo0 ? ((hi1 + 31) >> 5) - b0 : 0;
-    if (na >= b0) nb = max(b0 + nb, na), b0 = 0, na = 0;
-    const int blocks = na + nb;
-    const int c_end = min(blocks, one(work.c1));
-
-    // ---- the cache
-    const auto token0 = [&](int c) { return (c < na ? c : c - na + b0) << 5; };
-    // Pages of a block's two halves, as the table has them (places past its end:
-    // its last entry; a block past the part's last: the last's), and those that
-    // are the cache's, or -1.  Scalar loads: a wave's wait for them does not wait for the cache's.
-    struct Two {
-        int p[2];
-    };
-    const Scalars table = (Scalars)(uintptr_t)(a.pages.table + (size_t)b * a.pages.ld);
-    const auto near = [&](int c) { return max(min(c, c_end - 1), 0); };
-    const auto entries = [&](int c) {
-        const int t = token0(near(c));
-        return Two{{table[min(t >> a.pages.shift, a.pages.ld - 1)], table[min((t + 16) >> a.pages.shift, a.pages.ld - 1)]}};
-    };
-    const auto pages_at = [&](int c, Two e) {
-        const int t = token0(near(c));
-        return Two{{t < L && (uint32_t)e.p[0] < (uint32_t)a.pages.pages ? e.p[0] : -1,
-                    t + 16 < L && (uint32_t)e.p[1] < (uint32_t)a.pages.pages ? e.p[1] : -1}};
-    };
-    const int mask = (1 << a.pages.shift) - 1;
-    // A load's address is a block's, which is scalar, and an offset that is the
-    // lane's.  Scale codes come as the aligned word that holds a row's (with D 64 two rows').
-    constexpr int RC = D * BITS / 8, RS = D / 32;          // bytes of a row's codes and scale codes
-    const auto scale_in = [](uint32_t word, int row, int group) {
-        return scale_of(word >> (8 * (D == 128 ? group : 2 * (row & 1) + group)) & 0xff);
-    };
-    const uint32_t key_at = r16 * RC + g * (Tok::KW * 4), key_scale_at = r16 * RS & ~3;
-    const uint32_t value_at = lane / LPR * RC + lane % LPR * (Tok::VW * 4), value_scale_at = lane / LPR * RS & ~3;
-    Tok x;
-    const auto row_of = [&](int c, Two pg, int h) {        // the cache's row of a half's first token (in page 0 where there is none)
-        return (((long long)max(pg.p[h], 0) * a.pages.heads + head) << a.pages.shift) + ((token0(near(c)) + 16 * h) & mask);
-    };
-    const auto load_keys = [&](int c, Two pg) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const long long row = row_of(c, pg, h);
-            load_words<Tok::KW>(scalar(a.codes[0] + row * RC) + key_at, x.k[h]);
-            x.ks[h] = *(const __attribute__((address_space(1))) uint32_t*)(scalar(a.scales[0] + row * RS) + key_scale_at);
+        int lane = tid & 63;
+        asm volatile("" : "+v"(lane));                         // (what goes by the lane is formed for each tile, not kept over all of them)
+        const int r16 = lane & 15, g = lane >> 4;
+        if (a.shares) {
+            if (pos >= end) return;
+            const int b = (int)__popcll(__ballot(batch[lane].upto <= pos));
+            const Batch64 x = batch[b];
+            const int tiles = one(x.tiles), cost = one(x.cost), begin = one(x.upto) - tiles * cost, tile = (pos - begin) / cost;
+            const int first = begin + tile * cost, from = pos - first, to = min(cost, from + end - pos), number = one(x.tiles_upto) - tiles + tile;
+            pos += to - from;
+            work = {b, one(x.f0), one(x.f1), one(x.length), tile, max(from - TILE_COST, 0), max(to - TILE_COST, 0), 0, u + number, number, false};
+            if (work.c0 >= work.c1) continue;                  // (the part that stands for the tile's cost)
+            const int head_of = (first + TILE_COST) / share;   // the workgroup of its first block
+            work.parts = (first + cost - 1) / share - head_of + 1;
+            work.head = u == head_of;
         }
-    };
-    const auto load_values = [&](int c, Two pg) {
-#pragma unroll
-        for (int i = 0; i < Tok::VP; ++i) {                // piece i: token (64 / LPR) i + lane / LPR
-            const long long row = row_of(c, pg, (64 / LPR) * i < 16 ? 0 : 1) + (64 / LPR) * i % 16;
-            load_words<Tok::VW>(scalar(a.codes[1] + row * RC) + value_at, x.v[i]);
-            x.vs[i] = *(const __attribute__((address_space(1))) uint32_t*)(scalar(a.scales[1] + row * RS) + value_scale_at);
-        }
-    };
+        const int b = one(work.b), f0 = one(work.f0), f1 = one(work.f1), length = one(work.length);
+        const int L = (int)min((long long)length, reach(a.pages));
+        const int rows = (f1 - f0) * a.G, r0 = one(work.tile) * TR;
+        if (r0 < 0 || r0 >= rows) return;                      // (no such tile; of shares there is none)
+        const int pf = a.block && a.prefix ? min(max(((Scalars)(uintptr_t)a.prefix)[b], 0), L) : 0;
+        const int used = one(work.parts);
+        if (a.shares && work.head && tid == 0)
+            a.tiles[(size_t)head * a.most + work.number] = TileInfo{used, min(rows - r0, TR), f0, r0, work.slot, {0, 0, 0}};
 
-    v4f acc[RB][CB];
-    float m[RB], l[RB];
-    uint32_t nan[RB] = {};                                 // the sums that are NaN by what the masked blocks hold
-    uint32_t seen = 0;                                     // row blocks whose row (of this lane) saw a token
-#pragma unroll
-    for (int i = 0; i < RB; ++i) {
-        m[i] = -INFINITY, l[i] = 0.0f;
-#pragma unroll
-        for (int c = 0; c < CB; ++c) acc[i][c] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    }
+        // ---- what each row sees: [lo, hi) and [0, pf)
+        const int t0 = length - (f1 - f0);                     // the first row's place
+        const auto sees = [&](int r, int* lo, int* hi) {       // r: packed row
+            *lo = 0, *hi = L;
+            if (!a.block) return;
+            const int t = t0 + (int)((uint32_t)r / (uint32_t)a.G);
+            // the end of the row's block (0 before the first token)
+            const long long e = t < 0 ? 0 : a.block == 1 ? t + 1ll : (long long)((uint32_t)t / (uint32_t)a.block + 1) * a.block;
+            *hi = (int)min(e, (long long)L);
+            if (a.window) *lo = (int)min(max(e - a.window, 0ll), (long long)L);
+        };
+        int lo0, hi0, lo1, hi1;                                // of the tile's first and last row
+        sees(r0, &lo0, &hi0);
+        sees(min(rows, r0 + TR) - 1, &lo1, &hi1);
+        lo0 = one(lo0), hi0 = one(hi0), lo1 = one(lo1), hi1 = one(hi1);
+        // blocks of 32 tokens that some row sees: [0, na) and [b0, b0 + nb)
+        int na = (pf + 31) >> 5, b0 = lo0 >> 5, nb = hi1 > lo0 ? ((hi1 + 31) >> 5) - b0 : 0;
+        if (na >= b0) nb = max(b0 + nb, na), b0 = 0, na = 0;
+        const int blocks = na + nb;
+        const int c_end = min(blocks, one(work.c1));
 
-    // V [32][D] bf16: 32 bytes (16 channels) of a token at slot c16 ^ its own, so
-    // that the transposing reads' 8 rows of 32 bytes meet 64 banks
-    uint8_t* const mine = lds[w];                          // (64 D bytes: the slots' exclusive or stays inside)
-    const auto place_v = [&](int tok, int c16) {
-        const int s = D == 128 ? tok & 7 : (tok >> 1) & 3;
-        return tok * (2 * D) + ((c16 ^ s) << 5);
-    };
-    const auto place_values = [&](auto change) {
+        // ---- the cache
+        const auto token0 = [&](int c) { return (c < na ? c : c - na + b0) << 5; };
+        // Pages of a block's two halves, as the table has them (places past its end:
+        // its last entry; a block past the part's last: the last's), and those that
+        // are the cache's, or -1.  Scalar loads: a wave's wait for them does not wait for the cache's.
+        struct Two {
+            int p[2];
+        };
+        const Scalars table = (Scalars)(uintptr_t)(a.pages.table + (size_t)b * a.pages.ld);
+        const auto near = [&](int c) { return max(min(c, c_end - 1), 0); };
+        const auto entries = [&](int c) {
+            const int t = token0(near(c));
+            return Two{{table[min(t >> a.pages.shift, a.pages.ld - 1)], table[min((t + 16) >> a.pages.shift, a.pages.ld - 1)]}};
+        };
+        const auto pages_at = [&](int c, Two e) {
+            const int t = token0(near(c));
+            return Two{{t < L && (uint32_t)e.p[0] < (uint32_t)a.pages.pages ? e.p[0] : -1,
+                        t + 16 < L && (uint32_t)e.p[1] < (uint32_t)a.pages.pages ? e.p[1] : -1}};
+        };
+        const int mask = (1 << a.pages.shift) - 1;
+        // A load's address is a block's, which is scalar, and an offset that is the
+        // lane's.  Scale codes come as the aligned word that holds a row's (with D 64 two rows').
+        constexpr int RC = D * BITS / 8, RS = D / 32;          // bytes of a row's codes and scale codes
+        const auto scale_in = [](uint32_t word, int row, int group) {
+            return scale_of(word >> (8 * (D == 128 ? group : 2 * (row & 1) + group)) & 0xff);
+        };
+        const uint32_t key_at = r16 * RC + g * (Tok::KW * 4), key_scale_at = r16 * RS & ~3;
+        const uint32_t value_at = lane / LPR * RC + lane % LPR * (Tok::VW * 4), value_scale_at = lane / LPR * RS & ~3;
+        Tok x;
+        const auto row_of = [&](int c, Two pg, int h) {        // the cache's row of a half's first token (in page 0 where there is none)
+            return (((long long)max(pg.p[h], 0) * a.pages.heads + head) << a.pages.shift) + ((token0(near(c)) + 16 * h) & mask);
+        };
+        const auto load_keys = [&](int c, Two pg) {
 #pragma unroll
-        for (int i = 0; i < Tok::VP; ++i) {
-            const int tok = (64 / LPR) * i + lane / LPR, c16 = lane % LPR;
-            const float scale = scale_in(x.vs[i], tok, c16 / 2);
-            uint4* to = (uint4*)(mine + place_v(tok, c16));
-            to[0] = __builtin_bit_cast(uint4, change(decode8<BITS>(x.v[i], scale)));
-            to[1] = __builtin_bit_cast(uint4, change(decode8<BITS>(x.v[i] + BITS / 4, scale)));
-        }
-    };
-    const auto read_v = [&](int cb) {                      // V^T: channels 16 cb + lane % 16, tokens 4 g .. and 16 + 4 g ..
-        const int tok = 4 * g + (r16 >> 2), in = (r16 & 3) * 8;
-        const uint8_t* from = mine + ((place_v(tok, 0) + in) ^ (cb << 5));
-        const v4s p = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)from);
-        const v4s q = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(from + 32 * D));   // (16 tokens on)
-        typedef short v8s __attribute__((ext_vector_type(8)));
-        return __builtin_bit_cast(v8bf, v8s{p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]});
-    };
-
-    const int c_first = one(work.c0) + w;
-    Two pg = pages_at(c_first, entries(c_first)), later = entries(c_first + 4);
-    load_keys(c_first, pg);
-    load_values(c_first, pg);
-
-    // ---- q as the second operand: lane (row, g), channels (D / 4) g + 8 j ..
-    v8bf q[RB][QP][NJ];
-#pragma unroll
-    for (int i = 0; i < RB; ++i) {
-        const uint32_t r = min(r0 + 16 * i + r16, rows - 1), n = r / (uint32_t)a.G;
-        const T* p = (const T*)a.q + (long long)(f0 + n) * a.ldq + (head * a.G + (int)(r - n * a.G)) * D + (D / 4) * g;
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            if constexpr (F32) {
-                float v[8];
-                Stream<float>::load(p + 8 * j, v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const __bf16 h = (__bf16)v[e];
-                    const float rest = v[e] - (float)h;
-                    const __bf16 m = (__bf16)rest;
-                    q[i][0][j][e] = h;
-                    q[i][1][j][e] = m;
-                    q[i][2][j][e] = (__bf16)(rest - (float)m);
-                }
-                // (an infinite value has no rest)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if ((__float_as_uint(v[e]) & 0x7f800000u) == 0x7f800000u || fabsf((float)q[i][0][j][e]) > 3.4e38f) {
-                        q[i][1][j][e] = (__bf16)0.0f;
-                        q[i][2][j][e] = (__bf16)0.0f;
-                    }
-            } else {
-                q[i][0][j] = __builtin_bit_cast(v8bf, get16(p + 8 * j));
+            for (int h = 0; h < 2; ++h) {
+                const long long row = row_of(c, pg, h);
+                load_words<Tok::KW>(scalar(a.codes[0] + row * RC) + key_at, x.k[h]);
+                x.ks[h] = *(const __attribute__((address_space(1))) uint32_t*)(scalar(a.scales[0] + row * RS) + key_scale_at);
             }
+        };
+        const auto load_values = [&](int c, Two pg) {
+#pragma unroll
+            for (int i = 0; i < Tok::VP; ++i) {                // piece i: token (64 / LPR) i + lane / LPR
+                const long long row = row_of(c, pg, (64 / LPR) * i < 16 ? 0 : 1) + (64 / LPR) * i % 16;
+                load_words<Tok::VW>(scalar(a.codes[1] + row * RC) + value_at, x.v[i]);
+                x.vs[i] = *(const __attribute__((address_space(1))) uint32_t*)(scalar(a.scales[1] + row * RS) + value_scale_at);
+            }
+        };
+
+        v4f acc[RB][CB];
+        float m[RB], l[RB];
+        uint32_t nan[RB] = {};                                 // the sums that are NaN by what the masked blocks hold
+        uint32_t seen = 0;                                     // row blocks whose row (of this lane) saw a token
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+            m[i] = -INFINITY, l[i] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < CB; ++c) acc[i][c] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
         }
-    }
 
-    int lo[RB], hi[RB];
+        // V [32][D] bf16: 32 bytes (16 channels) of a token at slot c16 ^ its own, so
+        // that the transposing reads' 8 rows of 32 bytes meet 64 banks
+        uint8_t* const mine = lds[w];                          // (64 D bytes: the slots' exclusive or stays inside)
+        const auto place_v = [&](int tok, int c16) {
+            const int s = D == 128 ? tok & 7 : (tok >> 1) & 3;
+            return tok * (2 * D) + ((c16 ^ s) << 5);
+        };
+        const auto place_values = [&](auto change) {
 #pragma unroll
-    for (int i = 0; i < RB; ++i) sees(min(r0 + 16 * i + r16, rows - 1), &lo[i], &hi[i]);
+            for (int i = 0; i < Tok::VP; ++i) {
+                const int tok = (64 / LPR) * i + lane / LPR, c16 = lane % LPR;
+                const float scale = scale_in(x.vs[i], tok, c16 / 2);
+                uint4* to = (uint4*)(mine + place_v(tok, c16));
+                to[0] = __builtin_bit_cast(uint4, change(decode8<BITS>(x.v[i], scale)));
+                to[1] = __builtin_bit_cast(uint4, change(decode8<BITS>(x.v[i] + BITS / 4, scale)));
+            }
+        };
+        const auto read_v = [&](int cb) {                      // V^T: channels 16 cb + lane % 16, tokens 4 g .. and 16 + 4 g ..
+            const int tok = 4 * g + (r16 >> 2), in = (r16 & 3) * 8;
+            const uint8_t* from = mine + ((place_v(tok, 0) + in) ^ (cb << 5));
+            const v4s p = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)from);
+            const v4s q = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(from + 32 * D));   // (16 tokens on)
+            typedef short v8s __attribute__((ext_vector_type(8)));
+            return __builtin_bit_cast(v8bf, v8s{p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]});
+        };
 
-    for (int c = c_first; c < c_end;) {
-        // (The next block's keys are loaded as soon as this one's are used, its
-        // values too: no registers for two blocks.  Past the last block the last
-        // is loaded again: with a branch there the waits, which count loads,
-        // would have to assume that there were none.)
-        const Two here = pg;
-        pg = pages_at(c + 4, later);
-        later = entries(c + 8);
-        const int t = token0(c);
-        // ---- scores
-        v4f s[RB][2];
+        const int c_first = one(work.c0) + w;
+        Two pg = pages_at(c_first, entries(c_first)), later = entries(c_first + 4);
+        load_keys(c_first, pg);
+        load_values(c_first, pg);
+
+        // ---- q as the second operand: lane (row, g), channels (D / 4) g + 8 j ..
+        v8bf q[RB][QP][NJ];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float scale = scale_in(x.ks[h], r16, D / 4 * g / 32);
-#pragma unroll
-            for (int i = 0; i < RB; ++i) s[i][h] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < RB; ++i) {
+            const uint32_t r = min(r0 + 16 * i + r16, rows - 1), n = r / (uint32_t)a.G;
+            const T* p = (const T*)a.q + (long long)(f0 + n) * a.ldq + (head * a.G + (int)(r - n * a.G)) * D + (D / 4) * g;
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
-                const v8bf k = decode8<BITS>(x.k[h] + j * (BITS / 4), scale);
+                if constexpr (F32) {
+                    float v[8];
+                    Stream<float>::load(p + 8 * j, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const __bf16 h = (__bf16)v[e];
+                        const float rest = v[e] - (float)h;
+                        const __bf16 m = (__bf16)rest;
+                        q[i][0][j][e] = h;
+                        q[i][1][j][e] = m;
+                        q[i][2][j][e] = (__bf16)(rest - (float)m);
+                    }
+                    // (an infinite value has no rest)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if ((__float_as_uint(v[e]) & 0x7f800000u) == 0x7f800000u || fabsf((float)q[i][0][j][e]) > 3.4e38f) {
+                            q[i][1][j][e] = (__bf16)0.0f;
+                            q[i][2][j][e] = (__bf16)0.0f;
+                        }
+                } else {
+                    q[i][0][j] = __builtin_bit_cast(v8bf, get16(p + 8 * j));
+                }
+            }
+        }
+
+        int lo[RB], hi[RB];
+#pragma unroll
+        for (int i = 0; i < RB; ++i) sees(min(r0 + 16 * i + r16, rows - 1), &lo[i], &hi[i]);
+
+        for (int c = c_first; c < c_end;) {
+            // (The next block's keys are loaded as soon as this one's are used, its
+            // values too: no registers for two blocks.  Past the last block the last
+            // is loaded again: with a branch there the waits, which count loads,
+            // would have to assume that there were none.)
+            const Two here = pg;
+            pg = pages_at(c + 4, later);
+            later = entries(c + 8);
+            const int t = token0(c);
+            // ---- scores
+            v4f s[RB][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float scale = scale_in(x.ks[h], r16, D / 4 * g / 32);
+#pragma unroll
+                for (int i = 0; i < RB; ++i) s[i][h] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    const v8bf k = decode8<BITS>(x.k[h] + j * (BITS / 4), scale);
+#pragma unroll
+                    for (int i = 0; i < RB; ++i)
+#pragma unroll
+                        for (int p = QP - 1; p >= 0; --p) s[i][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[i][p][j], s[i][h], 0, 0, 0);
+                }
+            }
+            load_keys(c + 4, pg);
+            // ---- values into LDS
+            const bool all = here.p[0] >= 0 && here.p[1] >= 0 && ((t >= lo1 && t + 32 <= hi0) || t + 32 <= pf);   // every row sees every token
+            // (a value that is not finite would reach rows that do not see it, times 0)
+            const bool odd = !all && __ballot(x.not_finite()) != 0;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (!odd) place_values([](v8bf v) { return v; });
+            else place_values([](v8bf v) { return not_finite_of<false>(v); });
+            load_values(c + 4, pg);
+            // ---- weights
+            v8bf pw[RB][PP];
+            uint32_t vis[RB];
+            float grown[RB];                                   // what the sums so far are worth by the new maximum
+            const auto weigh = [&](auto masked) {
+#pragma unroll
+                for (int i = 0; i < RB; ++i) {
+                    float e[8];
+                    vis[i] = 0xff;
+                    if constexpr (decltype(masked)::value) {
+                        vis[i] = 0;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int tok = t + 16 * (j >> 2) + 4 * g + (j & 3);
+                            const bool on = ((tok >= lo[i] && tok < hi[i]) || tok < pf) && here.p[j >> 2] >= 0;
+                            vis[i] |= on ? 1u << j : 0u;
+                        }
+                    }
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) e[j] = s[i][j >> 2][j & 3];
+                    if (a.cap > 0.0f) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) e[j] = a.cap * LOG2E * tanh_of(e[j] * a.cap_in);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        if constexpr (decltype(masked)::value) e[j] = vis[i] >> j & 1 ? e[j] : -INFINITY;
+                        top = fmaxf(top, e[j]);
+                    }
+                    if (vis[i]) seen |= 1u << i;
+                    top = max_rows(top) * a.scale;             // (1 with a cap)
+                    const float mn = fmaxf(m[i], top);
+                    grown[i] = mn == m[i] ? 1.0f : power(m[i] - mn);   // (also where both are infinite, whose sums are NaN by the weights)
+                    m[i] = mn;
+                    l[i] *= grown[i];
+                    const float at = m[i] == -INFINITY ? 0.0f : m[i];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float p = power(__builtin_fmaf(e[j], a.scale, -at));
+                        const __bf16 h = (__bf16)p;
+                        pw[i][0][j] = h;
+                        if constexpr (PP == 2) {
+                            pw[i][1][j] = (__bf16)(p - (float)h);
+                            l[i] += p;
+                        } else {
+                            l[i] += (float)h;
+                        }
+                    }
+                }
+            };
+            if (all) weigh(std::false_type{});
+            else weigh(std::true_type{});
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+                if (__ballot(grown[i] != 1.0f)) {
+#pragma unroll
+                    for (int cb = 0; cb < CB; ++cb) acc[i][cb] *= grown[i];
+                }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            // ---- O^T += V^T P^T
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb) {
+                const v8bf v = read_v(cb);
 #pragma unroll
                 for (int i = 0; i < RB; ++i)
 #pragma unroll
-                    for (int p = QP - 1; p >= 0; --p) s[i][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[i][p][j], s[i][h], 0, 0, 0);
+                    for (int p = PP - 1; p >= 0; --p) acc[i][cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pw[i][p], acc[i][cb], 0, 0, 0);
             }
-        }
-        load_keys(c + 4, pg);
-        // ---- values into LDS
-        const bool all = here.p[0] >= 0 && here.p[1] >= 0 && ((t >= lo1 && t + 32 <= hi0) || t + 32 <= pf);   // every row sees every token
-        // (a value that is not finite would reach rows that do not see it, times 0)
-        const bool odd = !all && __ballot(x.not_finite()) != 0;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (!odd) place_values([](v8bf v) { return v; });
-        else place_values([](v8bf v) { return not_finite_of<false>(v); });
-        load_values(c + 4, pg);
-        // ---- weights
-        v8bf pw[RB][PP];
-        uint32_t vis[RB];
-        float grown[RB];                                   // what the sums so far are worth by the new maximum
-        const auto weigh = [&](auto masked) {
+            if (odd) {
+                // the rows that do see a value that is not finite: counted as ones times ones
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                load_values(c, here);
+                place_values([](v8bf v) { return not_finite_of<true>(v); });
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-            for (int i = 0; i < RB; ++i) {
-                float e[8];
-                vis[i] = 0xff;
-                if constexpr (decltype(masked)::value) {
-                    vis[i] = 0;
+                for (int i = 0; i < RB; ++i) {
+                    v8bf on;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int tok = t + 16 * (j >> 2) + 4 * g + (j & 3);
-                        const bool on = ((tok >= lo[i] && tok < hi[i]) || tok < pf) && here.p[j >> 2] >= 0;
-                        vis[i] |= on ? 1u << j : 0u;
+                    for (int j = 0; j < 8; ++j) on[j] = (__bf16)(vis[i] >> j & 1 ? 1.0f : 0.0f);
+#pragma unroll
+                    for (int cb = 0; cb < CB; ++cb) {
+                        const v4f n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(read_v(cb), on, v4f{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) nan[i] |= __float_as_uint(n[e]) ? 1u << (4 * cb + e) : 0u;
                     }
                 }
-                float top = -INFINITY;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) e[j] = s[i][j >> 2][j & 3];
-                if (a.cap > 0.0f) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) e[j] = a.cap * LOG2E * tanh_of(e[j] * a.cap_in);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if constexpr (decltype(masked)::value) e[j] = vis[i] >> j & 1 ? e[j] : -INFINITY;
-                    top = fmaxf(top, e[j]);
-                }
-                if (vis[i]) seen |= 1u << i;
-                top = max_rows(top) * a.scale;             // (1 with a cap)
-                const float mn = fmaxf(m[i], top);
-                grown[i] = mn == m[i] ? 1.0f : power(m[i] - mn);   // (also where both are infinite, whose sums are NaN by the weights)
-                m[i] = mn;
-                l[i] *= grown[i];
-                const float at = m[i] == -INFINITY ? 0.0f : m[i];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float p = power(__builtin_fmaf(e[j], a.scale, -at));
-                    const __bf16 h = (__bf16)p;
-                    pw[i][0][j] = h;
-                    if constexpr (PP == 2) {
-                        pw[i][1][j] = (__bf16)(p - (float)h);
-                        l[i] += p;
-                    } else {
-                        l[i] += (float)h;
-                    }
-                }
+                load_values(c + 4, pg);
             }
-        };
-        if (all) weigh(std::false_type{});
-        else weigh(std::true_type{});
-#pragma unroll
-        for (int i = 0; i < RB; ++i)
-            if (__ballot(grown[i] != 1.0f)) {
-#pragma unroll
-                for (int cb = 0; cb < CB; ++cb) acc[i][cb] *= grown[i];
-            }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        // ---- O^T += V^T P^T
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb) {
-            const v8bf v = read_v(cb);
-#pragma unroll
-            for (int i = 0; i < RB; ++i)
-#pragma unroll
-                for (int p = PP - 1; p >= 0; --p) acc[i][cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pw[i][p], acc[i][cb], 0, 0, 0);
+            c += 4;
         }
-        if (odd) {
-            // the rows that do see a value that is not finite: counted as ones times ones
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            load_values(c, here);
-            place_values([](v8bf v) { return not_finite_of<true>(v); });
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-            for (int i = 0; i < RB; ++i) {
-                v8bf on;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) on[j] = (__bf16)(vis[i] >> j & 1 ? 1.0f : 0.0f);
-#pragma unroll
-                for (int cb = 0; cb < CB; ++cb) {
-                    const v4f n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(read_v(cb), on, v4f{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) nan[i] |= __float_as_uint(n[e]) ? 1u << (4 * cb + e) : 0u;
-                }
-            }
-            load_values(c + 4, pg);
-        }
-        c += 4;
-    }
 
-    // ---- the four waves' sums, a block of rows at a time: thread (row, its D / 16 channels)
+        // ---- the four waves' sums, a block of rows at a time: thread (row, its D / 16 channels)
 #pragma unroll
-    for (int i = 0; i < RB; ++i) {
-        const float sum = sum_rows(l[i]);
-        const uint64_t s = __ballot(seen >> i & 1);
-        const bool any = ((s | s >> 16 | s >> 32 | s >> 48) >> r16) & 1;
-        if (g == 0) {
-            stat[w][0][16 * i + r16] = m[i];
-            stat[w][1][16 * i + r16] = sum;
-            stat[w][2][16 * i + r16] = any ? 1.0f : 0.0f;
+        for (int i = 0; i < RB; ++i) {
+            const float sum = sum_rows(l[i]);
+            const uint64_t s = __ballot(seen >> i & 1);
+            const bool any = ((s | s >> 16 | s >> 32 | s >> 48) >> r16) & 1;
+            if (g == 0) {
+                stat[w][0][16 * i + r16] = m[i];
+                stat[w][1][16 * i + r16] = sum;
+                stat[w][2][16 * i + r16] = any ? 1.0f : 0.0f;
+            }
         }
-    }
-    constexpr int CT = D / 16, Q4 = CT / 4;                // channels of a thread, in pieces of 4
-    const int row = tid >> 4, ch = (tid & 15) * CT;
-    const size_t unit = ((size_t)head * (a.shares + a.most) + work.slot) * RB;
-    const auto finish = [&](int i, const v4f* o, float sum, bool any) {
-        const uint32_t r = r0 + 16 * i + row, n = r / (uint32_t)a.G;
-        if ((int)r >= rows) return;
-        T* y = (T*)a.y + (long long)(f0 + n) * a.ldy + (head * a.G + (int)(r - n * a.G)) * D + ch;
+        constexpr int CT = D / 16, Q4 = CT / 4;                // channels of a thread, in pieces of 4
+        const int row = tid >> 4, ch = (tid & 15) * CT;
+        const size_t unit = ((size_t)head * (a.shares + a.most) + work.slot) * RB;
+        const auto finish = [&](int i, const v4f* o, float sum, bool any) {
+            const uint32_t r = r0 + 16 * i + row, n = r / (uint32_t)a.G;
+            if ((int)r >= rows) return;
+            T* y = (T*)a.y + (long long)(f0 + n) * a.ldy + (head * a.G + (int)(r - n * a.G)) * D + ch;
 #pragma unroll
-        for (int p = 0; p < Q4; ++p) store4(y + 4 * p, o[p], sum, any);
-    };
-    // (16-byte piece c of a row lies at c ^ row, so the lanes' stores and loads meet all banks)
+            for (int p = 0; p < Q4; ++p) store4(y + 4 * p, o[p], sum, any);
+        };
+        // (16-byte piece c of a row lies at c ^ row, so the lanes' stores and loads meet all banks)
 #pragma unroll
-    for (int i = 0; i < RB; ++i) {
-        __syncthreads();
-        v4f* o = (v4f*)mine;
+        for (int i = 0; i < RB; ++i) {
+            __syncthreads();
+            v4f* o = (v4f*)mine;
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) {
+            for (int cb = 0; cb < CB; ++cb) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][cb][e] = nan[i] >> (4 * cb + e) & 1 ? __builtin_nanf("") : acc[i][cb][e];
-            o[r16 * (D / 4) + ((4 * cb + g) ^ r16)] = acc[i][cb];
+                for (int e = 0; e < 4; ++e) acc[i][cb][e] = nan[i] >> (4 * cb + e) & 1 ? __builtin_nanf("") : acc[i][cb][e];
+                o[r16 * (D / 4) + ((4 * cb + g) ^ r16)] = acc[i][cb];
+            }
+            __syncthreads();
+            float top = -INFINITY, sum = 0.0f, any = 0.0f;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) top = fmaxf(top, stat[p][0][16 * i + row]);
+            v4f out[Q4];
+#pragma unroll
+            for (int p = 0; p < Q4; ++p) out[p] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const float mp = stat[p][0][16 * i + row], f = mp == -INFINITY ? 1.0f : power(mp - top);
+                sum += f * stat[p][1][16 * i + row];
+                any = fmaxf(any, stat[p][2][16 * i + row]);
+                const v4f* from = (const v4f*)lds[p] + row * (D / 4);
+#pragma unroll
+                for (int j = 0; j < Q4; ++j) out[j] += f * from[((ch >> 2) + j) ^ row];
+            }
+            if (used == 1) {
+                finish(i, out, sum, any > 0.0f);
+            } else {
+                if (r0 + 16 * i + row >= rows) continue;
+#pragma unroll
+                for (int j = 0; j < Q4; ++j) *(v4f*)(a.sums + ((unit + i) * 16 + row) * D + ch + 4 * j) = out[j];
+                if ((tid & 15) == 0) *(v4f*)(a.stats + ((unit + i) * 16 + row) * 4) = v4f{top, sum, any, 0.0f};
+            }
         }
-        __syncthreads();
-        float top = -INFINITY, sum = 0.0f, any = 0.0f;
-#pragma unroll
-        for (int p = 0; p < 4; ++p) top = fmaxf(top, stat[p][0][16 * i + row]);
-        v4f out[Q4];
-#pragma unroll
-        for (int p = 0; p < Q4; ++p) out[p] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const float mp = stat[p][0][16 * i + row], f = mp == -INFINITY ? 1.0f : power(mp - top);
-            sum += f * stat[p][1][16 * i + row];
-            any = fmaxf(any, stat[p][2][16 * i + row]);
-            const v4f* from = (const v4f*)lds[p] + row * (D / 4);
-#pragma unroll
-            for (int j = 0; j < Q4; ++j) out[j] += f * from[((ch >> 2) + j) ^ row];
-        }
-        if (used == 1) {
-            finish(i, out, sum, any > 0.0f);
-        } else {
-            if (r0 + 16 * i + row >= rows) continue;
-#pragma unroll
-            for (int j = 0; j < Q4; ++j) *(v4f*)(a.sums + ((unit + i) * 16 + row) * D + ch + 4 * j) = out[j];
-            if ((tid & 15) == 0) *(v4f*)(a.stats + ((unit + i) * 16 + row) * 4) = v4f{top, sum, any, 0.0f};
-        }
-    }
-    if (!a.shares) return;
-    __syncthreads();                                       // (the sums in LDS are read)
+        if (!a.shares) return;
+        __syncthreads();                                       // (the sums in LDS are read)
     }
 }
 
@@ -674,52 +678,52 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     const TileInfo info = a.tiles[(size_t)head * a.most + blockIdx.x / by];
     if (info.used < 2) return;
     for (int row = first + (threadIdx.x >> 6); row < min(info.rows, first + 16 / a.join); row += 4) {
-    const size_t unit = ((size_t)head * (a.shares + a.most) + info.slot) * RB + (row >> 4), step = RB;
-    const auto at = [&](int p) { return (unit + p * step) * 16 + (row & 15); };
-    // 64 parts at a time, a lane holding one's statistics, with the maximum and the sums so far rescaled
-    float top = -INFINITY, sum = 0.0f, any = 0.0f;
-    v4f out{0.0f, 0.0f, 0.0f, 0.0f};
-    const int sub = lane / LP, ch = 4 * (lane % LP);
-    for (int p64 = 0; p64 < info.used; p64 += 64) {
-        const int n = min(info.used - p64, 64);
-        v4f from[U];
-        const auto fetch = [&](int p0) {
+        const size_t unit = ((size_t)head * (a.shares + a.most) + info.slot) * RB + (row >> 4), step = RB;
+        const auto at = [&](int p) { return (unit + p * step) * 16 + (row & 15); };
+        // 64 parts at a time, a lane holding one's statistics, with the maximum and the sums so far rescaled
+        float top = -INFINITY, sum = 0.0f, any = 0.0f;
+        v4f out{0.0f, 0.0f, 0.0f, 0.0f};
+        const int sub = lane / LP, ch = 4 * (lane % LP);
+        for (int p64 = 0; p64 < info.used; p64 += 64) {
+            const int n = min(info.used - p64, 64);
+            v4f from[U];
+            const auto fetch = [&](int p0) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) from[u] = *(const v4f*)(a.sums + at(p64 + min(p0 + u * PL + sub, n - 1)) * D + ch);
-        };
-        const v4f st = *(const v4f*)(a.stats + at(p64 + min(lane, n - 1)) * 4);
-        fetch(0);
-        float m = st[0];
+                for (int u = 0; u < U; ++u) from[u] = *(const v4f*)(a.sums + at(p64 + min(p0 + u * PL + sub, n - 1)) * D + ch);
+            };
+            const v4f st = *(const v4f*)(a.stats + at(p64 + min(lane, n - 1)) * 4);
+            fetch(0);
+            float m = st[0];
 #pragma unroll
-        for (int s = 1; s < 64; s *= 2) m = fmaxf(m, __shfl_xor(m, s, 64));
-        m = fmaxf(m, top);
-        const float old = m == -INFINITY ? 1.0f : power(top - m);
-        const float f = lane >= n ? 0.0f : st[0] == -INFINITY ? 1.0f : power(st[0] - m);
-        top = m;
-        float more = lane < n ? f * st[1] : 0.0f;
+            for (int s = 1; s < 64; s *= 2) m = fmaxf(m, __shfl_xor(m, s, 64));
+            m = fmaxf(m, top);
+            const float old = m == -INFINITY ? 1.0f : power(top - m);
+            const float f = lane >= n ? 0.0f : st[0] == -INFINITY ? 1.0f : power(st[0] - m);
+            top = m;
+            float more = lane < n ? f * st[1] : 0.0f;
 #pragma unroll
-        for (int s = 1; s < 64; s *= 2) more += __shfl_xor(more, s, 64);
-        sum = sum * old + more;
-        any = fmaxf(any, __ballot(st[2] > 0.0f) ? 1.0f : 0.0f);
-        out *= old;
-        for (int p0 = 0; p0 < n; p0 += U * PL) {
-            if (p0) fetch(p0);
+            for (int s = 1; s < 64; s *= 2) more += __shfl_xor(more, s, 64);
+            sum = sum * old + more;
+            any = fmaxf(any, __ballot(st[2] > 0.0f) ? 1.0f : 0.0f);
+            out *= old;
+            for (int p0 = 0; p0 < n; p0 += U * PL) {
+                if (p0) fetch(p0);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int p = p0 + u * PL + sub;
-                const float wt = __shfl(f, p & 63, 64);
+                for (int u = 0; u < U; ++u) {
+                    const int p = p0 + u * PL + sub;
+                    const float wt = __shfl(f, p & 63, 64);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) out[e] = p < n ? out[e] + wt * from[u][e] : out[e];
+                    for (int e = 0; e < 4; ++e) out[e] = p < n ? out[e] + wt * from[u][e] : out[e];
+                }
             }
         }
-    }
 #pragma unroll
-    for (int s = LP; s < 64; s *= 2)
+        for (int s = LP; s < 64; s *= 2)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) out[e] += __shfl_xor(out[e], s, 64);
-    if (lane >= LP) continue;
-    const uint32_t r = info.r0 + row, n = r / (uint32_t)a.G;
-    store4((T*)a.y + (long long)(info.f0 + n) * a.ldy + (head * a.G + (int)(r - n * a.G)) * D + ch, out, sum, any > 0.0f);
+            for (int e = 0; e < 4; ++e) out[e] += __shfl_xor(out[e], s, 64);
+        if (lane >= LP) continue;
+        const uint32_t r = info.r0 + row, n = r / (uint32_t)a.G;
+        store4((T*)a.y + (long long)(info.f0 + n) * a.ldy + (head * a.G + (int)(r - n * a.G)) * D + ch, out, sum, any > 0.0f);
     }
 }
 
@@ -741,8 +745,8 @@ hipError_t launch_attn(AttnArgs a, int kv_heads, hipStream_t st) {
         return e;
     }
     a.most = (int)tiles;
-    a.shares = a.pages.seqs <= 64 && blocks > LEAST_SHARE && tiles < full && (full + tiles) * kv_heads <= MAX_SLOTS && tiles * (blocks + 16) < 1ll << 30
-                   ? (int)full : 0;
+    const bool fits = (full + tiles) * kv_heads <= MAX_SLOTS && tiles * (blocks + 16) < 1ll << 30;
+    a.shares = a.pages.seqs <= 64 && blocks > LEAST_SHARE && tiles < full && fits ? (int)full : 0;
     const hipError_t e = launch(k_attn<T, BITS, D, RB>, dim3((unsigned)(a.shares ? a.shares : tiles), kv_heads), 256u, st, a);
     if (e != hipSuccess || !a.shares) return e;
     // (a wave to a row while that makes no more workgroups than the card holds at once: 1 x 4096 14.0 -> 12.3 us; else
@@ -809,9 +813,9 @@ dq_status dq_attn_rows(const dq_kv* kv, const dq_seqs* seqs, int64_t N, const vo
         return fail(DQ_ERR_SHAPE, "q_heads must be a multiple of the cache's heads with q_heads * head_dim <= 32768");
     if (N * (q_heads / kv->heads) > 1 << 27) return fail(DQ_ERR_SHAPE, "N * q_heads / heads must be at most 2^27");
     if (!ops || !a) return fail(DQ_ERR_INVALID_ARG, "ops or workspace is NULL");
-    const double most = 18446744073709551616.0;            // 2^64
-    if (!(ops->scale > 0.0) || !(ops->scale <= most)) return fail(DQ_ERR_INVALID_ARG, "scale must be in (0, 2^64]");
-    if (ops->cap != 0.0 && !(ops->cap >= 1.0 / most && ops->cap <= most)) return fail(DQ_ERR_INVALID_ARG, "cap must be 0 or in [2^-64, 2^64]");
+    const double most = 4294967296.0;                      // 2^32: the factors of the scores stay in fp32's range
+    if (!(ops->scale >= 1.0 / most) || !(ops->scale <= most)) return fail(DQ_ERR_INVALID_ARG, "scale must be in [2^-32, 2^32]");
+    if (ops->cap != 0.0 && !(ops->cap >= 1.0 / most && ops->cap <= most)) return fail(DQ_ERR_INVALID_ARG, "cap must be 0 or in [2^-32, 2^32]");
     if (ops->block < 0 || ops->block >= int64_t(1) << 31 || ops->window < 0 || ops->window >= int64_t(1) << 31)
         return fail(DQ_ERR_SHAPE, "block and window must be in [0, 2^31)");
     if (ops->block == 0 && ops->window != 0) return fail(DQ_ERR_INVALID_ARG, "a window needs a block of 1 or more");

@@ -577,7 +577,8 @@ dq_status check_kv(const dq_kv* kv) {
     if (kv->page_tokens < 16 || kv->page_tokens > 65536 || (kv->page_tokens & (kv->page_tokens - 1)))
         return fail(DQ_ERR_SHAPE, "page_tokens must be a power of two in [16, 65536]");
     if (kv->pages < 1 || kv->pages >= int64_t(1) << 31) return fail(DQ_ERR_SHAPE, "pages must be in [1, 2^31)");
-    if (kv->pages > (int64_t(1) << 44) / ((int64_t)kv->heads * kv->page_tokens * kv->head_dim)) return fail(DQ_ERR_SHAPE, "the cache is larger than 2^44 values");
+    if (kv->pages > (int64_t(1) << 44) / ((int64_t)kv->heads * kv->page_tokens * kv->head_dim))
+        return fail(DQ_ERR_SHAPE, "the cache is larger than 2^44 values");
     if (!kv->k_codes || !kv->k_scales || !kv->v_codes || !kv->v_scales) return fail(DQ_ERR_INVALID_ARG, "a cache array is NULL");
     if (((uintptr_t)kv->k_codes | (uintptr_t)kv->v_codes) % 16 != 0) return fail(DQ_ERR_INVALID_ARG, "the cache's codes must be 16-byte aligned");
     if (((uintptr_t)kv->k_scales | (uintptr_t)kv->v_scales) % 4 != 0) return fail(DQ_ERR_INVALID_ARG, "the cache's scales must be 4-byte aligned");
