@@ -82,29 +82,26 @@ __device__ __forceinline__ long long token_row(const Pages& p, Place at, int hea
     return (((long long)at.page * p.heads + head) << p.shift) + (at.t & ((1 << p.shift) - 1));
 }
 
-
-
 // A scale code as the converters take it: 2^(e - 127), NaN for 255.
 __device__ __forceinline__ float scale_of(uint32_t e) { return __uint_as_float(e == 255 ? 0x7fc00000u : max(e << 23, 0x00400000u)); }
 
-// The fp32 values of 16 codes under one scale code.
+// The fp32 values of 8 codes (two words of E4M3, one of E2M1) under one scale code.
 template <int BITS>
-__device__ __forceinline__ void decode16(const uint32_t* code, uint32_t e, float* v) {
+__device__ __forceinline__ void decode8_f32(const uint32_t* code, uint32_t e, float* v) {
     const float scale = scale_of(e);
+    if constexpr (BITS == 8) {
 #pragma unroll
-    for (int i = 0; i < (BITS == 8 ? 4 : 2); ++i) {
-        if constexpr (BITS == 8) {
+        for (int i = 0; i < 2; ++i) {
             const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(code[i], scale, false);
             const v2f b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(code[i], scale, true);
             v[4 * i] = a[0], v[4 * i + 1] = a[1], v[4 * i + 2] = b[0], v[4 * i + 3] = b[1];
-        } else {
-            const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[i], scale, 0);
-            const v2f b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[i], scale, 1);
-            const v2f c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[i], scale, 2);
-            const v2f d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[i], scale, 3);
-            v[8 * i] = a[0], v[8 * i + 1] = a[1], v[8 * i + 2] = b[0], v[8 * i + 3] = b[1];
-            v[8 * i + 4] = c[0], v[8 * i + 5] = c[1], v[8 * i + 6] = d[0], v[8 * i + 7] = d[1];
         }
+    } else {
+        const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[0], scale, 0);
+        const v2f b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[0], scale, 1);
+        const v2f c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[0], scale, 2);
+        const v2f d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[0], scale, 3);
+        v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1], v[4] = c[0], v[5] = c[1], v[6] = d[0], v[7] = d[1];
     }
 }
 

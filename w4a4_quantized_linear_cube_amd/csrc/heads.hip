@@ -51,7 +51,7 @@ struct HeadsArgs {
     double eps;
     int lph;                // lanes (chunks) to a head
     int tpr;                // threads to a row, a power of two
-    int g_bf16, nt;
+    int g_bf16;
 };
 
 // Sums over groups of n neighbouring lanes (n a power of two, 4 to 64), pairwise by the lanes' bits, lowest first.
@@ -198,6 +198,8 @@ __device__ __forceinline__ void load_gains(const HeadsArgs& a, const Part& p, in
     else Stream<float>::load((const float*)p.g + at, g);
 }
 
+// What bounds it: HBM where there are many rows (32760 x 12 heads 48 us, 4.2 TB/s; 75600 x 40 fp32 heads 394, 5.9 TB/s);
+// launch and a chain of three loads where there are few (1 x 40 heads 3.5 us).
 // A row's part is held in registers by tpr threads (of several blocks, where no
 // sum crosses them), CH chunks of 8 channels each, chunk i of thread t: i tpr + t.
 // tpr is a multiple of the lanes to a head, so a thread's chunks are at one place
@@ -210,7 +212,7 @@ __global__ __launch_bounds__(1024) void k_heads(HeadsArgs a) {
     __shared__ double sums[64];                     // [row of the block][block of 64 chunks]
     // (the arguments' cache lines, all at once)
     asm volatile("" ::"s"(a.part[0].nch), "s"(a.part[1].ldy), "s"(a.part[2].g), "s"(a.part[2].turn), "s"(a.turn.table[1]), "s"(a.pages.first),
-                 "s"(a.N), "s"(a.nt));
+                 "s"(a.N), "s"(a.g_bf16));
     int seg = blockIdx.y, pi = 0;
     if (seg >= a.part[0].segs) {
         seg -= a.part[0].segs, pi = 1;
@@ -323,12 +325,10 @@ __global__ __launch_bounds__(1024) void k_heads(HeadsArgs a) {
             if (c >= p.nch) continue;
             if (p.kind == TO_BF16) {
                 uint16_t* y = (uint16_t*)p.y + row * p.ldy + 8 * c;
-                if (a.nt) Stream<uint16_t>::template store<true>(y, v[i]);
-                else Stream<uint16_t>::template store<false>(y, v[i]);
+                Stream<uint16_t>::template store<false>(y, v[i]);
             } else {
                 float* y = (float*)p.y + row * p.ldy + 8 * c;
-                if (a.nt) Stream<float>::template store<true>(y, v[i]);
-                else Stream<float>::template store<false>(y, v[i]);
+                Stream<float>::template store<false>(y, v[i]);
             }
         }
         return;
@@ -343,9 +343,7 @@ __global__ __launch_bounds__(1024) void k_heads(HeadsArgs a) {
         uint32_t e;
         if (p.kind == TO_FP8) {
             e = encode_group<false>(v[i], d);
-            v2w* to = (v2w*)((uint8_t*)p.y + (tok * a.lph + lane) * 8);
-            if (a.nt) put<true>(to, d);
-            else put<false>(to, d);
+            *(v2w*)((uint8_t*)p.y + (tok * a.lph + lane) * 8) = d;
         } else {
             e = encode_group<true>(v[i], d);
             *(uint32_t*)((uint8_t*)p.y + (tok * a.lph + lane) * 4) = d[0];
@@ -362,41 +360,53 @@ struct ReadArgs {
     long long ldy[2];
     Pages pages;
     long long N, first;
-    int lph;                // lanes of 16 channels to a head
-    int nch, tpr, segs;     // chunks of 16 channels to a row; threads and workgroups to one
+    int lph;                // lanes (chunks of 8 channels) to a head
+    int nch, tpr, segs;     // chunks to a row; threads and workgroups to one
     int part0;              // 1: only values are read
 };
 
-// A thread decodes 16 channels (half an MX group) of a row: with one chunk to a
-// thread there are twice the waves that two leave (32760 x 12 heads 70 -> 56 us, 5.5 TB/s).
-template <class T, int BITS>
+// A thread decodes U chunks of 8 channels, tpr apart, of a row's keys and values
+// (P: 2, or 1 of one of them), so one look at the page table serves 2 U loads, and
+// a wave writes whole 128-byte lines of bf16: 32760 x 12 heads from HBM 57.6 us
+// (5.3 TB/s).  With 16 channels to a thread, whose two stores leave every line
+// half written, 72; with U 1, 63.5.
+template <class T, int BITS, int P, int U>
 __global__ __launch_bounds__(256) void k_read(ReadArgs a) {
-    const int w = (int)blockIdx.y / a.segs + a.part0, tpr = a.tpr, shift = __builtin_ctz(tpr);
+    const int tpr = a.tpr, shift = __builtin_ctz(tpr), t = threadIdx.x & (tpr - 1);
     const long long row = a.first + (long long)blockIdx.x * (256 >> shift) + (threadIdx.x >> shift);
-    const int c = ((int)blockIdx.y % a.segs) * tpr + (threadIdx.x & (tpr - 1));
     const Place at = place_of(a.pages, starts_of(a.pages), row - ((threadIdx.x & 63) >> shift), tpr);
-    if (row >= a.N || at.t == NOWHERE || c >= a.nch) return;
-    constexpr int W = BITS == 8 ? 4 : 2;            // words of codes
-    uint32_t code[W] = {}, e = 0;
+    if (row >= a.N || at.t == NOWHERE) return;
+    constexpr int W = BITS == 8 ? 2 : 1;            // words of codes
+    const int lane = t & (a.lph - 1), c0 = (int)blockIdx.y * tpr * U + t;
+    uint32_t code[U][P][2] = {}, e[U][P] = {};
     if (at.page >= 0) {
-        const long long tok = token_row(a.pages, at, c / a.lph);
-        const int lane = c & (a.lph - 1);
-        const uint32_t* p = (const uint32_t*)a.codes[w] + (tok * a.lph + lane) * W;
-        if constexpr (BITS == 8) {
-            const v4w v = *(const v4w*)p;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) code[j] = v[j];
-        } else {
-            const v2w v = *(const v2w*)p;
-            code[0] = v[0], code[1] = v[1];
+        for (int u = 0; u < U; ++u) {
+            const long long tok = token_row(a.pages, at, min(c0 + u * tpr, a.nch - 1) / a.lph);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const uint32_t* p = (const uint32_t*)a.codes[a.part0 + i] + (tok * a.lph + lane) * W;
+                if constexpr (BITS == 8) {
+                    const v2w v = *((const v2w*)p);
+                    code[u][i][0] = v[0], code[u][i][1] = v[1];
+                } else {
+                    code[u][i][0] = *p;
+                }
+                e[u][i] = a.scales[a.part0 + i][tok * (a.lph >> 2) + (lane >> 2)];
+            }
         }
-        e = a.scales[w][tok * (a.lph >> 1) + (lane >> 1)];
     }
-    float v[16];
-    decode16<BITS>(code, e, v);
-    T* y = (T*)a.y[w] + row * a.ldy[w] + 16 * c;
-    Stream<T>::template store<true>(y, v);
-    Stream<T>::template store<true>(y + 8, v + 8);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * tpr;
+        if (c >= a.nch) continue;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            float v[8];
+            decode8_f32<BITS>(code[u][i], e[u][i], v);
+            Stream<T>::template store<true>((T*)a.y[a.part0 + i] + row * a.ldy[a.part0 + i] + 8 * c, v);
+        }
+    }
 }
 
 struct TableArgs {
@@ -446,7 +456,6 @@ hipError_t launch_heads(HeadsArgs a, int parts, hipStream_t st) {
     } else {
         share_row(nch, a.lph, &a.tpr, &ch);
     }
-    a.nt = !few;
     int segs = 0;
     for (int i = 0; i < 3; ++i) {
         Part& p = a.part[i];
@@ -469,19 +478,23 @@ hipError_t launch_heads(HeadsArgs a, int parts, hipStream_t st) {
     return e;
 }
 
-template <class T, int BITS>
-hipError_t launch_read(ReadArgs a, int parts, hipStream_t st) {
-    // as many threads as leave the fewest idle, of equal ones the most
-    int best = 1 << 30;
-    for (int t = a.lph; t <= 256; t *= 2) {
-        const int n = (a.nch + t - 1) / t;
-        if (n * t <= best && (n == 1 || t >= 64)) best = n * t, a.tpr = t, a.segs = n;
-    }
+template <class T, int BITS, int P>
+hipError_t launch_read(ReadArgs a, hipStream_t st) {
+    // chunks to a thread and threads to a row that leave the fewest idle, of equal
+    // ones the most (540 rows of 8 x 64 channels take as long with one chunk to a thread)
+    int best = 1 << 30, per = 1;
+    for (int u = 1; u <= 4; ++u)
+        for (int t = u == 1 ? a.lph : 64; t <= 256; t *= 2) {
+            const int n = (a.nch + t * u - 1) / (t * u);
+            if (n * t * u <= best && (n == 1 || t >= 64)) best = n * t * u, a.tpr = t, a.segs = n, per = u;
+        }
     const int rows = 256 / a.tpr;
     const long long most = (1ll << 31) / 256;
     hipError_t e = hipSuccess;
+    const auto kernel = per == 1 ? k_read<T, BITS, P, 1> : per == 2 ? k_read<T, BITS, P, 2> :
+                        per == 3 ? k_read<T, BITS, P, 3> : k_read<T, BITS, P, 4>;
     for (; a.first < a.N && e == hipSuccess; a.first += most * rows)
-        e = launch(k_read<T, BITS>, dim3((unsigned)std::min(most, (a.N - a.first + rows - 1) / rows), parts * a.segs), 256u, st, a);
+        e = launch(kernel, dim3((unsigned)std::min(most, (a.N - a.first + rows - 1) / rows), a.segs), 256u, st, a);
     return e;
 }
 
@@ -755,13 +768,14 @@ dq_status dq_kv_read(const dq_kv* kv, const dq_seqs* seqs, int64_t N, void* k_de
     a.ldy[0] = ldk, a.ldy[1] = ldv;
     a.pages = pages_of(kv, seqs);
     a.N = N;
-    a.lph = kv->head_dim / 16;
-    a.nch = (int)(C / 16);
+    a.lph = kv->head_dim / 8;
+    a.nch = (int)(C / 8);
     a.part0 = k_dev ? 0 : 1;
     const int parts = k_dev && v_dev ? 2 : 1;
     const auto go = [&](auto bits) {
         constexpr int B = decltype(bits)::value;
-        return dt == DQ_BF16 ? launch_read<uint16_t, B>(a, parts, (hipStream_t)stream) : launch_read<float, B>(a, parts, (hipStream_t)stream);
+        if (parts == 2) return dt == DQ_BF16 ? launch_read<uint16_t, B, 2>(a, (hipStream_t)stream) : launch_read<float, B, 2>(a, (hipStream_t)stream);
+        return dt == DQ_BF16 ? launch_read<uint16_t, B, 1>(a, (hipStream_t)stream) : launch_read<float, B, 1>(a, (hipStream_t)stream);
     };
     const hipError_t e = kv->bits == 8 ? go(std::integral_constant<int, 8>{}) : go(std::integral_constant<int, 4>{});
     return e == hipSuccess ? DQ_OK : hip_fail(e, "cache read launch");
