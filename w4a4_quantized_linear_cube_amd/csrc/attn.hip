@@ -47,9 +47,12 @@ constexpr size_t SUM_FLOATS = size_t(MAX_SLOTS) * MAX_RB * 16 * 128, STAT_FLOATS
 struct TileInfo {
     int used, rows, f0, r0, slot, pad[3];
 };
-// In blocks of 32 tokens: what a tile costs beside them (its start and end take
-// a workgroup as long), and the least that a workgroup takes.
-constexpr int TILE_COST = 4, LEAST_SHARE = 8;
+// In blocks of 32 tokens: what a tile costs beside them where a workgroup takes
+// parts of several (its start and end take as long; 3 and 8: slower), the least
+// that a workgroup takes (8: 1 x 8192 12.6 us, with 4 14.4, with 12 13.5), and the
+// most that one takes without a part in the join (24: 1 x 512 9.5 us against 11.2
+// in two parts, 16 x 768 12.2 against 14; 32 blocks 13.7 against 11.5).
+constexpr int TILE_COST = 4, LEAST_SHARE = 8, MOST_WHOLE = 24;
 constexpr float LOG2E = 1.44269504088896340736f;
 
 struct AttnArgs {
@@ -221,12 +224,17 @@ struct Work {
     bool head;                // its first part
 };
 // Up to 64 sequences: a lane holds one.  Their tiles stand in a row, each as long
-// as the blocks of tokens that it sees at most, and TILE_COST, and a workgroup
-// takes an equal stretch of the row: a part of a long tile or several short ones,
-// whatever the lengths (64 sequences of 132 to 8192 tokens 111 us; three parts to each tile 144).
+// as the blocks of tokens that it sees at most, and a workgroup takes an equal
+// stretch of the row, a share.  Where the card holds a workgroup for each part, a
+// tile's length is rounded up to whole shares, so that no workgroup meets two
+// tiles (16 sequences of 1024 tokens 14.9 us against 19.1, 8 11.9 against 15.6).
+// Otherwise TILE_COST is added to it, and a workgroup takes a part of a long tile or
+// several short ones, whatever the lengths (64 sequences of 132 to 8192 tokens
+// 111 us; three parts to each tile 144).
 struct Batch64 {
     int f0, f1, length, tiles;
-    int cost, upto, tiles_upto, pad;   // of one tile; of this sequence's and earlier tiles together
+    int cost, upto, tiles_upto;     // of one tile; of this sequence's and earlier tiles together
+    int parts;                      // of a tile, where they are whole shares
 };
 template <int TR>
 __device__ __forceinline__ Batch64 batch_of(const AttnArgs& a) {
@@ -239,10 +247,10 @@ __device__ __forceinline__ Batch64 batch_of(const AttnArgs& a) {
     const long long L = min((long long)x.length, reach(p));
     long long tokens = L;                                  // that a tile's rows see, or a few more
     if (a.block && a.window) tokens = min(L, min(L, a.window + a.block + TR) + min((long long)max(keep, 0), L) + 64);
-    x.cost = (int)((tokens + 31) / 32) + 1 + TILE_COST;
+    x.cost = max((int)((tokens + 31) / 32) + (a.window ? 1 : 0), 1);   // (a tile that sees nothing is answered, too)
     x.tiles_upto = scan(x.tiles);
-    x.upto = a.shares ? scan(x.tiles * x.cost) : 0;
-    x.pad = 0;
+    x.upto = 0;
+    x.parts = 0;
     return x;
 }
 __device__ __forceinline__ Batch64 of_lane(const Batch64& x, int b) {
@@ -290,16 +298,39 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
     asm volatile("" ::"s"(a.q), "s"(a.scales[1]), "s"(a.prefix), "s"(a.tiles));
     Work work;
     int pos = 0, end = 0, share = 0;                       // of the row of tiles: what is left to this workgroup
+    int lead = TILE_COST;                                  // of a tile's length, before its first block
     if (a.shares) {
-        const Batch64 x = batch_of<TR>(a);
-        batch[tid & 63] = x;                                   // (every wave the same)
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        const int total = __builtin_amdgcn_readlane(x.upto, 63), tiles = __builtin_amdgcn_readlane(x.tiles_upto, 63);
+        Batch64 x = batch_of<TR>(a);
+        const int tiles = __builtin_amdgcn_readlane(x.tiles_upto, 63);
         // (more tiles than there can be: first_dev is not ascending, and nothing is done)
         const bool fit = tiles <= a.most;
         if (u >= (fit ? tiles : 0) && u < a.most && tid == 0) a.tiles[(size_t)head * a.most + u].used = 0;   // (no tile of that number)
         if (!fit) return;
-        share = one(max((int)(((uint32_t)total + a.shares - 1) / (uint32_t)a.shares), LEAST_SHARE));
+        const auto last = [](int v) { return __builtin_amdgcn_readlane(v, 63); };
+        // whole shares: the least, or a few sizes from an equal division on
+        share = LEAST_SHARE;
+        int parts = (x.cost + LEAST_SHARE - 1) / LEAST_SHARE;
+        x.upto = scan(x.tiles * parts);
+        if (last(x.upto) > a.shares) {
+            const int sum = last(scan(x.tiles * x.cost));
+            share = one((int)(((uint32_t)sum + a.shares - 1) / (uint32_t)a.shares));
+#pragma unroll 1
+            for (int i = 0;; ++i, share += 4) {
+                parts = (int)(((uint32_t)x.cost + share - 1) / (uint32_t)share);
+                x.upto = scan(x.tiles * parts);
+                if (i == 4 || last(x.upto) <= a.shares) break;
+            }
+        }
+        if (last(x.upto) <= a.shares) {
+            x.cost = parts * share, x.upto *= share, lead = 0;
+        } else {
+            x.cost += TILE_COST, x.upto = scan(x.tiles * x.cost);
+            share = one((int)(((uint32_t)last(x.upto) + a.shares - 1) / (uint32_t)a.shares));
+        }
+        const int total = last(x.upto);
+        x.parts = parts;
+        batch[tid & 63] = x;                                   // (every wave the same)
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         pos = (int)min((long long)u * share, (long long)total), end = min(total, pos + share);
     } else {
         work = whole_tile<TR>(a, u);
@@ -312,14 +343,18 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
             if (pos >= end) return;
             const int b = (int)__popcll(__ballot(batch[lane].upto <= pos));
             const Batch64 x = batch[b];
-            const int tiles = one(x.tiles), cost = one(x.cost), begin = one(x.upto) - tiles * cost, tile = (pos - begin) / cost;
+            const int tiles = one(x.tiles), cost = one(x.cost), begin = one(x.upto) - tiles * cost, tile = tiles > 1 ? (pos - begin) / cost : 0;
             const int first = begin + tile * cost, from = pos - first, to = min(cost, from + end - pos), number = one(x.tiles_upto) - tiles + tile;
             pos += to - from;
-            work = {b, one(x.f0), one(x.f1), one(x.length), tile, max(from - TILE_COST, 0), max(to - TILE_COST, 0), 0, u + number, number, false};
+            work = {b, one(x.f0), one(x.f1), one(x.length), tile, max(from - lead, 0), max(to - lead, 0), 0, u + number, number, false};
             if (work.c0 >= work.c1) continue;                  // (the part that stands for the tile's cost)
-            const int head_of = (first + TILE_COST) / share;   // the workgroup of its first block
-            work.parts = (first + cost - 1) / share - head_of + 1;
-            work.head = u == head_of;
+            if (!lead) {
+                work.parts = one(x.parts), work.head = from == 0;
+            } else {
+                const int head_of = (first + lead) / share;    // the workgroup of its first block
+                work.parts = (first + cost - 1) / share - head_of + 1;
+                work.head = u == head_of;
+            }
         }
         const int b = one(work.b), f0 = one(work.f0), f1 = one(work.f1), length = one(work.length);
         const int L = (int)min((long long)length, reach(a.pages));
@@ -746,7 +781,7 @@ hipError_t launch_attn(AttnArgs a, int kv_heads, hipStream_t st) {
     }
     a.most = (int)tiles;
     const bool fits = (full + tiles) * kv_heads <= MAX_SLOTS && tiles * (blocks + 16) < 1ll << 30;
-    a.shares = a.pages.seqs <= 64 && blocks > LEAST_SHARE && tiles < full && fits ? (int)full : 0;
+    a.shares = a.pages.seqs <= 64 && blocks > MOST_WHOLE && tiles < full && fits ? (int)full : 0;
     const hipError_t e = launch(k_attn<T, BITS, D, RB>, dim3((unsigned)(a.shares ? a.shares : tiles), kv_heads), 256u, st, a);
     if (e != hipSuccess || !a.shares) return e;
     // (a wave to a row while that makes no more workgroups than the card holds at once: 1 x 4096 14.0 -> 12.3 us; else
