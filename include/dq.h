@@ -520,8 +520,9 @@ void dq_attn_destroy(dq_attn* a);
 /* Which tokens a row sees, and its scores.  With t the row's place, L its
  * sequence's length and block > 0, e = (floor(t / block) + 1) block: tokens
  * [max(0, e - window), min(e, L)) (window 0: from 0 on) and [0, min(prefix[b], L));
- * block 0: all L (window must then be 0, prefix has no effect).  block 1 is the causal mask; with
- * block the tokens of a frame, a row sees its own frame and those before it. */
+ * block 0: all L (window must then be 0, prefix has no effect).  block 1 is the
+ * causal mask; with block the tokens of a frame, a row sees its own frame and
+ * those before it. */
 typedef struct {
     double scale;                  /* [2^-32, 2^32]; head_dim ** -0.5 as a rule */
     double cap;                    /* scores cap tanh(s / cap); 0: as they are; else [2^-32, 2^32] */
@@ -536,8 +537,9 @@ typedef struct {
  *         apart, 16-byte aligned; y must not share memory with anything read
  * head_dim 64 or 128; q_heads a multiple of the cache's heads, q_heads *
  * head_dim <= 32768; 0 <= N <= 2^24, N * q_heads / heads <= 2^27.  The rows' own
- * tokens are read from the cache, so write them first.  A row that sees no token is zero; a token in a page
- * that is none of the cache's is not seen.  What masked tokens hold (NaN included) has no effect.
+ * tokens are read from the cache, so write them first.  A row that sees no token
+ * is zero; a token in a page that is none of the cache's is not seen.  What masked
+ * tokens hold (NaN included) has no effect.
  * bf16: weights are rounded to bf16 for their product with v and summed as
  * rounded; fp32: q is taken at its full precision, weights to 16 bits.
  * Tuned for few rows: those of a sequence that share a key head are taken up to

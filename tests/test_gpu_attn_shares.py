@@ -57,6 +57,20 @@ def test_masks_of_long_sequences(dqm, how, dtype):
     _check(dqm, Batch([40, 3, 1], [2000, 1100, 64], 64, DEV, seed=11), 1, 2, 64, dtype, seed=13, **how)
 
 
+# parts of whole shares of the least size and of larger ones, and parts that cross from tile to tile (the more of them
+# the more sequences, heads and tokens); 769 tokens are one block past what a workgroup takes without a join
+@pytest.mark.parametrize("n,longest", [(1, 769), (5, 1100), (33, 800), (64, 1500), (64, 3000), (66, 900)])
+@pytest.mark.parametrize("kv_heads,group,dim,dtype", [(1, 3, 128, "bf16"), (8, 2, 64, "bf16"), (8, 1, 64, "f32")])
+def test_parts_of_tiles(dqm, n, longest, kv_heads, group, dim, dtype):
+    _say(f"parts {n} sequences of up to {longest}, {kv_heads} x {group} x {dim} {dtype}")
+    g = np.random.default_rng(n + longest)
+    length = g.integers(longest // 4, longest + 1, n)
+    length[0] = longest
+    rows = g.integers(0, 2, n)
+    rows[0] = 2
+    _check(dqm, Batch(rows.tolist(), length.tolist(), 64, DEV, seed=n, tail=1), kv_heads, group, dim, dtype, seed=n)
+
+
 def test_a_long_sequence_beside_short_ones(dqm):
     length = [5000] + [1] * 20 + [33] * 20
     _check(dqm, Batch([1] * 41, length, 64, DEV, seed=15), 1, 4, 64, "bf16", seed=17)
