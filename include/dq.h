@@ -540,8 +540,8 @@ typedef struct {
  * tokens are read from the cache, so write them first.  A row that sees no token
  * is zero; a token in a page that is none of the cache's is not seen.  What masked
  * tokens hold (NaN included) has no effect.
- * bf16: weights are rounded to bf16 for their product with v and summed as
- * rounded; fp32: q is taken at its full precision, weights to 16 bits.
+ * q is taken at its full precision; for their product with v weights keep 16 bits
+ * (bf16) or 24 (fp32), in the sum that divides them all.
  * Tuned for few rows: those of a sequence that share a key head are taken up to
  * 32 (rows times heads) at a time, each such group reading the cache again.
  * Repeated calls agree bit for bit. */
