@@ -170,7 +170,7 @@ PyObject* rmsnorm8(PyObject*, PyObject* const* v, Py_ssize_t n) {
     });
 }
 
-// Attribute `name` of a handle or description of dq.py as an address (0 for None, with *ok kept).
+// Attribute `name` of a handle or description of dq.py (whose class dq.py has checked) as an address (0 for None, with *ok kept).
 void* address_of(PyObject* o, const char* name, bool* ok) {
     if (o == Py_None) return nullptr;
     PyObject* v = PyObject_GetAttrString(o, name);
@@ -216,7 +216,7 @@ bool ints_of(PyObject* o, int64_t n, int64_t c, int device, const int32_t** p) {
     return true;
 }
 
-// The norm and rotation of a call: (norm, eps, rope, pos) with the gains' dtype.
+// The norm and rotation of a call: (norm, eps, rope, pos) with the gains' dtype.  `rope` is followed: dq.py has seen that it is a Rope or None.
 bool ops_of(PyObject* norm, PyObject* eps, PyObject* rope, PyObject* pos, int64_t n, int device, dq_head_ops* ops) {
     if (!PyLong_Check(norm) || !PyFloat_Check(eps)) return false;
     const long k = PyLong_AsLong(norm);

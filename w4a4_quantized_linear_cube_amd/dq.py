@@ -860,7 +860,7 @@ def dq_norm_rope(x, heads: int, y, norm: Optional[str] = None, gain=None, eps: f
     be x itself."""
     f = "dq_norm_rope"
     call = _CALL or _native()
-    if call is not None:
+    if call is not None and (rope is None or isinstance(rope, Rope)):
         status = call.norm_rope(x, heads, y, NORMS.get(norm, -1), gain, eps, rope, pos, _raw(stream))
         if status is not None:
             return _check(status, f) if status else None
@@ -892,7 +892,7 @@ def dq_kv_write(kv: KV, seqs: Seqs, k, v, q=None, y=None, norm: Optional[str] = 
     receives them in bf16 or fp32."""
     f = "dq_kv_write"
     call = _CALL or _native()
-    if call is not None and isinstance(kv, KV) and isinstance(seqs, Seqs):
+    if call is not None and isinstance(kv, KV) and isinstance(seqs, Seqs) and (rope is None or isinstance(rope, Rope)):
         status = call.kv_write(kv, seqs, k, v, q, y, NORMS.get(norm, -1), gain, gain_q, eps, rope, pos, _raw(stream))
         if status is not None:
             return _check(status, f) if status else None
