@@ -539,7 +539,11 @@ typedef struct {
  * head_dim <= 32768; 0 <= N <= 2^24, N * q_heads / heads <= 2^27.  The rows' own
  * tokens are read from the cache, so write them first.  A row that sees no token
  * is zero; a token in a page that is none of the cache's is not seen.  What masked
- * tokens hold (NaN included) has no effect.
+ * tokens hold (NaN included) has no effect.  A
+ * value past bf16's range is infinite, and where a row sees one its channel is
+ * infinite by that sign, whatever the weight; with both signs, or NaN, it is NaN.
+ * The values are summed in fp32 with weights of up to 1 and divided at the end:
+ * values of 2^128 / L and more may end infinite among L tokens.
  * q is taken at its full precision; for their product with v weights keep 16 bits
  * (bf16) or 24 (fp32), in the sum that divides them all.
  * Tuned for few rows: those of a sequence that share a key head are taken up to

@@ -106,6 +106,9 @@ __device__ __forceinline__ float sum_rows(float v) {
 typedef const __attribute__((address_space(4))) int* Scalars;   // (nothing that the kernel writes)
 
 __device__ __forceinline__ float power(float x) { return __builtin_amdgcn_exp2f(x); }
+// What a sum is worth by a larger maximum.  Never 0, which would turn a sum that is infinite to NaN: below fp32's range its
+// smallest number (a selection of infinite sums instead, here and in both joins, costs 1 row over 4097 tokens 6 %, 4 x 1024 rows 2 %).
+__device__ __forceinline__ float worth(float from, float to) { return fmaxf(power(from - to), 0x1p-149f); }
 
 // tanh: (1 - t) / (1 + t) with t = e^-2|x|, and its series where that cancels.
 __device__ __forceinline__ float tanh_of(float x) {
@@ -163,29 +166,41 @@ struct Tokens {
     uint32_t k[2][KW], v[VP][VW];
     uint32_t ks[2], vs[VP];
 
-    // Whether one of the lane's values may not be finite: a NaN code, or a scale
-    // that is NaN or so large that a value may pass bf16's range.
-    __device__ __forceinline__ bool not_finite() const {
-        uint32_t nan = 0, large = 0;
+    // Whether one of the lane's values may be infinite, or has a NaN scale: a scale so large that a value may pass bf16's range.
+    __device__ __forceinline__ bool large() const {
+        uint32_t large = 0;
 #pragma unroll
-        for (int i = 0; i < VP; ++i) {
-            large |= ((vs[i] & 0x7f7f7f7fu) + 0x0a0a0a0au) & vs[i];   // (a code of 246 or more: carries into the sign's place, which it has)
-            if constexpr (BITS == 8) {
+        for (int i = 0; i < VP; ++i) large |= ((vs[i] & 0x7f7f7f7fu) + 0x0a0a0a0au) & vs[i];   // (a code of 246 or more: carries into the sign's place, which it has)
+        return (large & 0x80808080u) != 0;
+    }
+    // Whether one has a NaN code.
+    __device__ __forceinline__ bool nan_code() const {
+        uint32_t nan = 0;
+        if constexpr (BITS == 8) {
+#pragma unroll
+            for (int i = 0; i < VP; ++i)
 #pragma unroll
                 for (int j = 0; j < VW; ++j) nan |= (v[i][j] & 0x7f7f7f7fu) + 0x01010101u;   // (0x7f: carries into the sign's place)
-            }
         }
-        return ((nan | large) & 0x80808080u) != 0;
+        return (nan & 0x80808080u) != 0;
     }
 };
-// Of 8 bf16 values those that are not finite: as ones (else zeros), or put to zero.
-template <bool ONES>
-__device__ __forceinline__ v8bf not_finite_of(v8bf v) {
+// Of 8 bf16 values those that are not finite put to zero ...
+__device__ __forceinline__ v8bf finite(v8bf v) {
+    v4w w = __builtin_bit_cast(v4w, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] &= ~(((((w[i] & 0x7f807f80u) + 0x00800080u) >> 15) & 0x00010001u) * 0xffffu);   // (a full exponent carries into the sign's place)
+    return __builtin_bit_cast(v8bf, w);
+}
+// ... or put to what counts them, and zero for the rest: 1 for +infinity, 64 for -infinity, 65 for NaN (of 32 tokens: sums are exact, and
+// each of the first two is below 64 times).
+__device__ __forceinline__ v8bf counted(v8bf v) {
     v4w w = __builtin_bit_cast(v4w, v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t c = (((w[i] & 0x7f807f80u) + 0x00800080u) >> 15) & 0x00010001u;   // (a full exponent carries into the sign's place)
-        w[i] = ONES ? c * 0x3f80u : w[i] & ~(c * 0xffffu);
+        const uint32_t c = (((w[i] & 0x7f807f80u) + 0x00800080u) >> 15) & 0x00010001u;
+        const uint32_t nan = (((w[i] & 0x7fff7fffu) + 0x007f007fu) >> 15) & 0x00010001u, sign = w[i] >> 15;
+        w[i] = nan * 0x4282u | (c & ~nan & sign) * 0x4280u | (c & ~nan & ~sign) * 0x3f80u;
     }
     return __builtin_bit_cast(v8bf, w);
 }
@@ -445,7 +460,6 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
 
         v4f acc[RB][CB];
         float m[RB], l[RB];
-        uint32_t nan[RB] = {};                                 // the sums that are NaN by what the masked blocks hold
         uint32_t seen = 0;                                     // row blocks whose row (of this lane) saw a token
 #pragma unroll
         for (int i = 0; i < RB; ++i) {
@@ -550,11 +564,12 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
             load_keys(c + 4, pg);
             // ---- values into LDS
             const bool all = here.p[0] >= 0 && here.p[1] >= 0 && ((t >= lo1 && t + 32 <= hi0) || t + 32 <= pf);   // every row sees every token
-            // (a value that is not finite would reach rows that do not see it, times 0)
-            const bool odd = !all && __ballot(x.not_finite()) != 0;
+            // (in the product a value that is not finite would reach rows that do not see it, times 0, and an infinite
+            // one turn to NaN by a weight's part that is 0 or negative)
+            const bool odd = __ballot(x.large()) != 0 || (!all && __ballot(x.nan_code()) != 0);
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             if (!odd) place_values([](v8bf v) { return v; });
-            else place_values([](v8bf v) { return not_finite_of<false>(v); });
+            else place_values([](v8bf v) { return finite(v); });
             load_values(c + 4, pg);
             // ---- weights
             v8bf pw[RB][PP];
@@ -589,7 +604,7 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
                     if (vis[i]) seen |= 1u << i;
                     top = max_rows(top) * a.scale;             // (1 with a cap)
                     const float mn = fmaxf(m[i], top);
-                    grown[i] = mn == m[i] ? 1.0f : power(m[i] - mn);   // (also where both are infinite, whose sums are NaN by the weights)
+                    grown[i] = mn == m[i] ? 1.0f : worth(m[i], mn);   // (also where both are infinite, whose sums are NaN by the weights)
                     m[i] = mn;
                     l[i] *= grown[i];
                     const float at = m[i] == -INFINITY ? 0.0f : m[i];
@@ -629,10 +644,10 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
                     for (int p = PP - 1; p >= 0; --p) acc[i][cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pw[i][p], acc[i][cb], 0, 0, 0);
             }
             if (odd) {
-                // the rows that do see a value that is not finite: counted as ones times ones
+                // the rows that do see a value that is not finite: counted as ones times ones, whatever its weight
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 load_values(c, here);
-                place_values([](v8bf v) { return not_finite_of<true>(v); });
+                place_values([](v8bf v) { return counted(v); });
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
                 for (int i = 0; i < RB; ++i) {
@@ -643,7 +658,12 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
                     for (int cb = 0; cb < CB; ++cb) {
                         const v4f n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(read_v(cb), on, v4f{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) nan[i] |= __float_as_uint(n[e]) ? 1u << (4 * cb + e) : 0u;
+                        for (int e = 0; e < 4; ++e) {
+                            const int k = (int)n[e];
+                            acc[i][cb][e] += k & 63 ? INFINITY : 0.0f;
+                            acc[i][cb][e] -= k >> 6 ? INFINITY : 0.0f;
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
                     }
                 }
                 load_values(c + 4, pg);
@@ -679,11 +699,7 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
             __syncthreads();
             v4f* o = (v4f*)mine;
 #pragma unroll
-            for (int cb = 0; cb < CB; ++cb) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][cb][e] = nan[i] >> (4 * cb + e) & 1 ? __builtin_nanf("") : acc[i][cb][e];
-                o[r16 * (D / 4) + ((4 * cb + g) ^ r16)] = acc[i][cb];
-            }
+            for (int cb = 0; cb < CB; ++cb) o[r16 * (D / 4) + ((4 * cb + g) ^ r16)] = acc[i][cb];
             __syncthreads();
             float top = -INFINITY, sum = 0.0f, any = 0.0f;
 #pragma unroll
@@ -693,7 +709,7 @@ __global__ __launch_bounds__(256, waves_of(sizeof(T) == 4, D, RB)) void k_attn(A
             for (int p = 0; p < Q4; ++p) out[p] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
-                const float mp = stat[p][0][16 * i + row], f = mp == -INFINITY ? 1.0f : power(mp - top);
+                const float mp = stat[p][0][16 * i + row], f = mp == -INFINITY ? 1.0f : worth(mp, top);
                 sum += f * stat[p][1][16 * i + row];
                 any = fmaxf(any, stat[p][2][16 * i + row]);
                 const v4f* from = (const v4f*)lds[p] + row * (D / 4);
@@ -743,8 +759,8 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 #pragma unroll
             for (int s = 1; s < 64; s *= 2) m = fmaxf(m, __shfl_xor(m, s, 64));
             m = fmaxf(m, top);
-            const float old = m == -INFINITY ? 1.0f : power(top - m);
-            const float f = lane >= n ? 0.0f : st[0] == -INFINITY ? 1.0f : power(st[0] - m);
+            const float old = m == -INFINITY ? 1.0f : worth(top, m);
+            const float f = lane >= n ? 0.0f : st[0] == -INFINITY ? 1.0f : worth(st[0], m);
             top = m;
             float more = lane < n ? f * st[1] : 0.0f;
 #pragma unroll
