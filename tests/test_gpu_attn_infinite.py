@@ -100,3 +100,55 @@ def test_whatever_their_weight(dqm, dtype, slope, L):
     q = torch.zeros(2, dim)
     q[:, 0] = 8.0
     _check(dqm, batch, 8, 1, 1, dim, dtype, [(0, 1, 0, 4, 1), (0, L // 2, 0, 20, -1), (0, L - 2, 0, 50, 1)], 15, q=q.to(TYPES[dtype]), cache=cache)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nbits", [8, 4])
+@pytest.mark.parametrize("rows,dim", [(5, 64), (20, 128)])
+@pytest.mark.parametrize("cap", [0.0, 2.0])
+def test_infinite_keys(dqm, dtype, nbits, rows, dim, cap):
+    """A key's infinite channel: a score of the sign of its product with the query's.  Of -infinity the token has no
+    weight, of +infinity none but NaN is the answer; capped scores are the cap.  (The queries' bits past bf16's are of either sign.)"""
+    _say(f"infinite keys {rows} x {dim} {dtype} {nbits} bits cap {cap}")
+    batch = Batch([rows], [200], 16, DEV, seed=17)
+    cache = host_cache(batch, 1, dim, nbits, 19)
+    q = (1.5 * torch.randn(rows, 2 * dim, generator=torch.Generator().manual_seed(21))).to(TYPES[dtype])
+    q[0] = q[0].bfloat16().to(q.dtype)
+    for t, channel, sign in ((7, 3, 1), (100, 40, -1), (199 - rows // 2, 3, 1)):
+        page, place, group = batch.pages[0, t // 16], t % 16, channel // 32
+        codes = cache[0][page, 0, place]
+        codes[group * 32 * nbits // 8:(group + 1) * 32 * nbits // 8] = 0
+        if nbits == 8:
+            codes[channel] = 0x7E | (0x80 if sign < 0 else 0)
+        else:
+            codes[channel // 2] |= (0x7 | (0x8 if sign < 0 else 0)) << (4 * (channel % 2))
+        cache[1][page, 0, place, group] = 254
+    y = _run(dqm, batch, cache, q, cap=cap)
+    # the definition, with an infinite score in the place of its product
+    k, v = heads.decode(*cache[:2], nbits), heads.decode(*cache[2:], nbits)
+    at = np.arange(200)
+    k, v = k[batch.pages[0, at // 16], 0, at % 16], v[batch.pages[0, at // 16], 0, at % 16]
+    finite = np.where(np.abs(k) < 2.0 ** 120, k, 0.0)
+    seen = set()
+    for i in range(rows):
+        on = np.arange(200) <= 200 - rows + i
+        for h in range(2):
+            x = q[i, h * dim:(h + 1) * dim].double().numpy()
+            far = np.where(np.abs(k) < 2.0 ** 120, 0.0, np.copysign(np.inf, k * x)).sum(axis=1)   # (one in a key at most)
+            s = finite @ x * dim ** -0.5 + far
+            got = y[i, h * dim:(h + 1) * dim]
+            if cap:
+                s = cap * np.tanh(s / cap)
+            w = np.where(on, np.exp(s - s[on].max()), 0.0) if not (s[on] == np.inf).any() else None
+            seen.add(w is None)
+            if w is None:
+                assert np.isnan(got).all()
+                continue
+            w = w / w.sum()
+            # the bound of attend_all's, of the keys' finite part
+            size = w @ np.abs(v)
+            qk = (np.abs(finite) @ np.abs(x) * dim ** -0.5)[on].max()
+            e = 2 * ((dim + 8) * 2.0 ** -24 * qk + 6 * 2.0 ** -24 * min(qk, cap or qk) + 2.0 ** -21 + 4 * 2.0 ** -24 * cap) + 216 * 2.0 ** -24
+            e = (e + 2.0 ** -16) * size + (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) * np.abs(w @ v)
+            assert (np.abs(got - w @ v) <= e).all()
+    assert seen == ({False} if cap else {False, True})
