@@ -548,6 +548,13 @@ typedef struct {
  * (bf16) or 24 (fp32), in the sum that divides them all.
  * Tuned for few rows: those of a sequence that share a key head are taken up to
  * 32 (rows times heads) at a time, each such group reading the cache again.
+ * Tokens of one group are shared among workgroups only where the batch has fewer
+ * of them (N * q_heads / heads / 16, or / 32 for more than 16 a sequence, and seqs)
+ * than the card holds workgroups for each key head (256 to 1024 / heads, by type and
+ * width; 96 for bf16 and 8 heads of 128): in a larger batch a sequence much longer
+ * than the others is best given in a call of its own.  A page table of up to 768
+ * tokens (pages_ld * page_tokens) saves a launch; more than 64 sequences that do
+ * not fill the card take one or two launches for every 64.
  * Repeated calls agree bit for bit. */
 dq_status dq_attn_rows(const dq_kv* kv, const dq_seqs* seqs, int64_t N, const void* q_dev, int64_t ldq, dq_dtype dt,
                        int32_t q_heads, const dq_attn_ops* ops, dq_attn* a, void* y_dev, int64_t ldy, int32_t device,

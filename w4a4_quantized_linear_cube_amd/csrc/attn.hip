@@ -17,16 +17,17 @@
 //     lie (the order of tokens is again free); V goes through the wave's own part
 //     of LDS as bf16 and comes back transposed.
 // The four waves of a workgroup take blocks of tokens in turn, without a
-// barrier, and join at the end; a long cache is split over workgroups, whose sums
-// a second launch joins in order.
+// barrier, and join at the end; a long cache is split over workgroups while the
+// batch leaves the card room for that (launch_attn), and a second launch joins
+// their sums in order.
 //
 // What bounds it (8 key heads of 128 channels, 40 query heads): HBM where the cache
-// is long (64 sequences of 132 to 8192 tokens 117 us, 4.9 TB/s; 2 of 131072 in 4
-// bits 53 us, 5.4); where it is short, launch, a chain of loads (the batch, the
-// pages, the tokens) and the join's launch (1 x 4096 11.6 us, of them 4 in the join;
-// 1 x 128, without one, 6.0); from 16 rows that share a key head on the decoding
-// and the weights' vector instructions (4 x 1024 rows over 8192 tokens 280 us, 490
-// TFLOP/s).
+// is long (64 sequences of 132 to 8192 tokens 119 us, 4.8 TB/s; one of 131072 and
+// one of 81006 in 4 bits 55 us, 4.2, the kernel alone 51); where it is short,
+// launch, a chain of loads (the batch, the pages, the tokens) and the join's launch
+// (1 x 4097 12.4 us: 8.8 and 4.1 in the two kernels; 1 x 128, without a join, 6.1);
+// from 16 rows that share a key head on the decoding and the weights' vector
+// instructions (4 x 1024 rows over 8192 tokens 291 us, 472 TFLOP/s).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -56,10 +57,13 @@ struct TileInfo {
     int used, rows, f0, r0, slot, pad[3];
 };
 // In blocks of 32 tokens: what a tile costs beside them where a workgroup takes
-// parts of several (its start and end take as long; 3 and 8: slower), the least
-// that a workgroup takes (8: 1 x 8192 12.6 us, with 4 14.4, with 12 13.5), and the
-// most that one takes without a part in the join (24: 1 x 512 9.5 us against 11.2
-// in two parts, 16 x 768 12.2 against 14; 32 blocks 13.7 against 11.5).
+// parts of several (its start and end take as long; 64 ragged sequences 116 us with
+// 3, 4 and 8), the least that a workgroup takes (8: 1 x 8192 12.8 us, with 4 14.4,
+// with 12 13.9; 1 x 1024 11.6, 10.4 and 12.9), and the widest page table whose tiles
+// are taken whole, without a join.  The host does not know the lengths, so the
+// table's width stands for them: 1 x 512 in a table of 512 10.1 us against 11.5 in two
+// parts, 16 x 768 12.8 against 14.5 (1 x 768 12.6 against 11.6); of 1024 15.4 against
+// 11.6.  1 x 128 takes 6.1 us in a table of up to 768 tokens, 8.3 in a wider one.
 constexpr int TILE_COST = 4, LEAST_SHARE = 8, MOST_WHOLE = 24;
 constexpr float LOG2E = 1.44269504088896340736f;
 
@@ -255,10 +259,11 @@ struct Work {
 // as the blocks of tokens that it sees at most, and a workgroup takes an equal
 // stretch of the row, a share.  Where the card holds a workgroup for each part, a
 // tile's length is rounded up to whole shares, so that no workgroup meets two
-// tiles (16 sequences of 1024 tokens 14.9 us against 19.1, 8 11.9 against 15.6).
-// Otherwise TILE_COST is added to it, and a workgroup takes a part of a long tile or
-// several short ones, whatever the lengths (64 sequences of 132 to 8192 tokens
-// 111 us; three parts to each tile 144).
+// tiles (16 sequences of 1024 tokens 15.1 us against 16.7, 8 12.2 against 14.1, one of
+// 8192 12.8 against 17.7).  Otherwise TILE_COST is added to it, and a workgroup takes
+// a part of a long tile or several short ones, whatever the lengths (64 sequences of
+// 132 to 8192 tokens 116 us; in three parts to each tile, when this was chosen, 144
+// against 111).
 struct Batch64 {
     int f0, f1, length, tiles;
     int cost, upto, tiles_upto;     // of one tile; of this sequence's and earlier tiles together
@@ -806,9 +811,13 @@ template <class T, int BITS, int D, int RB>
 hipError_t launch_attn(AttnArgs a, int kv_heads, hipStream_t st) {
     const long long tiles = ((long long)a.N * a.G) / (16 * RB) + a.pages.seqs;   // at most, of one key head
     const long long blocks = (((long long)a.pages.ld << a.pages.shift) + 31) / 32;
-    // as many workgroups as the card holds at once, if the tiles do not make them by themselves
+    // as many workgroups as the card holds at once, if the tiles do not make them by themselves.  If they do, each is one
+    // workgroup's whatever its length, so a sequence much longer than the others sets the time (8 key heads: one of 131072
+    // tokens beside 63 of 500 80 us, beside 80 1280; 80 of 500 alone 21)
     const long long full = 256 * waves_of(sizeof(T) == 4, D, RB) / kv_heads;
-    if (a.pages.seqs > 64 && tiles < full) {               // (64 sequences at a time)
+    if (a.pages.seqs > 64 && tiles < full) {
+        // 64 sequences at a time, one launch or two for each (one key head: 500 sequences of 100 tokens 52 us; 800, which
+        // fill the card and are one launch, 15)
         hipError_t e = hipSuccess;
         for (int i = 0; i < a.pages.seqs && e == hipSuccess; i += 64) {
             AttnArgs some = a;
@@ -824,7 +833,7 @@ hipError_t launch_attn(AttnArgs a, int kv_heads, hipStream_t st) {
     a.shares = a.pages.seqs <= 64 && blocks > MOST_WHOLE && tiles < full && fits ? (int)full : 0;
     const hipError_t e = launch(k_attn<T, BITS, D, RB>, dim3((unsigned)(a.shares ? a.shares : tiles), kv_heads), 256u, st, a);
     if (e != hipSuccess || !a.shares) return e;
-    // (a wave to a row while that makes no more workgroups than the card holds at once: 1 x 4096 14.0 -> 12.3 us; else
+    // (a wave to a row while that makes no more workgroups than the card holds at once: 1 x 4096 12.9 -> 11.7 us; else
     // four rows to a wave: 64 sequences 118 -> 116)
     a.join = tiles * kv_heads * RB <= 512 ? 4 : 1;
     return launch(k_attn_join<T, D, RB>, dim3((unsigned)tiles * RB * a.join, kv_heads), 256u, st, a);
@@ -833,8 +842,8 @@ hipError_t launch_attn(AttnArgs a, int kv_heads, hipStream_t st) {
 template <class T, int BITS, int D>
 hipError_t launch_attn(const AttnArgs& a, int kv_heads, hipStream_t st) {
     const long long rows = ((long long)a.N * a.G + a.pages.seqs - 1) / a.pages.seqs;   // of a sequence, in the mean
-    // (4 sequences of 8192 tokens: 16 rows 23.5 us in one block of rows, 25.9 with room for two; 32 rows 27.1 in two
-    // at once against 32.7, 256 rows 91 against 170)
+    // (4 sequences of 8192 tokens: 16 rows 23.5 us in one block of rows, 24.7 with room for two; 32 rows 26.1 in two
+    // at once against 32.8, 256 rows 93 against 171)
     if (rows <= 16) return launch_attn<T, BITS, D, 1>(a, kv_heads, st);
     return launch_attn<T, BITS, D, 2>(a, kv_heads, st);
 }

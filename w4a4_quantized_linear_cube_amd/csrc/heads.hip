@@ -198,7 +198,8 @@ __device__ __forceinline__ void load_gains(const HeadsArgs& a, const Part& p, in
     else Stream<float>::load((const float*)p.g + at, g);
 }
 
-// What bounds it: HBM where there are many rows (32760 x 12 heads 45.5 us, 4.4 TB/s; 75600 x 40 fp32 heads 395, 5.9 TB/s);
+// What bounds it: HBM where there are many rows (32760 x 12 heads 45.5 us a call among others, 4.4 TB/s, the kernel
+// by itself 47 to 53; 75600 x 40 fp32 heads 394, 5.9 TB/s);
 // launch and a chain of three loads where there are few (1 x 40 heads 3.5 us).
 // A row's part is held in registers by tpr threads (of several blocks, where no
 // sum crosses them), CH chunks of 8 channels each, chunk i of thread t: i tpr + t.
@@ -451,7 +452,9 @@ hipError_t launch_heads(HeadsArgs a, int parts, hipStream_t st) {
     }
     // Few chunks: one to a thread, for the shortest chain (of 5120 channels 1 row 2.9
     // us against 3.9, 200 rows 3.2 against 4.5); more: as share_row has it (800
-    // rows, norm of the row 5.9 us against 7.9 with one to a thread).
+    // rows, norm of the row 5.9 us against 7.9 with one to a thread).  All parts go
+    // by the widest, so narrow keys leave most of their threads' chunks idle: 4096 rows
+    // of 40 query and 8 key heads 42 us (their bytes 23), of 8 and 8 16 (9).
     const bool few = a.N * nch <= (1 << 17);
     if (few) {
         a.tpr = std::min(pow2_at_least(nch, a.lph), row_norm ? 1024 : 256);
